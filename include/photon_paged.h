@@ -278,6 +278,120 @@ photon_status_t photon_paged_decode_fp8(const void* q, const void* k_cache, cons
                                         const photon_paged_shape_t* shape,
                                         photon_stream_t stream);
 
+/* ---- 4-bit KV cache.  A cached row (one token, one KV head, head_dim
+ * elements) is held as 4-bit codes with two numbers of the storage type:
+ *     lo   = its smallest element,
+ *     step = (largest - smallest) / 15, rounded once to the storage type,
+ *     n    = clamp(round_half_even((x - lo) / step), 0, 15)   (0 if step == 0),
+ * and element x stands for lo + n * step.  shape->dtype is PHOTON_F16 or
+ * PHOTON_BF16 (PHOTON_ERR_UNSUPPORTED for f32); q, out and new rows have that
+ * type.  A row that holds a NaN or an infinity is stored with step = lo = NaN,
+ * so that it reads back as NaN.  Each pool (K and V apart) is a byte array of
+ * one record per (block, KV head), [num_blocks][num_kv_heads][record], a
+ * record being 8 * head_dim + 64 bytes:
+ *     codes   8 * head_dim bytes, below
+ *     pairs   16 x (step, lo), row by row
+ * K codes: 16 rows of head_dim / 2 bytes, element 2i in the low nibble of
+ * byte i, element 2i + 1 in the high one.  V codes: 8 row pairs of head_dim
+ * bytes; in a pair, 4-byte words c = 0 .. head_dim / 4 - 1 with elements 4c ..
+ * 4c + 3 of the even row in the low half and of the odd row in the high half
+ * (lowest element in the lowest nibble). */
+
+/* Bytes of one pool (K or V) of shape->num_blocks blocks; 0 for an invalid
+ * shape or f32. */
+size_t photon_cache_int4_bytes(const photon_paged_shape_t* shape);
+
+/* Quantising batched cache write: row t of k and v ([num_tokens][Hkv][d]) is
+ * stored at slot_mapping[t] in the form above, code for code as its definition
+ * gives it in exact arithmetic.  k_stride, v_stride: elements from one token's
+ * rows to the next one's (0: packed, Hkv * d); at least Hkv * d and a multiple
+ * of 8, else PHOTON_ERR_INVALID_ARG / PHOTON_ERR_MISALIGNED, so a slice of a
+ * fused projection goes in as it is.  Slots as photon_cache_write (negative =
+ * padding, out of range: device error bit 2; no duplicates). */
+photon_status_t photon_cache_write_int4(const void* k, int64_t k_stride, const void* v,
+                                        int64_t v_stride, const int64_t* slot_mapping,
+                                        int32_t num_tokens, void* k_cache, void* v_cache,
+                                        const photon_paged_shape_t* shape,
+                                        photon_stream_t stream);
+
+/* photon_paged_gather over a 4-bit cache: k_dense, v_dense ([num_seqs][Hkv]
+ * [max_blocks_per_seq * block_size][d], the storage type) receive the values
+ * lo + n * step, rounded once, of each context's rows, and zeros after. */
+photon_status_t photon_paged_gather_int4(const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables,
+                                         const int32_t* context_lens, void* k_dense,
+                                         void* v_dense, const photon_paged_shape_t* shape,
+                                         photon_stream_t stream);
+
+/* Workspace bytes of photon_paged_decode_int4 (0 for an invalid shape or f32,
+ * or num_seqs == 0). */
+size_t photon_paged_decode_int4_workspace_size(const photon_paged_shape_t* shape);
+
+/* photon_paged_decode over a 4-bit cache: out = softmax(scale * q . K) V with
+ * the rows' values as defined above (the codes are never widened in memory),
+ * fp32 accumulation on the tensor cores, the softmax weights times step fed as
+ * an fp16 rounding plus its fp16 residual.  The batch's blocks are cut into
+ * equal runs, one per resident warp, so partition_size is ignored.  Layouts of
+ * q, out, tables and lengths, errors and workspace rules as
+ * photon_paged_decode. */
+photon_status_t photon_paged_decode_int4(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables,
+                                         const int32_t* context_lens, float scale, void* out,
+                                         void* workspace, size_t workspace_bytes,
+                                         const photon_paged_shape_t* shape,
+                                         photon_stream_t stream);
+
+/* ---- q and k between the projection and the attention */
+
+/* Which position turns which pair of a row.  A row's first rotary_dim =
+ * 2 * (section[0] + .. + section[num_axes - 1]) elements are turned, the rest
+ * keep their place; pair k (of rotary_dim / 2) is elements k and k +
+ * rotary_dim / 2.  One axis is the ordinary rotary embedding; images and video
+ * have one axis each for time, height and width.  interleaved == 0: the axes
+ * own runs of section[a] pairs in order.  interleaved == 1: axis a > 0 owns
+ * pairs a, a + num_axes, a + 2 num_axes, .. (section[a] of them) and axis 0
+ * the pairs that are left. */
+typedef struct {
+  int32_t num_axes;    /* 1 .. 4 */
+  int32_t section[4];  /* pairs of each axis, >= 0; entries past num_axes are ignored */
+  int32_t interleaved; /* 0 or 1 */
+} photon_rope_axes_t;
+
+/* Per-head RMS norm of q and k and their rotation by position, in one pass
+ * over both: for every token t and every head row x of q and of k,
+ *     y = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
+ * and then, for each pair k of axis a, with (cos, sin) =
+ * rope_cos_sin[positions[a][t]][k],
+ *     z[k]        = y[k] cos - y[k + r/2] sin,   r = rotary_dim
+ *     z[k + r/2]  = y[k + r/2] cos + y[k] sin,   z = y elsewhere,
+ * in fp32, rounded once to the storage type (f32, f16 or bf16).
+ *   q, q_out      [num_tokens] rows of num_q_heads x head_dim
+ *   k, k_out      [num_tokens] rows of num_kv_heads x head_dim
+ *   *_stride      elements from a token's row to the next one's (0: packed);
+ *                 a slice of a fused projection goes in as it is.  At least
+ *                 the row's elements, and a multiple of 16 bytes
+ *   *_weight      [head_dim] in the storage type, or NULL: no norm
+ *   positions     int32 [num_axes][num_tokens]
+ *   rope_cos_sin  from photon_rope_cos_sin(base, max_positions, rotary_dim)
+ * In place (q_out == q, k_out == k, same strides) is allowed; any other
+ * overlap is not.  A token whose position on axis 0 is negative is padding:
+ * its outputs are left as they were.  Any other position outside [0,
+ * max_positions) sets device error bit 16 and leaves that token's rows normed
+ * but unturned.  eps must be finite and >= 0.  rotary_dim must be a multiple
+ * of 16, at least 16 and at most head_dim, and with interleaved == 1 every
+ * axis' pairs must lie below rotary_dim / 2 (PHOTON_ERR_UNSUPPORTED /
+ * PHOTON_ERR_INVALID_ARG).  num_tokens == 0 is a no-op.  Uses shape:
+ * num_q_heads, num_kv_heads, head_dim, dtype (num_seqs and the pool's sizes
+ * are not used). */
+photon_status_t photon_qk_norm_rope(const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* q_weight,
+                                    const void* k_weight, float eps, const int32_t* positions,
+                                    const void* rope_cos_sin, int32_t max_positions,
+                                    const photon_rope_axes_t* axes, int32_t num_tokens,
+                                    void* q_out, int64_t q_out_stride, void* k_out,
+                                    int64_t k_out_stride, const photon_paged_shape_t* shape,
+                                    photon_stream_t stream);
+
 /* Test and tuning hook: which consumer the decode attention kernel runs
  * (photon_paged_decode, _step, _step_rope, _noalloc).  0 (default) = by the group size: the tensor-core consumer
  * (mma.sync over tensor-map copies of the blocks) for fp16/bf16 storage and

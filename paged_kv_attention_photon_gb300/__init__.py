@@ -31,6 +31,9 @@ __all__ = [
     "photon_paged_multi_query_workspace_size", "photon_debug_set_multi_query_kernel",
     "photon_debug_set_decode_consumer", "photon_cache_write_fp8",
     "photon_paged_decode_fp8_workspace_size", "photon_paged_decode_fp8",
+    "photon_cache_int4_bytes", "photon_cache_write_int4", "photon_paged_gather_int4",
+    "photon_paged_decode_int4_workspace_size", "photon_paged_decode_int4",
+    "RopeAxes", "photon_qk_norm_rope",
     "photon_debug_wait_probe", "photon_debug_read_probe", "Scheduler",
     "F32", "F16", "BF16", "STATUS",
 ]
@@ -62,6 +65,20 @@ class PagedShape(ctypes.Structure):
              num_blocks, max_blocks_per_seq, dtype, partition_size=0) -> "PagedShape":
         return cls(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
                    max_blocks_per_seq, dtype, partition_size)
+
+
+class RopeAxes(ctypes.Structure):
+    """Mirror of photon_rope_axes_t."""
+
+    _fields_ = [("num_axes", ctypes.c_int32), ("section", ctypes.c_int32 * 4),
+                ("interleaved", ctypes.c_int32)]
+
+    @classmethod
+    def make(cls, sections, interleaved=False) -> "RopeAxes":
+        """sections: pairs of each axis (rotary_dim / 2 in all), one entry per axis."""
+        sections = [int(x) for x in sections]
+        held = (ctypes.c_int32 * 4)(*sections[:4])
+        return cls(len(sections), held, int(interleaved))
 
 
 def library_path() -> str:
@@ -124,6 +141,20 @@ def _load() -> ctypes.CDLL:
     lib.photon_paged_decode_fp8.argtypes = [P, P, P, P, P, F32, F32, F32, P, P, SZ,
                                             ctypes.POINTER(PagedShape), P]
     lib.photon_paged_decode_fp8.restype = ctypes.c_int
+    I64 = ctypes.c_int64
+    lib.photon_cache_int4_bytes.argtypes = [SP]
+    lib.photon_cache_int4_bytes.restype = SZ
+    lib.photon_cache_write_int4.argtypes = [P, I64, P, I64, P, I32, P, P, SP, P]
+    lib.photon_cache_write_int4.restype = ctypes.c_int
+    lib.photon_paged_gather_int4.argtypes = [P, P, P, P, P, P, SP, P]
+    lib.photon_paged_gather_int4.restype = ctypes.c_int
+    lib.photon_paged_decode_int4_workspace_size.argtypes = [SP]
+    lib.photon_paged_decode_int4_workspace_size.restype = SZ
+    lib.photon_paged_decode_int4.argtypes = [P, P, P, P, P, F32, P, P, SZ, SP, P]
+    lib.photon_paged_decode_int4.restype = ctypes.c_int
+    lib.photon_qk_norm_rope.argtypes = [P, I64, P, I64, P, P, F32, P, P, I32,
+                                        ctypes.POINTER(RopeAxes), I32, P, I64, P, I64, SP, P]
+    lib.photon_qk_norm_rope.restype = ctypes.c_int
     lib.photon_paged_multi_query.restype = ctypes.c_int
     # host scheduler (include/photon_scheduler.h)
     lib.photon_scheduler_create.argtypes = [P, ctypes.POINTER(P)]
@@ -318,6 +349,59 @@ def photon_paged_decode_fp8(q, k_cache, v_cache, block_tables, context_lens, sca
                                            _ptr(out), _ptr(workspace), int(workspace_bytes),
                                            ctypes.byref(shape), _stream(stream)),
            "photon_paged_decode_fp8")
+
+
+def photon_cache_int4_bytes(shape: PagedShape) -> int:
+    """Bytes of one 4-bit pool (K or V) of shape.num_blocks blocks."""
+    return int(_load().photon_cache_int4_bytes(ctypes.byref(shape)))
+
+
+def photon_cache_write_int4(k, k_stride: int, v, v_stride: int, slot_mapping, num_tokens: int,
+                            k_cache, v_cache, shape: PagedShape, stream=None) -> None:
+    """Quantising cache write into 4-bit pools (uint8 tensors); the strides are
+    elements from one token's rows to the next one's, 0 = packed."""
+    _check(_load().photon_cache_write_int4(_ptr(k), int(k_stride), _ptr(v), int(v_stride),
+                                           _ptr(slot_mapping), int(num_tokens), _ptr(k_cache),
+                                           _ptr(v_cache), ctypes.byref(shape), _stream(stream)),
+           "photon_cache_write_int4")
+
+
+def photon_paged_gather_int4(k_cache, v_cache, block_tables, context_lens, k_dense, v_dense,
+                             shape: PagedShape, stream=None) -> None:
+    """The contexts' rows of 4-bit pools as values of the storage type."""
+    _check(_load().photon_paged_gather_int4(_ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                                            _ptr(context_lens), _ptr(k_dense), _ptr(v_dense),
+                                            ctypes.byref(shape), _stream(stream)),
+           "photon_paged_gather_int4")
+
+
+def photon_paged_decode_int4_workspace_size(shape: PagedShape) -> int:
+    return int(_load().photon_paged_decode_int4_workspace_size(ctypes.byref(shape)))
+
+
+def photon_paged_decode_int4(q, k_cache, v_cache, block_tables, context_lens, scale: float, out,
+                             workspace, workspace_bytes: int, shape: PagedShape,
+                             stream=None) -> None:
+    """Paged decode over 4-bit K/V pools (uint8 tensors)."""
+    _check(_load().photon_paged_decode_int4(_ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                            _ptr(block_tables), _ptr(context_lens),
+                                            float(scale), _ptr(out), _ptr(workspace),
+                                            int(workspace_bytes), ctypes.byref(shape),
+                                            _stream(stream)),
+           "photon_paged_decode_int4")
+
+
+def photon_qk_norm_rope(q, q_stride: int, k, k_stride: int, q_weight, k_weight, eps: float,
+                        positions, rope_cos_sin, max_positions: int, axes: RopeAxes,
+                        num_tokens: int, q_out, q_out_stride: int, k_out, k_out_stride: int,
+                        shape: PagedShape, stream=None) -> None:
+    """Per-head RMS norm of q and k (weight None: no norm) and their rotation by
+    position, on one axis or several; strides in elements, 0 = packed."""
+    _check(_load().photon_qk_norm_rope(
+        _ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(q_weight), _ptr(k_weight),
+        float(eps), _ptr(positions), _ptr(rope_cos_sin), int(max_positions),
+        ctypes.byref(axes), int(num_tokens), _ptr(q_out), int(q_out_stride), _ptr(k_out),
+        int(k_out_stride), ctypes.byref(shape), _stream(stream)), "photon_qk_norm_rope")
 
 
 def photon_paged_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, scale: float,

@@ -13,7 +13,9 @@
 #include <cstring>
 
 #include "../../include/photon_paged.h"
+#include "int4_common.cuh"
 #include "photon_common.cuh"
+#include "qk_norm_rope.cuh"
 
 namespace photon {
 // selftest.cu
@@ -587,6 +589,265 @@ photon_status_t photon_paged_multi_query(const void* q, const void* k_cache, con
   const cudaError_t e = tc ? photon::launch_multi_query_tc(a, s) : photon::launch_multi_query(a, s);
   return e == cudaSuccess ? PHOTON_OK : PHOTON_ERR_CUDA;
 }
+
+}  // extern "C"
+
+namespace {
+
+// Checks of a shape with a 4-bit cache.
+photon_status_t check_int4_shape(const photon_paged_shape_t* s) {
+  const photon_status_t st = check_shape(s);
+  if (st != PHOTON_OK) return st;
+  return s->dtype == PHOTON_F32 ? PHOTON_ERR_UNSUPPORTED : PHOTON_OK;
+}
+
+// Token stride of rows of `row` elements (`given` == 0: packed): at least the
+// row, and a multiple of 16 bytes.
+photon_status_t token_stride(int64_t given, int64_t row, size_t elem, int64_t* out) {
+  *out = given == 0 ? row : given;
+  if (given < 0 || *out < row) return PHOTON_ERR_INVALID_ARG;
+  return (*out * (int64_t)elem) % 16 == 0 ? PHOTON_OK : PHOTON_ERR_MISALIGNED;
+}
+
+// Workspace of photon_paged_decode_int4: [pairs][(m, l)][o], the last two per
+// partial slot and query head of a group; a run of the unit line has one
+// partial per (sequence, KV head) pair it touches, so slots number at most
+// warps + pairs.
+struct Int4Layout {
+  size_t off_ml, off_o, total;
+  int max_warps;
+};
+
+Int4Layout int4_layout(const photon_paged_shape_t* s) {
+  Int4Layout w{};
+  const size_t pairs = (size_t)s->num_seqs * s->num_kv_heads;
+  const size_t G = s->num_q_heads / s->num_kv_heads;
+  // warps that can have work at all, in whole CTAs of 4
+  const size_t units = pairs * (size_t)s->max_blocks_per_seq;
+  w.max_warps = (int)std::min<size_t>(photon::kInt4MaxWarps, round_up(std::max<size_t>(units, 1), 4));
+  const size_t rows = (pairs + w.max_warps) * G;
+  w.off_ml = round_up(pairs * sizeof(int2), 256);
+  w.off_o = w.off_ml + round_up(rows * sizeof(float2), 256);
+  w.total = pairs ? w.off_o + round_up(rows * s->head_dim * sizeof(float), 256) : 0;
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t photon_cache_int4_bytes(const photon_paged_shape_t* shape) {
+  if (check_int4_shape(shape) != PHOTON_OK) return 0;
+  return (size_t)shape->num_blocks * shape->num_kv_heads *
+         photon::int4_record_bytes(shape->head_dim);
+}
+
+photon_status_t photon_cache_write_int4(const void* k, int64_t k_stride, const void* v,
+                                        int64_t v_stride, const int64_t* slot_mapping,
+                                        int32_t num_tokens, void* k_cache, void* v_cache,
+                                        const photon_paged_shape_t* shape,
+                                        photon_stream_t stream) {
+  photon_status_t st = check_int4_shape(shape);
+  if (st != PHOTON_OK) return st;
+  if (num_tokens < 0) return PHOTON_ERR_INVALID_ARG;
+  photon::CacheWriteInt4Args a{};
+  const int64_t row = (int64_t)shape->num_kv_heads * shape->head_dim;
+  if ((st = token_stride(k_stride, row, 2, &a.k_stride)) != PHOTON_OK) return st;
+  if ((st = token_stride(v_stride, row, 2, &a.v_stride)) != PHOTON_OK) return st;
+  if (num_tokens == 0) return PHOTON_OK;
+  if (!k || !v || !slot_mapping || !k_cache || !v_cache) return PHOTON_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return PHOTON_ERR_MISALIGNED;
+  uint32_t* err = nullptr;
+  if ((st = error_word(&err)) != PHOTON_OK) return st;
+  a.k = k;
+  a.v = v;
+  a.slot_mapping = slot_mapping;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.err = err;
+  a.T = num_tokens;
+  a.Hkv = shape->num_kv_heads;
+  a.D = shape->head_dim;
+  a.NB = shape->num_blocks;
+  a.dtype = shape->dtype;
+  return photon::launch_cache_write_int4(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PHOTON_OK
+             : PHOTON_ERR_CUDA;
+}
+
+photon_status_t photon_paged_gather_int4(const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables,
+                                         const int32_t* context_lens, void* k_dense,
+                                         void* v_dense, const photon_paged_shape_t* shape,
+                                         photon_stream_t stream) {
+  photon_status_t st = check_int4_shape(shape);
+  if (st != PHOTON_OK) return st;
+  if (shape->num_seqs == 0) return PHOTON_OK;
+  if (!k_cache || !v_cache || !block_tables || !context_lens || !k_dense || !v_dense)
+    return PHOTON_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(block_tables) ||
+      !aligned16(context_lens) || !aligned16(k_dense) || !aligned16(v_dense))
+    return PHOTON_ERR_MISALIGNED;
+  uint32_t* err = nullptr;
+  if ((st = error_word(&err)) != PHOTON_OK) return st;
+  photon::GatherInt4Args a{};
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.k_dense = k_dense;
+  a.v_dense = v_dense;
+  a.err = err;
+  a.B = shape->num_seqs;
+  a.Hkv = shape->num_kv_heads;
+  a.D = shape->head_dim;
+  a.NB = shape->num_blocks;
+  a.MBS = shape->max_blocks_per_seq;
+  a.dtype = shape->dtype;
+  return photon::launch_gather_int4(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PHOTON_OK
+             : PHOTON_ERR_CUDA;
+}
+
+size_t photon_paged_decode_int4_workspace_size(const photon_paged_shape_t* shape) {
+  if (check_int4_shape(shape) != PHOTON_OK) return 0;
+  return int4_layout(shape).total;
+}
+
+photon_status_t photon_paged_decode_int4(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables,
+                                         const int32_t* context_lens, float scale, void* out,
+                                         void* workspace, size_t workspace_bytes,
+                                         const photon_paged_shape_t* shape,
+                                         photon_stream_t stream) {
+  photon_status_t st = check_int4_shape(shape);
+  if (st != PHOTON_OK) return st;
+  if (!std::isfinite(scale)) return PHOTON_ERR_INVALID_ARG;
+  if (shape->num_seqs == 0) return PHOTON_OK;
+  // (sequence, head) pairs are numbered in 32 bits
+  if ((int64_t)shape->num_seqs * shape->num_q_heads > INT_MAX / 2) return PHOTON_ERR_UNSUPPORTED;
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out)
+    return PHOTON_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(block_tables) ||
+      !aligned16(context_lens) || !aligned16(out))
+    return PHOTON_ERR_MISALIGNED;
+  const Int4Layout wl = int4_layout(shape);
+  if (!workspace || workspace_bytes < wl.total) return PHOTON_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return PHOTON_ERR_MISALIGNED;
+  uint32_t* err = nullptr;
+  if ((st = error_word(&err)) != PHOTON_OK) return st;
+  photon::DecodeInt4Args a{};
+  if ((st = num_sms(&a.num_sms)) != PHOTON_OK) return st;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.out = out;
+  char* ws = static_cast<char*>(workspace);
+  a.ws_pair = reinterpret_cast<int2*>(ws);
+  a.ws_ml = reinterpret_cast<float2*>(ws + wl.off_ml);
+  a.ws_o = reinterpret_cast<float*>(ws + wl.off_o);
+  a.err = err;
+  a.qscale = (float)((double)scale * 1.4426950408889634);
+  a.B = shape->num_seqs;
+  a.Hq = shape->num_q_heads;
+  a.Hkv = shape->num_kv_heads;
+  a.D = shape->head_dim;
+  a.NB = shape->num_blocks;
+  a.MBS = shape->max_blocks_per_seq;
+  a.dtype = shape->dtype;
+  a.max_warps = wl.max_warps;
+  a.ev_start = g_ev_start.load(std::memory_order_acquire);
+  a.ev_stop = g_ev_stop.load(std::memory_order_acquire);
+  if (!a.ev_start || !a.ev_stop) a.ev_start = a.ev_stop = nullptr;
+  return photon::launch_paged_decode_int4(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PHOTON_OK
+             : PHOTON_ERR_CUDA;
+}
+
+photon_status_t photon_qk_norm_rope(const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* q_weight,
+                                    const void* k_weight, float eps, const int32_t* positions,
+                                    const void* rope_cos_sin, int32_t max_positions,
+                                    const photon_rope_axes_t* axes, int32_t num_tokens,
+                                    void* q_out, int64_t q_out_stride, void* k_out,
+                                    int64_t k_out_stride, const photon_paged_shape_t* shape,
+                                    photon_stream_t stream) {
+  photon_status_t st = check_shape(shape);
+  if (st != PHOTON_OK) return st;
+  if (!axes || num_tokens < 0 || max_positions <= 0 || !std::isfinite(eps) || eps < 0.f)
+    return PHOTON_ERR_INVALID_ARG;
+  if (axes->num_axes < 1 || axes->num_axes > 4 || axes->interleaved < 0 || axes->interleaved > 1)
+    return PHOTON_ERR_INVALID_ARG;
+  int64_t half = 0;
+  for (int i = 0; i < axes->num_axes; ++i) {
+    if (axes->section[i] < 0) return PHOTON_ERR_INVALID_ARG;
+    half += axes->section[i];
+  }
+  if (half < 1 || 2 * half > shape->head_dim) return PHOTON_ERR_INVALID_ARG;
+  if (half % 8 != 0) return PHOTON_ERR_UNSUPPORTED;
+  photon::QkNormRopeArgs a{};
+  for (int k = 0, ax = 0, left = axes->section[0]; k < half; ++k) {
+    // the axis of pair k
+    int of = 0;
+    if (axes->interleaved) {
+      const int r = k % axes->num_axes;
+      of = k / axes->num_axes < axes->section[r] ? r : 0;
+    } else {
+      while (left == 0) left = axes->section[++ax];
+      --left;
+      of = ax;
+    }
+    a.axis[k / 16] |= (uint32_t)of << (2 * (k % 16));
+  }
+  if (axes->interleaved)
+    for (int i = 1; i < axes->num_axes; ++i)
+      if (axes->section[i] > 0 && i + (int64_t)axes->num_axes * (axes->section[i] - 1) >= half)
+        return PHOTON_ERR_INVALID_ARG;
+  const size_t eb = elem_bytes(shape->dtype);
+  const int64_t qrow = (int64_t)shape->num_q_heads * shape->head_dim;
+  const int64_t krow = (int64_t)shape->num_kv_heads * shape->head_dim;
+  if ((st = token_stride(q_stride, qrow, eb, &a.q_stride)) != PHOTON_OK) return st;
+  if ((st = token_stride(k_stride, krow, eb, &a.k_stride)) != PHOTON_OK) return st;
+  if ((st = token_stride(q_out_stride, qrow, eb, &a.q_out_stride)) != PHOTON_OK) return st;
+  if ((st = token_stride(k_out_stride, krow, eb, &a.k_out_stride)) != PHOTON_OK) return st;
+  if (num_tokens == 0) return PHOTON_OK;
+  if (!q || !k || !positions || !rope_cos_sin || !q_out || !k_out) return PHOTON_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) ||
+      !aligned16(rope_cos_sin) || !aligned16(q_out) || !aligned16(k_out) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return PHOTON_ERR_MISALIGNED;
+  uint32_t* err = nullptr;
+  if ((st = error_word(&err)) != PHOTON_OK) return st;
+  a.q = q;
+  a.k = k;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.positions = positions;
+  a.cs = static_cast<const float2*>(rope_cos_sin);
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.err = err;
+  a.eps = eps;
+  a.T = num_tokens;
+  a.Hq = shape->num_q_heads;
+  a.Hkv = shape->num_kv_heads;
+  a.D = shape->head_dim;
+  a.max_pos = max_positions;
+  a.num_axes = axes->num_axes;
+  a.dtype = shape->dtype;
+  a.half = (int)half;
+  return photon::launch_qk_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PHOTON_OK
+             : PHOTON_ERR_CUDA;
+}
+
+}  // extern "C"
+
+extern "C" {
 
 photon_status_t photon_debug_set_decode_consumer(int32_t which) {
   if (which < 0 || which > 2) return PHOTON_ERR_INVALID_ARG;

@@ -1,0 +1,409 @@
+"""The 4-bit KV cache on the GPU against the definition in 64 bits: codes and
+pairs bit for bit, read-back values to one rounding, attention within the
+bound of its documented arithmetic (int4_util.decode)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import int4_util as I
+import paged_kv_attention_photon_gb300 as P
+import workloads as W
+from gpu_util import dev, host, to_float64
+
+pytestmark = pytest.mark.gpu
+TYPES = [W.DTYPE_F16, W.DTYPE_BF16]
+
+
+def shape_for(*, seqs, hq, hkv, d, nb, mbs, dtype):
+    return P.PagedShape.make(num_seqs=seqs, num_q_heads=hq, num_kv_heads=hkv, head_dim=d,
+                             num_blocks=nb, max_blocks_per_seq=mbs, dtype=dtype)
+
+
+def ok_status():
+    st, bits = P.photon_get_last_device_error()
+    assert st == 0, bits
+
+
+def run_write(k, v, slots, nb, dtype, k_stride=0, v_stride=0, kd=None, vd=None):
+    T, hkv, d = k.shape
+    pools = [torch.full((nb, hkv, I.record_bytes(d)), 0xFF, dtype=torch.uint8, device="cuda")
+             for _ in range(2)]
+    shape = shape_for(seqs=1, hq=hkv, hkv=hkv, d=d, nb=nb, mbs=1, dtype=dtype)
+    P.photon_cache_write_int4(dev(k) if kd is None else kd, k_stride,
+                              dev(v) if vd is None else vd, v_stride, dev(slots), T, *pools, shape)
+    return [p.cpu().numpy() for p in pools]
+
+
+def want_pools(k, v, slots, nb, dtype):
+    T, hkv, d = k.shape
+    want = [np.full((nb, hkv, I.record_bytes(d)), 0xFF, dtype=np.uint8) for _ in range(2)]
+    for which, (x, pool) in enumerate(zip((k, v), want)):
+        codes, step, lo = I.quantise(x, dtype)
+        for t in range(T):
+            if 0 <= slots[t] < nb * 16:
+                for h in range(hkv):
+                    I.store_row(pool, which == 0, d, slots[t] // 16, h, slots[t] % 16, codes[t, h],
+                                step[t, h], lo[t, h])
+    return want
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,hkv", [(1, 1), (3, 2), (37, 8), (130, 3)])
+def test_write_bit_exact(dtype, d, T, hkv):
+    rng = np.random.default_rng(T * d + hkv)
+    nb = T // 16 + 3
+    slots = rng.permutation(nb * 16)[:T].astype(np.int64)
+    k = I.narrow(rng.standard_normal((T, hkv, d)) * np.exp(rng.uniform(-6, 6, (T, hkv, 1))), dtype)
+    v = I.narrow(rng.standard_normal((T, hkv, d)) + 3, dtype)
+    if T > 2:
+        slots[1] = -1
+    got = run_write(k, v, slots, nb, dtype)
+    ok_status()
+    for a, b in zip(got, want_pools(k, v, slots, nb, dtype)):
+        assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_write_hard_rows(dtype, d):
+    """Constant, tiny, huge and one-outlier rows, rows on a grid that puts many elements
+    exactly between two codes, and rows of few distinct values."""
+    rng = np.random.default_rng(5)
+    top = 65504.0 if dtype == W.DTYPE_F16 else 3.3e38
+    low = 2.0 ** -24 if dtype == W.DTYPE_F16 else 2.0 ** -130
+    rows = [np.zeros(d), np.full(d, 1.5), np.full(d, -0.0), np.full(d, top), np.full(d, -top),
+            rng.choice([-top, top], d), rng.uniform(-1, 1, d) * top,
+            rng.integers(0, 9, d) * low, rng.integers(-40, 40, d) * low,
+            np.concatenate([rng.standard_normal(d - 1), [500.0]]),
+            np.concatenate([np.full(d - 1, -7.0), [-6.5]])]
+    for unit in (1.0, 0.25, 2.0 ** -9, 3.0):
+        # steps of exactly 2 units: odd multiples of the unit lie on a border
+        rows.append(np.concatenate([rng.integers(0, 31, d - 2), [0, 30]]) * unit)
+        rows.append(np.concatenate([rng.integers(-15, 16, d - 2), [-15, 15]]) * unit)
+    for s in range(64):   # many steps near the border of two storage values
+        rows.append(np.round(rng.standard_normal(d) * 64) / 64 * (1 + s))
+    x = I.narrow(np.stack(rows)[:, None, :], dtype)
+    T = x.shape[0]
+    nb = T // 16 + 1
+    slots = np.arange(T, dtype=np.int64)[::-1].copy()
+    got = run_write(x, x[::-1].copy(), slots, nb, dtype)
+    ok_status()
+    want = want_pools(x, x[::-1].copy(), slots, nb, dtype)
+    for a, b in zip(got, want):
+        # a row's smallest element may be either zero
+        for pool in (a, b):
+            pairs = pool[:, :, 8 * d:].reshape(nb, 1, 16, 4)
+            pairs[..., 3][(pairs[..., 2] == 0) & (pairs[..., 3] == 0x80)] = 0
+        assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_write_rows_that_are_not_finite(dtype):
+    d, hkv = 128, 2
+    rng = np.random.default_rng(8)
+    x = rng.standard_normal((6, hkv, d))
+    x[1, 0, 5] = np.nan
+    x[2, 1, 127] = np.inf
+    x[3, 0, 0] = -np.inf
+    k = I.narrow(x, dtype)
+    slots = np.arange(6, dtype=np.int64)
+    got = run_write(k, k, slots, 1, dtype)
+    ok_status()
+    storage = np.float16 if dtype == W.DTYPE_F16 else np.uint16
+    for pool in got:
+        pairs = I.to_f64(np.ascontiguousarray(pool[:, :, 8 * d:]).view(storage), dtype)
+        pairs = pairs.reshape(hkv, 16, 2)
+        bad = np.zeros((hkv, 16), bool)
+        bad[0, 1] = bad[1, 2] = bad[0, 3] = True
+        bad[:, 6:] = True     # never written
+        assert np.array_equal(np.isnan(pairs).any(-1), bad)
+        assert np.array_equal(np.isnan(pairs).all(-1), bad)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_write_strides_and_bad_slots(dtype, d):
+    """A slice of a fused projection; slots outside the pool flag bit 2 and skip their row."""
+    rng = np.random.default_rng(11)
+    T, hkv, nb = 19, 4, 3
+    fused = I.narrow(rng.standard_normal((T, 3 * hkv, d)), dtype)
+    slots = rng.permutation(nb * 16)[:T].astype(np.int64)
+    slots[4], slots[7], slots[18] = nb * 16, -5, 1 << 40
+    on = dev(fused)
+    got = run_write(fused[:, :hkv], fused[:, 2 * hkv:], slots, nb, dtype, 3 * hkv * d, 3 * hkv * d,
+                    on, on[:, 2 * hkv:])
+    st, bits = P.photon_get_last_device_error()
+    assert (st, bits) == (6, 2)
+    k, v = np.ascontiguousarray(fused[:, :hkv]), np.ascontiguousarray(fused[:, 2 * hkv:])
+    for a, b in zip(got, want_pools(k, v, slots, nb, dtype)):
+        assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_gather(dtype, d):
+    contexts = [0, 1, 15, 16, 17, 50]
+    hkv = 3
+    kp, vp, bt, cl = I.build_pools(21, contexts=contexts, hkv=hkv, d=d, dtype=dtype, mbs=6)
+    shape = shape_for(seqs=6, hq=hkv, hkv=hkv, d=d, nb=kp.shape[0], mbs=6, dtype=dtype)
+    like = np.zeros((6, hkv, 96, d), dtype=np.float16 if dtype == W.DTYPE_F16 else np.uint16)
+    out = [torch.full(like.shape, -1, dtype=torch.int16, device="cuda") for _ in range(2)]
+    P.photon_paged_gather_int4(dev(kp), dev(vp), dev(bt), dev(cl), *out, shape)
+    ok_status()
+    for which, (pool, t) in enumerate(zip((kp, vp), out)):
+        got = I.to_f64(host(t, like), dtype)
+        for b, ctx in enumerate(contexts):
+            want = I.load_rows(pool, which == 0, d, bt[b], ctx, dtype)
+            # fp32 first (2^-24), then half a step of the storage type
+            tol = np.abs(want) * (I.EPS[dtype] / 2 + 2.0 ** -23) + 2.0 ** -25
+            assert (np.abs(got[b, :, :ctx] - want) <= tol).all()
+            assert not got[b, :, ctx:].any()
+    # a block outside the pool and a length outside the table: zeros and the error bits
+    bt2, cl2 = bt.copy(), cl.copy()
+    bt2[5, 1] = kp.shape[0]
+    cl2[4] = 97
+    P.photon_paged_gather_int4(dev(kp), dev(vp), dev(bt2), dev(cl2), *out, shape)
+    st, bits = P.photon_get_last_device_error()
+    assert (st, bits) == (6, 1 | 4)
+    got = I.to_f64(host(out[0], like), dtype)
+    assert not got[5, :, 16:32].any() and got[5, :, 32:50].any() and not got[4].any()
+
+
+class Decode:
+    """One decode call's device buffers; the output starts as -1 bits, the workspace as NaNs."""
+
+    def __init__(self, seed, contexts, hq, hkv, d, dtype, **pool):
+        self.kp, self.vp, self.bt, self.cl = I.build_pools(seed, contexts=contexts, hkv=hkv, d=d,
+                                                           dtype=dtype, **pool)
+        rng = np.random.default_rng(seed + 1)
+        self.q = I.narrow(rng.standard_normal((len(contexts), hq, d)), dtype)
+        self.dtype, self.scale = dtype, d ** -0.5
+        self.shape = shape_for(seqs=len(contexts), hq=hq, hkv=hkv, d=d, nb=self.kp.shape[0],
+                               mbs=self.bt.shape[1], dtype=dtype)
+        self.ws_bytes = P.photon_paged_decode_int4_workspace_size(self.shape)
+        self.ws = torch.full((max(16, self.ws_bytes),), 0xFF, dtype=torch.uint8, device="cuda")
+        self.out = torch.full(self.q.shape, -1, dtype=torch.int16, device="cuda")
+        self.up()
+
+    def up(self):
+        self.dev = [dev(x) for x in (self.q, self.kp, self.vp, self.bt, self.cl)]
+
+    def run(self, stream=None):
+        P.photon_paged_decode_int4(*self.dev, self.scale, self.out, self.ws, self.ws_bytes,
+                                   self.shape, stream)
+
+    def got(self):
+        return I.to_f64(host(self.out, self.q), self.dtype)
+
+    def check(self):
+        want, bound = I.decode(self.q, self.kp, self.vp, self.bt, self.cl, self.scale, self.dtype)
+        got = self.got()
+        assert np.isfinite(got).all()
+        worst = (np.abs(got - want) - bound).max()
+        assert worst <= 0, f"off by {np.abs(got - want).max()}, {worst} over the bound"
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (4, 1), (8, 1), (24, 3)])
+def test_decode(dtype, d, hq, hkv):
+    c = Decode(31 + hq, [0, 1, 15, 16, 17, 63, 64, 65, 300, 1, 0, 129], hq, hkv, d, dtype)
+    for _ in range(2):   # the workspace's last contents do not matter
+        c.run()
+        ok_status()
+        c.check()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (8, 1, 128)])
+def test_decode_one_long_context(hq, hkv, d):
+    c = Decode(41, [20011], hq, hkv, d, W.DTYPE_F16)
+    c.run()
+    ok_status()
+    c.check()
+
+
+def test_decode_large_batch():
+    """More sequences than threads of a CTA, empty ones in a row, more units than warps."""
+    rng = np.random.default_rng(2)
+    contexts = [int(x) for x in rng.integers(0, 40, 700)]
+    contexts[100:240] = [0] * 140
+    contexts[5], contexts[699], contexts[0] = 3000, 0, 0
+    c = Decode(43, contexts, 8, 4, 64, W.DTYPE_BF16)
+    c.run()
+    ok_status()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("direction", [1, -1])
+def test_decode_rows_of_very_different_size(dtype, direction):
+    """K and V rows that grow, or shrink, by 2^13 along the context: the running maximum
+    and the V steps' scale move."""
+    n = 400
+    c = Decode(47, [n], 4, 2, 128, dtype, scale_of=lambda j: 2.0 ** (direction * (j * 13 / n)
+                                                                     - (13 if direction > 0 else 0)))
+    c.scale = 1.0
+    c.run()
+    ok_status()
+    c.check()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
+def test_decode_scales(scale):
+    c = Decode(53, [77, 5, 200], 8, 2, 64, W.DTYPE_F16)
+    c.scale = scale
+    c.run()
+    ok_status()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size", [2.0 ** -14, 2.0 ** 10])
+def test_decode_small_and_large_queries(dtype, size):
+    c = Decode(59, [40, 17], 4, 2, 128, dtype)
+    c.q = I.narrow(I.to_f64(c.q, dtype) * size, dtype)
+    c.scale /= size
+    c.up()
+    c.run()
+    ok_status()
+    c.check()
+
+
+def test_decode_nan_row_stays_with_its_sequence():
+    """A cached row that reads back as NaN, or a NaN query, reaches its own heads only."""
+    c = Decode(61, [30, 30, 30], 8, 2, 64, W.DTYPE_F16)
+    blk = int(c.bt[1, 0])
+    c.kp[blk, 0, 8 * 64 + 12:8 * 64 + 16] = 0xFF      # row 3 of KV head 0 of sequence 1
+    c.q[2, 5, 1] = np.nan
+    c.up()
+    c.run()
+    ok_status()
+    bad = np.isnan(c.got()).any(-1)
+    want = np.zeros((3, 8), bool)
+    want[1, :4] = True
+    want[2, 5] = True
+    assert np.array_equal(bad, want)
+
+
+def test_decode_bad_tables_and_lengths():
+    c = Decode(67, [40, 100, 33], 4, 2, 128, W.DTYPE_F16)
+    want, bound = I.decode(c.q, c.kp, c.vp, c.bt, c.cl, c.scale, c.dtype)
+    c.cl[0] = c.bt.shape[1] * 16 + 1
+    c.cl[2] = -1
+    c.up()
+    c.run()
+    assert P.photon_get_last_device_error() == (6, 4)
+    got = c.got()
+    assert not got[0].any() and not got[2].any()
+    assert (np.abs(got[1] - want[1]) <= bound[1]).all()
+    # a block id outside the pool: its keys are absent
+    c.cl[:] = [16, 100, 48]
+    c.bt[1, 3] = c.kp.shape[0]
+    c.bt[0, 0] = -7                # the whole context
+    c.up()
+    c.run()
+    assert P.photon_get_last_device_error() == (6, 1)
+    got = c.got()
+    assert not got[0].any()
+    kept = np.r_[0:48, 64:100]
+    k = np.concatenate([I.load_rows(c.kp, True, 128, c.bt[1], 48, c.dtype),
+                        I.load_rows(c.kp, True, 128, c.bt[1, 4:], 36, c.dtype)], 1)
+    v = np.concatenate([I.load_rows(c.vp, False, 128, c.bt[1], 48, c.dtype),
+                        I.load_rows(c.vp, False, 128, c.bt[1, 4:], 36, c.dtype)], 1)
+    assert k.shape[1] == kept.size
+    for h in range(4):
+        s = c.scale * (k[h // 2] @ I.to_f64(c.q, c.dtype)[1, h])
+        p = np.exp(s - s.max())
+        assert (np.abs(got[1, h] - (p / p.sum()) @ v[h // 2]) <= bound[1, h] + 1e-3).all()
+
+
+def test_decode_captured_and_on_another_stream():
+    """Two calls with workspaces of their own in one graph, replayed with other lengths and
+    queries; a call on a side stream."""
+    a = Decode(71, [300, 17, 64], 8, 4, 64, W.DTYPE_F16, mbs=20)
+    b = Decode(73, [5, 900], 8, 1, 128, W.DTYPE_BF16)
+    a.run(), b.run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.run(), b.run()
+    a.cl[:] = [255, 1, 0]
+    a.q = a.q[::-1].copy()
+    a.dev[0].copy_(dev(a.q))
+    a.dev[4].copy_(dev(a.cl))
+    for _ in range(2):
+        graph.replay()
+    ok_status()
+    a.check()
+    b.check()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a.cl[:] = [300, 17, 64]
+    with torch.cuda.stream(side):
+        a.dev[4].copy_(dev(a.cl))
+        a.run()
+    side.synchronize()
+    a.check()
+
+
+def test_pool_offsets_past_32_bits():
+    """Pools of more than 4 GiB whose used blocks are at the far end."""
+    d, hkv, nb = 128, 8, 500_000
+    small = Decode(79, [40, 100], 16, hkv, d, W.DTYPE_F16)
+    n = small.kp.shape[0]
+    shape = shape_for(seqs=2, hq=16, hkv=hkv, d=d, nb=nb, mbs=small.bt.shape[1], dtype=W.DTYPE_F16)
+    assert P.photon_cache_int4_bytes(shape) > 1 << 32
+    pools = []
+    for x in (small.kp, small.vp):
+        t = torch.empty((nb, hkv, I.record_bytes(d)), dtype=torch.uint8, device="cuda")
+        t[nb - n:] = dev(x)
+        pools.append(t)
+    bt = np.where(small.bt >= 0, small.bt + nb - n, -1).astype(np.int32)
+    P.photon_paged_decode_int4(small.dev[0], *pools, dev(bt), small.dev[4], small.scale, small.out,
+                               small.ws, small.ws_bytes, shape)
+    ok_status()
+    small.check()
+    # and a write there
+    rng = np.random.default_rng(3)
+    k = I.narrow(rng.standard_normal((2, hkv, d)), W.DTYPE_F16)
+    slots = np.array([nb * 16 - 1, (nb - n) * 16 + 3], dtype=np.int64)
+    P.photon_cache_write_int4(dev(k), 0, dev(k), 0, dev(slots), 2, *pools, shape)
+    ok_status()
+    want = want_pools(k, k, slots - (nb - n) * 16, n, W.DTYPE_F16)
+    for pool, w in zip(pools, want):
+        got = pool[nb - n:].cpu().numpy()
+        for s, t in ((n * 16 - 1, 0), (3, 1)):
+            pair = slice(8 * d + 4 * (s % 16), 8 * d + 4 * (s % 16) + 4)
+            assert np.array_equal(got[s // 16, :, pair], w[s // 16, :, pair])
+
+
+def test_write_then_decode():
+    """A step at a time: the new rows go in, the attention sees them."""
+    dtype, hq, hkv, d = W.DTYPE_BF16, 8, 4, 64
+    c = Decode(83, [33, 16, 1], hq, hkv, d, dtype, mbs=4)
+    rng = np.random.default_rng(4)
+    fresh = [b for b in range(c.kp.shape[0]) if b not in c.bt]
+    for step in range(3):
+        slots = np.zeros(3, dtype=np.int64)
+        for b in range(3):
+            pos = int(c.cl[b])
+            if pos % 16 == 0:
+                c.bt[b, pos // 16] = fresh.pop()
+            slots[b] = int(c.bt[b, pos // 16]) * 16 + pos % 16
+            c.cl[b] += 1
+        k = I.narrow(rng.standard_normal((3, hkv, d)), dtype)
+        v = I.narrow(rng.standard_normal((3, hkv, d)), dtype)
+        P.photon_cache_write_int4(dev(k), 0, dev(v), 0, dev(slots), 3, c.dev[1], c.dev[2], c.shape)
+        for which, (x, pool) in enumerate(((k, c.kp), (v, c.vp))):
+            codes, st, lo = I.quantise(x, dtype)
+            for b in range(3):
+                for h in range(hkv):
+                    I.store_row(pool, which == 0, d, slots[b] // 16, h, slots[b] % 16, codes[b, h],
+                                st[b, h], lo[b, h])
+        c.dev[3], c.dev[4] = dev(c.bt), dev(c.cl)
+        c.run()
+        ok_status()
+        assert np.array_equal(c.dev[1].cpu().numpy(), c.kp)
+        assert np.array_equal(c.dev[2].cpu().numpy(), c.vp)
+        c.check()
