@@ -392,6 +392,37 @@ photon_status_t photon_qk_norm_rope(const void* q, int64_t q_stride, const void*
                                     int64_t k_out_stride, const photon_paged_shape_t* shape,
                                     photon_stream_t stream);
 
+/* Causal attention of whole prompts over their own K and V rows, before (or
+ * without) a cache: what a prompt that goes into a 4-bit cache attends with.
+ * Prompt b is tokens query_start[b] .. query_start[b+1]-1 of q, k and v; for
+ * its token i and q head h
+ *     out[i][h] = sum_{j <= i} softmax_j(scale * q[i][h] . k[j][kvh]) v[j][kvh]
+ * over the prompt's tokens j, kvh = h / G, in fp32 arithmetic from fp16/bf16
+ * operands on the tensor cores, out rounded to the stored dtype (the softmax
+ * weights enter the second product rounded to the storage type).
+ *   q, out        [num_tokens] rows of num_q_heads x head_dim
+ *   k, v          [num_tokens] rows of num_kv_heads x head_dim
+ *   *_stride      elements from a token's row to the next one's (0: packed),
+ *                 at least the row's elements and a multiple of 8
+ *   query_start   int32 [num_seqs + 1], non-decreasing, query_start[0] >= 0,
+ *                 query_start[num_seqs] <= num_tokens
+ *   max_query_len host upper bound of every prompt's length
+ * Rows of out that belong to no prompt are left as they were, and rows of q, k
+ * and v that belong to none may hold anything; a NaN or an infinity in a
+ * prompt's own v may reach any of that prompt's rows.  dtype must be
+ * PHOTON_F16 or PHOTON_BF16 (PHOTON_ERR_UNSUPPORTED for f32).  A prompt with a
+ * negative length, rows outside [0, num_tokens) or more tokens than
+ * max_query_len sets device error bit 32 and is skipped.  num_seqs == 0,
+ * num_tokens == 0 or max_query_len == 0 is a no-op.  out must not overlap q, k
+ * or v.  No workspace.  Uses shape: num_seqs, num_q_heads, num_kv_heads,
+ * head_dim, dtype. */
+photon_status_t photon_prompt_attention(const void* q, int64_t q_stride, const void* k,
+                                        int64_t k_stride, const void* v, int64_t v_stride,
+                                        const int32_t* query_start, int32_t num_tokens,
+                                        int32_t max_query_len, float scale, void* out,
+                                        int64_t out_stride, const photon_paged_shape_t* shape,
+                                        photon_stream_t stream);
+
 /* Test and tuning hook: which consumer the decode attention kernel runs
  * (photon_paged_decode, _step, _step_rope, _noalloc).  0 (default) = by the group size: the tensor-core consumer
  * (mma.sync over tensor-map copies of the blocks) for fp16/bf16 storage and
@@ -487,7 +518,7 @@ photon_status_t photon_paged_gather(const void* k_cache, const void* v_cache,
  * 4 = context length out of range, 8 = a bounded wait inside a kernel ran out
  * (the call's output is then incomplete), 16 = a RoPE position outside the
  * cos/sin table, 32 = inconsistent query_start / max_query_len of
- * photon_paged_multi_query. */
+ * photon_paged_multi_query or photon_prompt_attention. */
 photon_status_t photon_get_last_device_error(photon_stream_t stream, uint32_t* bits);
 
 /* Static text for a status code (never NULL). */

@@ -33,7 +33,7 @@ __all__ = [
     "photon_paged_decode_fp8_workspace_size", "photon_paged_decode_fp8",
     "photon_cache_int4_bytes", "photon_cache_write_int4", "photon_paged_gather_int4",
     "photon_paged_decode_int4_workspace_size", "photon_paged_decode_int4",
-    "RopeAxes", "photon_qk_norm_rope",
+    "RopeAxes", "photon_qk_norm_rope", "photon_prompt_attention",
     "photon_debug_wait_probe", "photon_debug_read_probe", "Scheduler",
     "F32", "F16", "BF16", "STATUS",
 ]
@@ -155,6 +155,8 @@ def _load() -> ctypes.CDLL:
     lib.photon_qk_norm_rope.argtypes = [P, I64, P, I64, P, P, F32, P, P, I32,
                                         ctypes.POINTER(RopeAxes), I32, P, I64, P, I64, SP, P]
     lib.photon_qk_norm_rope.restype = ctypes.c_int
+    lib.photon_prompt_attention.argtypes = [P, I64, P, I64, P, I64, P, I32, I32, F32, P, I64, SP, P]
+    lib.photon_prompt_attention.restype = ctypes.c_int
     lib.photon_paged_multi_query.restype = ctypes.c_int
     # host scheduler (include/photon_scheduler.h)
     lib.photon_scheduler_create.argtypes = [P, ctypes.POINTER(P)]
@@ -402,6 +404,17 @@ def photon_qk_norm_rope(q, q_stride: int, k, k_stride: int, q_weight, k_weight, 
         float(eps), _ptr(positions), _ptr(rope_cos_sin), int(max_positions),
         ctypes.byref(axes), int(num_tokens), _ptr(q_out), int(q_out_stride), _ptr(k_out),
         int(k_out_stride), ctypes.byref(shape), _stream(stream)), "photon_qk_norm_rope")
+
+
+def photon_prompt_attention(q, q_stride: int, k, k_stride: int, v, v_stride: int, query_start,
+                            num_tokens: int, max_query_len: int, scale: float, out,
+                            out_stride: int, shape: PagedShape, stream=None) -> None:
+    """Causal attention of packed whole prompts over their own K and V rows;
+    strides in elements from token to token, 0 = packed."""
+    _check(_load().photon_prompt_attention(
+        _ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(v), int(v_stride),
+        _ptr(query_start), int(num_tokens), int(max_query_len), float(scale), _ptr(out),
+        int(out_stride), ctypes.byref(shape), _stream(stream)), "photon_prompt_attention")
 
 
 def photon_paged_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, scale: float,

@@ -15,6 +15,7 @@
 #include "../../include/photon_paged.h"
 #include "int4_common.cuh"
 #include "photon_common.cuh"
+#include "prompt_attention.cuh"
 #include "qk_norm_rope.cuh"
 
 namespace photon {
@@ -848,6 +849,56 @@ photon_status_t photon_qk_norm_rope(const void* q, int64_t q_stride, const void*
 }  // extern "C"
 
 extern "C" {
+
+photon_status_t photon_prompt_attention(const void* q, int64_t q_stride, const void* k,
+                                        int64_t k_stride, const void* v, int64_t v_stride,
+                                        const int32_t* query_start, int32_t num_tokens,
+                                        int32_t max_query_len, float scale, void* out,
+                                        int64_t out_stride, const photon_paged_shape_t* shape,
+                                        photon_stream_t stream) {
+  photon_status_t st = check_shape(shape);
+  if (st != PHOTON_OK) return st;
+  if (shape->dtype == PHOTON_F32) return PHOTON_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || num_tokens < 0 || max_query_len < 0) return PHOTON_ERR_INVALID_ARG;
+  photon::PromptArgs a{};
+  const int64_t qrow = (int64_t)shape->num_q_heads * shape->head_dim;
+  const int64_t krow = (int64_t)shape->num_kv_heads * shape->head_dim;
+  if ((st = token_stride(q_stride, qrow, 2, &a.q_stride)) != PHOTON_OK) return st;
+  if ((st = token_stride(k_stride, krow, 2, &a.k_stride)) != PHOTON_OK) return st;
+  if ((st = token_stride(v_stride, krow, 2, &a.v_stride)) != PHOTON_OK) return st;
+  if ((st = token_stride(out_stride, qrow, 2, &a.out_stride)) != PHOTON_OK) return st;
+  if (shape->num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PHOTON_OK;
+  // a copy's coordinates, a prompt's rows and its items are 32-bit numbers; a
+  // tensor map's strides end at 2^40 bytes
+  const int64_t G = shape->num_q_heads / shape->num_kv_heads;
+  if (num_tokens * G > INT_MAX / 2 || max_query_len * G > INT_MAX / 2 || krow > INT_MAX / 2 ||
+      std::max(a.q_stride, std::max(a.k_stride, a.v_stride)) >= (1ll << 38))
+    return PHOTON_ERR_UNSUPPORTED;
+  if (!q || !k || !v || !query_start || !out) return PHOTON_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(query_start) & 3u))
+    return PHOTON_ERR_MISALIGNED;
+  uint32_t* err = nullptr;
+  if ((st = error_word(&err)) != PHOTON_OK) return st;
+  if ((st = num_sms(&a.num_sms)) != PHOTON_OK) return st;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.query_start = query_start;
+  a.out = out;
+  a.err = err;
+  a.qscale = (float)((double)scale * 1.4426950408889634);
+  a.B = shape->num_seqs;
+  a.Hq = shape->num_q_heads;
+  a.Hkv = shape->num_kv_heads;
+  a.D = shape->head_dim;
+  a.num_tokens = num_tokens;
+  a.max_query_len = max_query_len;
+  a.dtype = shape->dtype;
+  return photon::launch_prompt_attention(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PHOTON_OK
+             : PHOTON_ERR_CUDA;
+}
 
 photon_status_t photon_debug_set_decode_consumer(int32_t which) {
   if (which < 0 || which > 2) return PHOTON_ERR_INVALID_ARG;

@@ -141,6 +141,36 @@ def test_qk_axes_refusals(lib):
     assert _qk(lib, s, bad) == INVALID
 
 
+def _prompt(lib, shape, q=FAKE, qs=0, k=FAKE, ks=0, v=FAKE, vs=0, start=FAKE, n=7, longest=7,
+            scale=0.1, out=FAKE2, os=0):
+    return lib.photon_prompt_attention(q, qs, k, ks, v, vs, start, n, longest, scale, out, os,
+                                       ctypes.byref(shape), None)
+
+
+def test_prompt_refusals(lib):
+    for over, want in BAD_SHAPES:
+        assert _prompt(lib, _shape(**over)) == want
+    s = _shape()
+    assert _prompt(lib, s, n=-1) == INVALID
+    assert _prompt(lib, s, longest=-1) == INVALID
+    for scale in (float("nan"), float("inf")):
+        assert _prompt(lib, s, scale=scale) == INVALID
+    assert _prompt(lib, s, n=0, q=None) == OK
+    assert _prompt(lib, s, longest=0, q=None) == OK
+    assert _prompt(lib, _shape(num_seqs=0), q=None) == OK
+    for name in ("q", "k", "v", "start", "out"):
+        assert _prompt(lib, s, **{name: None}) == INVALID
+    for name in ("q", "k", "v", "out"):
+        assert _prompt(lib, s, **{name: FAKE + 8}) == MISALIGNED
+    assert _prompt(lib, s, start=FAKE + 2) == MISALIGNED
+    for name, row in (("qs", 2048), ("ks", 1024), ("vs", 1024), ("os", 2048)):
+        assert _prompt(lib, s, **{name: row - 8}) == INVALID
+        assert _prompt(lib, s, **{name: row + 4}) == MISALIGNED
+    assert _prompt(lib, s, vs=1 << 38) == UNSUPPORTED
+    assert _prompt(lib, s, n=2 ** 31 - 1, longest=1) == UNSUPPORTED
+    assert _prompt(lib, s, longest=2 ** 31 - 1) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("dtype", [W.DTYPE_F16, W.DTYPE_BF16])
 @pytest.mark.parametrize("keys", [True, False])
 def test_oracle_round_trip(dtype, keys):
