@@ -872,7 +872,9 @@ photon_status_t photon_prompt_attention(const void* q, int64_t q_stride, const v
   // tensor map's strides end at 2^40 bytes
   const int64_t G = shape->num_q_heads / shape->num_kv_heads;
   if (num_tokens * G > INT_MAX / 2 || max_query_len * G > INT_MAX / 2 || krow > INT_MAX / 2 ||
-      std::max(a.q_stride, std::max(a.k_stride, a.v_stride)) >= (1ll << 38))
+      (num_tokens * G / 256 + shape->num_seqs) * shape->num_kv_heads > INT_MAX / 2 ||
+      std::max(std::max(a.q_stride, a.out_stride), std::max(a.k_stride, a.v_stride)) >=
+          (1ll << 38))
     return PHOTON_ERR_UNSUPPORTED;
   if (!q || !k || !v || !query_start || !out) return PHOTON_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||

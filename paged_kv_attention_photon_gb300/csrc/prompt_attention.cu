@@ -13,10 +13,12 @@
 //
 // A persistent CTA per SM takes items of 256 query rows of one (prompt, KV
 // head) -- row r is (token r / G, head r % G), so one K/V chunk serves the
-// whole group -- as two tiles of 128 rows, and runs 12 warps in fixed roles:
+// whole group -- as two tiles of 128 rows, and runs 15 warps in fixed roles:
 //   warps 0-3, 4-7  softmax of tile 0, 1: thread r owns TMEM lane r
 //   warp 8, 9       tensor-map copies of Q and K, of V (128-byte swizzle)
-//   warp 10, 11     issue the products of tile 0, 1
+//   warp 10, 11     issue S of tile 0, 1
+//   warp 12, 13     issue P V of tile 0, 1
+//   warp 14         finds the items
 // The two tiles run in antiphase: while one's softmax is on, the other's
 // products are.  Per tile, TMEM holds S (128 columns) and O (D columns); P
 // overwrites the second half of S as 16-bit pairs and is read from there as
@@ -27,14 +29,16 @@
 //
 // Items are numbered tile by tile from the prompts' far ends (the longest key
 // ranges) to their beginnings, and dealt to the CTAs forwards and backwards in
-// turn, so that all finish close together; every warp finds its next item from
-// the lengths alone (pa_locate), without a queue.
+// turn, so that all finish close together; each CTA finds its items from the lengths alone
+// (pa_locate), without a queue.
 //
 // Barriers complete once per use; use i has parity i & 1:
 //   k_full, v_full[st]   a chunk landed      k_free, v_free[st]  both tiles are done with it
 //   q_full[t]            Q tile landed       q_free[t]           the item's last S product is done
-//   s_full[t]            S written           p_full[t]           P written, S read
+//   s_full[t]            S written           p_full[t][h]        P of 64 keys written
 //   o_done[t]            O += P V done; the tile's next S may overwrite P
+//   turn[t]              tile t's weights of a chunk are written
+//   item_full, item_free[i]  an item is known; every role has read it
 #include <math.h>
 
 #include <algorithm>
@@ -49,20 +53,32 @@ constexpr int kPaRows = 128;            // query rows of a tile = TMEM lanes
 constexpr int kPaKeys = 128;            // keys of a chunk
 constexpr int kPaTiles = 2;
 constexpr int kPaItemRows = kPaTiles * kPaRows;
-constexpr int kPaThreads = 384;
+constexpr int kPaThreads = 512;        // four warpgroups; warp 15 has no role
+// Registers a thread: 512 x 128 at launch, dealt anew to the softmax
+// warpgroups and the other two (160 + 160 + 96 + 96 = 4 x 128).
+constexpr int kPaSoftmaxRegs = 160, kPaOtherRegs = 96;
 constexpr uint32_t kPaTmemP = 64;       // P of a tile: the second half of its S columns
 constexpr uint32_t kPaTmemO = 256;      // S of tile t: columns [128 t, 128 t + 128); then the O's
 constexpr float kPaRescaleLog2 = 8.f;
+constexpr int kPaItems = 4;             // items found ahead
+constexpr int kPaRoles = 14;            // warps that work on an item
 
 template <int D>
 struct PaCfg {
-  static constexpr int kKStages = 3;
+  static constexpr int kKStages = D == 128 ? 2 : 3;
   static constexpr int kVStages = D == 128 ? 2 : 3;
+  // The tiles' softmaxes take turns, so that one's runs while the other's
+  // products do (left alone they fall into step: 1 x 16384 tokens 811 us).
+  // At d = 128 the turn covers the maximum too (703 us, the weights alone
+  // 774 us); at d = 64, where the products are half as long, only the weights
+  // (4 x 4096 tokens 334 us, with the maximum 369 us).
+  static constexpr bool kTurnFirst = D == 128;
   static constexpr int kQBytes = kPaRows * D * 2;
   static constexpr int kKvBytes = kPaKeys * D * 2;
   static constexpr int kOffK = kPaTiles * kQBytes;
   static constexpr int kOffV = kOffK + kKStages * kKvBytes;
-  static constexpr int kSmem = kOffV + kVStages * kKvBytes + 1024;   // + alignment to a swizzle atom
+  static constexpr int kOffO = kOffV + kVStages * kKvBytes;   // 4 KB a softmax warp: 32 rows x 64
+  static constexpr int kSmem = kOffO + kPaTiles * 4 * 4096 + 1024;   // + alignment to a swizzle atom
 };
 
 // MN-major V operand (sw128_desc walked along N): 64-element blocks of N are
@@ -84,6 +100,21 @@ __device__ __forceinline__ void tma_load_box3(uint32_t dst, const CUtensorMap* m
       "%3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
+}
+
+// Tensor copy of a box from shared memory to global memory, in a bulk group of
+// its own.
+__device__ __forceinline__ void tma_store_box3(const CUtensorMap* map, int x, int y, int z,
+                                               uint32_t src) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(src)
+      : "memory");
+}
+// This thread's bulk stores have read their shared memory.
+__device__ __forceinline__ void bulk_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // Bounded wait for a barrier phase, by a whole warp; false after kWaitLimitNs,
@@ -123,19 +154,21 @@ __device__ __forceinline__ int pa_tiles_of(const PromptArgs& a, int G, int b) {
 // index of any prompt down, prompts in order within one index.  F(x), the
 // number of (prompt, tile) with tile index >= x, falls with x: the tile index
 // is the largest x with F(x) > L / Hkv.  `first` holds pa_tiles_of(lane).
-__device__ __forceinline__ bool pa_locate(const PromptArgs& a, int G, long long L, int first,
+__device__ __forceinline__ bool pa_locate(const PromptArgs& a, int G, uint32_t L, int first,
                                           int lane, PaItem& it) {
   auto tiles = [&](int b0) { return b0 == 0 ? first : pa_tiles_of(a, G, b0 + lane); };
-  auto above = [&](int x) -> int {   // F(x)
+  auto above = [&](int x) -> uint32_t {   // F(x)
     int s = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) s += max(0, tiles(b0) - x);
-    return (int)__reduce_add_sync(0xffffffffu, (unsigned)s);
+    return __reduce_add_sync(0xffffffffu, (unsigned)s);
   };
-  const long long i = L / a.Hkv;
+  const uint32_t i = L / (uint32_t)a.Hkv;
   if (i >= above(0)) return false;
-  int lo = 0, hi = (a.max_query_len * G + kPaItemRows - 1) / kPaItemRows, f_hi = 0;
+  int lo = 0, hi = (a.max_query_len * G + kPaItemRows - 1) / kPaItemRows;
+  uint32_t f_hi = 0;
   while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2, f = above(mid);
+    const int mid = lo + (hi - lo) / 2;
+    const uint32_t f = above(mid);
     if (f > i) {
       lo = mid;
     } else {
@@ -143,7 +176,7 @@ __device__ __forceinline__ bool pa_locate(const PromptArgs& a, int G, long long 
       f_hi = f;
     }
   }
-  int r = (int)i - f_hi, b = 0;
+  int r = (int)(i - f_hi), b = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const bool in = tiles(b0) > lo;
     const unsigned mask = __ballot_sync(0xffffffffu, in);
@@ -157,7 +190,7 @@ __device__ __forceinline__ bool pa_locate(const PromptArgs& a, int G, long long 
   }
   it.q0 = __ldg(a.query_start + b);
   it.n = __ldg(a.query_start + b + 1) - it.q0;
-  it.kvh = (int)(L % a.Hkv);
+  it.kvh = (int)(L - i * a.Hkv);
   it.row0 = lo * kPaItemRows;
   return true;
 }
@@ -183,20 +216,26 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kPaThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
                             const __grid_constant__ CUtensorMap tm_k,
-                            const __grid_constant__ CUtensorMap tm_v, const PromptArgs a) {
+                            const __grid_constant__ CUtensorMap tm_v,
+                            const __grid_constant__ CUtensorMap tm_o, const PromptArgs a) {
   using C = PaCfg<D>;
   constexpr int SK = C::kKStages, SV = C::kVStages;
   extern __shared__ unsigned char pa_smem_raw[];
   __shared__ __align__(8) uint64_t k_full[SK], k_free[SK], v_full[SV], v_free[SV],
-      q_full[kPaTiles], q_free[kPaTiles], s_full[kPaTiles], p_full[kPaTiles], o_done[kPaTiles],
-      v_tail;
+      q_full[kPaTiles], q_free[kPaTiles], s_full[kPaTiles], p_full[kPaTiles][2], o_done[kPaTiles],
+      v_tail, turn[kPaTiles], item_full[kPaItems], item_free[kPaItems];
+  __shared__ int4 items[kPaItems];   // (first token, tokens, KV head, first row); tokens 0: the end
   __shared__ uint32_t tmem_slot;
   __shared__ int gave_up_word;
   volatile int* gave_up = &gave_up_word;
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(pa_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sQ = smem_addr(smem), sK = sQ + C::kOffK, sV = sQ + C::kOffV;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // uniform() tells the compiler that a value is the same in all lanes, so that
+  // what the products take (descriptors, addresses) is kept and computed in
+  // uniform registers
+  auto uniform = [](uint32_t x) -> uint32_t { return __shfl_sync(0xffffffffu, x, 0); };
+  const int tid = threadIdx.x, warp = (int)uniform(tid >> 5), lane = tid & 31;
   const int G = a.Hq / a.Hkv;
 
   if (tid == 0) {
@@ -213,10 +252,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       mbar_init(&q_full[t], 1);
       mbar_init(&q_free[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);   // one arrival per softmax warp
+      mbar_init(&p_full[t][0], 4);   // one arrival per softmax warp
+      mbar_init(&p_full[t][1], 4);
       mbar_init(&o_done[t], 1);
+      mbar_init(&turn[t], 4);     // one arrival per softmax warp
     }
     mbar_init(&v_tail, 1);
+    for (int i = 0; i < kPaItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_free[i], kPaRoles);
+    }
     mbar_init_fence();
   }
   if (warp == 0) {
@@ -236,7 +281,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = uniform(tmem_slot);
 
   if (blockIdx.x == 0 && warp == 0) {
     // rejected prompts
@@ -246,190 +291,47 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         raise_error(a.err, kErrQuery);
     }
   }
-  const int first = pa_tiles_of(a, G, lane);
-  const long long N = gridDim.x;
-  // the CTA's items: one from each run of N, forwards and backwards in turn
-  auto item_of = [&](long long round) -> long long {
-    return round * N + (round & 1 ? N - 1 - blockIdx.x : blockIdx.x);
-  };
   bool ok = true;
   PaItem it;
-
-  if (warp == 8) {
-    // ================================================================ Q and K copies
-    uint32_t kc = 0;                      // chunks so far
-    uint32_t q_count[kPaTiles] = {0, 0};   // Q tiles asked for so far
-    for (long long m = 0; ok && pa_locate(a, G, item_of(m), first, lane, it); ++m) {
-      const PaTile t0 = pa_tile(it, G, 0), t1 = pa_tile(it, G, 1);
-      const int chunks = max(t0.chunks, t1.chunks);
-      for (int c = 0; c < chunks && ok; ++c, ++kc) {
-        const int st = kc % SK;
-        if (kc >= SK) ok = pa_wait(&k_free[st], ((kc / SK) - 1) & 1, gave_up);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&k_full[st], C::kKvBytes);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_box(sK + st * C::kKvBytes + h * (kPaKeys * 128), &tm_k, it.kvh * D + h * 64,
-                         it.q0 + c * kPaKeys, &k_full[st]);
-        }
-        __syncwarp();
-        if (c > 0) continue;
-        // the Q tiles, after the first chunk is on its way
-        for (int t = 0; t < kPaTiles && ok; ++t) {
-          if (m > 0) ok = pa_wait(&q_free[t], (m - 1) & 1, gave_up);
-          if (!ok) break;
-          ++q_count[t];
-          if (lane != 0) continue;
-          if ((t == 0 ? t0.rows : t1.rows) == 0) {
-            mbar_arrive(&q_full[t]);
-            continue;
-          }
-          mbar_arrive_expect_tx(&q_full[t], C::kQBytes);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_box3(sQ + t * C::kQBytes + h * (kPaRows * 128), &tm_q, h * 64, it.kvh * G,
-                          it.q0 + (it.row0 + t * kPaRows) / G, &q_full[t]);
-        }
-        __syncwarp();
-      }
-    }
-    if (!ok) {
-      // what is in flight lands before the CTA ends
-      for (uint32_t c = kc > SK ? kc - SK : 0; c < kc; ++c)
-        (void)mbar_wait_bounded(&k_full[c % SK], (c / SK) & 1);
-      for (int t = 0; t < kPaTiles; ++t)
-        if (q_count[t] > 0) (void)mbar_wait_bounded(&q_full[t], (q_count[t] - 1) & 1);
-    }
-  } else if (warp == 9) {
-    // ================================================================ V copies
-    uint32_t vc = 0, tails = 0;
-    for (long long m = 0; ok && pa_locate(a, G, item_of(m), first, lane, it); ++m) {
-      const PaTile t0 = pa_tile(it, G, 0), t1 = pa_tile(it, G, 1);
-      const int chunks = max(t0.chunks, t1.chunks), kend = max(t0.kend, t1.kend);
-      for (int c = 0; c < chunks && ok; ++c, ++vc) {
-        const int st = vc % SV;
-        if (vc >= SV) ok = pa_wait(&v_free[st], ((vc / SV) - 1) & 1, gave_up);
-        if (!ok) break;
-        // The products read whole groups of 16 keys.  Rows past the last key
-        // meet zero weights, but 0 x NaN would not vanish: the last chunk
-        // lands on a barrier of its own and its group is filled up with zeros
-        // before the stage is handed over.
-        const int valid = min(kPaKeys, kend - c * kPaKeys);
-        const bool fill = valid % 16 != 0;
-        uint64_t* land = fill ? &v_tail : &v_full[st];
-        if (lane == 0) {
-          mbar_arrive_expect_tx(land, C::kKvBytes);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_box(sV + st * C::kKvBytes + h * (kPaKeys * 128), &tm_v, it.kvh * D + h * 64,
-                         it.q0 + c * kPaKeys, land);
-        }
-        __syncwarp();
-        if (fill) {
-          ok = pa_wait(&v_tail, tails & 1, gave_up);
-          ++tails;
-          if (!ok) break;
-          unsigned char* rows = smem + C::kOffV + st * C::kKvBytes;
-          for (int i = lane; i < (16 - valid % 16) * (D / 8); i += 32) {
-            const int r = valid + i / (D / 8), ch = i % (D / 8);
-            *reinterpret_cast<uint4*>(rows + (ch >> 3) * (kPaKeys * 128) + r * 128 +
-                                      (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_full[st]);
-        }
-      }
-    }
-    if (!ok) {
-      for (uint32_t c = vc > SV ? vc - SV : 0; c < vc; ++c)
-        (void)mbar_wait_bounded(&v_full[c % SV], (c / SV) & 1);
-    }
-  } else if (warp >= 10) {
-    // ================================================================ products
-    const int t = warp - 10;
-    const uint32_t id_s = f16_idesc<T>(kPaRows, kPaKeys);
-    const uint32_t id_o = f16_idesc<T>(kPaRows, D) | (1u << 16);   // B (V) MN-major
-    // a descriptor's start address is address >> 4 in its low 14 bits; every
-    // operand lies below 256 KB, so offsets are added to the base's descriptor
-    const uint64_t q_desc = sw128_desc(sQ + t * C::kQBytes);
-    const uint64_t k_desc = sw128_desc(sK), v_desc = pa_v_desc(sV);
-    const uint32_t t_s = tmem + t * kPaKeys, t_o = tmem + kPaTmemO + t * D;
-    uint32_t kc = 0, vc = 0, done = 0;   // K and V chunks so far; chunks of this tile
-    for (long long m = 0; ok && pa_locate(a, G, item_of(m), first, lane, it); ++m) {
-      const PaTile mine = pa_tile(it, G, t), other = pa_tile(it, G, 1 - t);
-      const int chunks = max(mine.chunks, other.chunks);
-      ok = pa_wait(&q_full[t], m & 1, gave_up);
-      if (!ok) break;
-      if (mine.chunks == 0 && lane == 0) mbar_arrive(&q_free[t]);
-      for (int c = 0; c <= chunks; ++c) {
-        if (c > 0) {
-          // O += P V of chunk c - 1
-          const int st = vc % SV;
-          ok = pa_wait(&v_full[st], (vc / SV) & 1, gave_up);
-          if (!ok) break;
-          if (c - 1 < mine.chunks) {
-            ok = pa_wait(&p_full[t], done & 1, gave_up);
-            if (!ok) break;
-            tc_fence_after();
-            const int steps = (min(kPaKeys, mine.kend - (c - 1) * kPaKeys) + 15) / 16;
-            const uint64_t vb = v_desc + (uint64_t)((st * C::kKvBytes) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < kPaKeys / 16; ++kk)
-              tc_mma_ts_warp(t_o, t_s + kPaTmemP + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), id_o,
-                             (c > 1 || kk > 0) ? 1u : 0u, lane == 0 && kk < steps);
-            if (lane == 0) {
-              tc_commit(&o_done[t]);
-              tc_commit(&v_free[st]);
-            }
-            ++done;
-          } else if (lane == 0) {
-            mbar_arrive(&v_free[st]);
-          }
-          ++vc;
-        }
-        if (c < chunks) {
-          // S = Q K^T of chunk c, over the P of the tile's previous chunk
-          const int st = kc % SK;
-          ok = pa_wait(&k_full[st], (kc / SK) & 1, gave_up);
-          if (!ok) break;
-          if (c < mine.chunks) {
-            if (done > 0) ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t kb = k_desc + (uint64_t)((st * C::kKvBytes) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * (kPaKeys * 128) + (kk & 3) * 32;
-              tc_mma_warp(t_s, q_desc + (uint64_t)(off >> 4), kb + (uint64_t)(off >> 4), id_s,
-                          kk > 0, lane == 0);
-            }
-            if (lane == 0) {
-              tc_commit(&s_full[t]);
-              tc_commit(&k_free[st]);
-              if (c + 1 == mine.chunks) tc_commit(&q_free[t]);
-            }
-          } else if (lane == 0) {
-            mbar_arrive(&k_free[st]);
-          }
-          ++kc;
-        }
-      }
-    }
-  } else {
+  // the CTA's m-th item, from the warp that finds them; false past the last one
+  auto take = [&](uint32_t m, PaItem& to) -> bool {
+    const int slot = m % kPaItems;
+    ok = pa_wait(&item_full[slot], (m / kPaItems) & 1, gave_up);
+    if (!ok) return false;
+    const int4 v = items[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_free[slot]);
+    to.q0 = v.x;
+    to.n = v.y;
+    to.kvh = v.z;
+    to.row0 = v.w;
+    return to.n > 0;
+  };
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPaSoftmaxRegs));
     // ================================================================ softmax rows
     const int t = warp >> 2;
     const int trow = (warp & 3) * 32 + lane;   // row inside the tile = TMEM lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_base + t * kPaKeys;
     const uint32_t t_o = tmem + lane_base + kPaTmemO + t * D;
+    unsigned char* stage = smem + C::kOffO + warp * 4096;
     const float qscale = a.qscale;
-    const float qmul = qscale > 0.f ? qscale : 1.f;   // multiplier left for the exponent
+    // a zero scale as a tiny one: every weight is 1 and -inf stays -inf
+    const float qmul = fmaxf(fabsf(qscale), 1e-37f);
     uint32_t done = 0;                                // chunks of this tile so far
-    for (long long m = 0; ok && pa_locate(a, G, item_of(m), first, lane, it); ++m) {
+    uint32_t turns = 0;                               // of them, chunks that both tiles have
+    PaItem next;
+    bool have = take(0, next);
+    for (uint32_t m = 1; ok && have; ++m) {
+      it = next;
       const PaTile mine = pa_tile(it, G, t);
-      if (mine.rows == 0) continue;
+      if (mine.rows == 0) {
+        have = take(m, next);
+        continue;
+      }
+      // chunks that both tiles work on (the first tile's key range is the shorter one)
+      const int both = min(mine.chunks, pa_tile(it, G, 1 - t).chunks);
       const int first_row = it.row0 + t * kPaRows;
       const int my_pos = (first_row + min(trow, mine.rows - 1)) / G;
       const int warp_row = (warp & 3) * 32;
@@ -437,27 +339,39 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const int pos_max = (first_row + min(warp_row + 31, mine.rows - 1)) / G;
       float m_run = -INFINITY, l_run = 0.f;
       for (int c = 0; c < mine.chunks; ++c, ++done) {
+        // The tiles take turns on chunks that both have: tile 1 after tile 0,
+        // tile 0's next after tile 1.
+        auto my_turn = [&]() -> bool {
+          if (c < both && (t == 1 || turns > 0))
+            ok = pa_wait(&turn[1 - t], (t == 1 ? turns : turns - 1) & 1, gave_up);
+          return ok;
+        };
         ok = pa_wait(&s_full[t], done & 1, gave_up);
         if (!ok) break;
+        if (C::kTurnFirst && !my_turn()) break;
         tc_fence_after();
         const int key0 = c * kPaKeys;
         // scores of 64 of the chunk's keys, -inf where they lie past the row
-        auto scores = [&](int half, float (&s)[64]) {
+        float s[64];
+        auto scores = [&](int half) {
           tmem_ld64(t_s + 64 * half, s);
-          const int k0 = key0 + 64 * half;
-          if (k0 + 63 > pos_min) {
+          const int lim = my_pos - key0 - 64 * half;   // the row's last key of these
+          if (key0 + 64 * half + 63 > pos_min) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (k0 + j > my_pos) s[j] = -INFINITY;
-          }
-          if (!(qscale > 0.f)) {
-            // a negative (or zero) scale turns the order of the scores around
-#pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (k0 + j <= my_pos) s[j] *= qscale;
+            for (int j = 0; j < 64; ++j) s[j] = j > lim ? -INFINITY : s[j];
           }
         };
-        auto maximum = [&](const float (&s)[64]) -> float {
+        // The second half's scores stay in registers while the maximum is
+        // settled; the first half's are read again after them (128 scores a
+        // thread would spill).  P takes the columns of the second half, so
+        // what is still to be read is not overwritten.  One instance of each
+        // piece of code: unrolled twice it no longer stays in the instruction
+        // cache, and the rarely taken masks then cost thousands of clocks.
+        const bool second = key0 + 64 <= pos_max;   // a row of the warp sees keys there
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int half = 0; half < (second ? 2 : 1); ++half) {
+          scores(half);
           float m8[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) m8[k] = fmaxf(s[k], s[8 + k]);
@@ -465,25 +379,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           for (int j = 16; j < 64; j += 16)
 #pragma unroll
             for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], s[j + k], s[j + 8 + k]);
-          return fmaxf(fmax3(m8[0], m8[1], m8[2]),
-                       fmax3(fmaxf(m8[3], m8[4]), fmaxf(m8[5], m8[6]), m8[7]));
-        };
-        // The second half's scores stay in registers while the maximum is
-        // settled; the first half's are read again after them (128 scores a
-        // thread would spill).  P takes the columns of the second half, so
-        // what is still to be read is not overwritten.
-        const bool second = key0 + 64 <= pos_max;   // a row of the warp sees keys there
-        float s[64];
-        scores(0, s);
-        float mx = maximum(s);
-        if (second) {
-          scores(1, s);
-          mx = fmaxf(mx, maximum(s));
+          mx = fmax3(mx, fmax3(m8[0], m8[1], m8[2]),
+                     fmax3(fmaxf(m8[3], m8[4]), fmaxf(m8[5], m8[6]), m8[7]));
         }
-        mx *= qmul;
         // The running maximum only moves when a score passes it by more than
         // 2^8, and only then is O rescaled: weights stay below 2^8, and the
         // stale maximum cancels in O / l.
+        mx *= qmul;
         const bool moved = mx > m_run + kPaRescaleLog2;
         const float corr = moved ? softmax_exp2(m_run - mx) : 1.f;   // 0 on the first chunk
         l_run *= corr;
@@ -503,9 +405,23 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           }
           tc_fence_before();
         }
-        // weights, as 16-bit pairs
+        if (!C::kTurnFirst && !my_turn()) break;
+        // weights, as 16-bit pairs, the second half's first
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        auto weights = [&](int half) {
+        if (!second) {
+          if (mine.kend - key0 > 64) {   // another warp's rows see keys there
+            float zero[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) zero[j] = 0.f;
+            tmem_st32(t_s + kPaTmemP + 32, zero);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[t][1]);
+        }
+#pragma unroll 1
+        for (int half = second ? 1 : 0; half >= 0; --half) {
+          if (second && half == 0) scores(0);
           float w[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -516,44 +432,290 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             w[j] = __uint_as_float(Mma<T>::pack(p0, p1));
           }
           tmem_st32(t_s + kPaTmemP + 32 * half, w);
-        };
-        if (second) {
-          weights(1);
-          scores(0, s);
-        } else {
-          float zero[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) zero[j] = 0.f;
-          tmem_st32(t_s + kPaTmemP + 32, zero);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[t][half]);
         }
-        weights(0);
         l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
+        if (c < both) {
+          if (lane == 0) mbar_arrive(&turn[t]);
+          ++turns;
+        }
       }
+      if (!ok) break;
+      have = take(m, next);   // while the last product runs
       if (!ok) break;
       // ---- O / l
       ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
       if (!ok) break;
       tc_fence_after();
-      T* dst = static_cast<T*>(a.out) + (int64_t)(it.q0 + my_pos) * a.out_stride +
-               (int64_t)(it.kvh * G + (first_row + trow) % G) * D;
+      // Through shared memory in the copies' swizzled layout.  A warp whose 32
+      // rows all belong to the prompt hands them to a tensor copy, which runs
+      // on while the next item begins; at a prompt's end 8 lanes write 128
+      // bytes of a row (rows past it belong to others).
       const float inv = 1.f / l_run;
+      const bool whole = warp_row + 32 <= mine.rows;
+      T* dst = static_cast<T*>(a.out) + (int64_t)it.q0 * a.out_stride + (int64_t)it.kvh * G * D;
 #pragma unroll 1
-      for (int col = 0; col < D; col += 32) {
-        float o[32];
-        tmem_ld32(t_o + col, o);   // warp-wide: every lane
-        if (trow >= mine.rows) continue;
+      for (int col = 0; col < D; col += 64) {
+        float o[64];
+        tmem_ld64(t_o + col, o);
+        if (lane == 0) bulk_store_wait_read();   // the staging rows' last copy has read them
+        __syncwarp();
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch)
-          *reinterpret_cast<uint4*>(dst + col + ch * 8) =
+        for (int ch = 0; ch < 8; ++ch)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((ch ^ (lane & 7)) << 4)) =
               make_uint4(Mma<T>::pack(o[ch * 8] * inv, o[ch * 8 + 1] * inv),
                          Mma<T>::pack(o[ch * 8 + 2] * inv, o[ch * 8 + 3] * inv),
                          Mma<T>::pack(o[ch * 8 + 4] * inv, o[ch * 8 + 5] * inv),
                          Mma<T>::pack(o[ch * 8 + 6] * inv, o[ch * 8 + 7] * inv));
+        if (whole) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0)
+            tma_store_box3(&tm_o, col, it.kvh * G, it.q0 + (first_row + warp_row) / G,
+                           smem_addr(stage));
+        } else {
+          __syncwarp();
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3), ch = lane & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+            const int row = first_row + warp_row + r;
+            if (warp_row + r < mine.rows)
+              *reinterpret_cast<uint4*>(dst + (int64_t)(row / G) * a.out_stride + (row % G) * D +
+                                        col + ch * 8) = v;
+          }
+          __syncwarp();
+        }
       }
       tc_fence_before();   // O is read before the next item's products (p_full orders them)
+    }
+    if (lane == 0) bulk_store_wait_read();   // before the CTA's shared memory goes
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaOtherRegs));
+    if (warp == 8) {
+      // ================================================================ Q and K copies
+      uint32_t kc = 0;                      // chunks so far
+      uint32_t q_count[kPaTiles] = {0, 0};   // Q tiles asked for so far
+      for (uint32_t m = 0; ok && take(m, it); ++m) {
+        const PaTile t0 = pa_tile(it, G, 0), t1 = pa_tile(it, G, 1);
+        const int chunks = max(t0.chunks, t1.chunks);
+        for (int c = 0; c < chunks && ok; ++c, ++kc) {
+          const int st = kc % SK;
+          if (kc >= SK) ok = pa_wait(&k_free[st], ((kc / SK) - 1) & 1, gave_up);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&k_full[st], C::kKvBytes);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_box(sK + st * C::kKvBytes + h * (kPaKeys * 128), &tm_k, it.kvh * D + h * 64,
+                           it.q0 + c * kPaKeys, &k_full[st]);
+          }
+          __syncwarp();
+          if (c > 0) continue;
+          // the Q tiles, after the first chunk is on its way
+          for (int t = 0; t < kPaTiles && ok; ++t) {
+            if (m > 0) ok = pa_wait(&q_free[t], (m - 1) & 1, gave_up);
+            if (!ok) break;
+            ++q_count[t];
+            if (lane != 0) continue;
+            if ((t == 0 ? t0.rows : t1.rows) == 0) {
+              mbar_arrive(&q_full[t]);
+              continue;
+            }
+            mbar_arrive_expect_tx(&q_full[t], C::kQBytes);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_box3(sQ + t * C::kQBytes + h * (kPaRows * 128), &tm_q, h * 64, it.kvh * G,
+                            it.q0 + (it.row0 + t * kPaRows) / G, &q_full[t]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) {
+        // what is in flight lands before the CTA ends
+        for (uint32_t c = kc > SK ? kc - SK : 0; c < kc; ++c)
+          (void)mbar_wait_bounded(&k_full[c % SK], (c / SK) & 1);
+        for (int t = 0; t < kPaTiles; ++t)
+          if (q_count[t] > 0) (void)mbar_wait_bounded(&q_full[t], (q_count[t] - 1) & 1);
+      }
+    } else if (warp == 9) {
+      // ================================================================ V copies
+      uint32_t vc = 0, tails = 0;
+      for (uint32_t m = 0; ok && take(m, it); ++m) {
+        const PaTile t0 = pa_tile(it, G, 0), t1 = pa_tile(it, G, 1);
+        const int chunks = max(t0.chunks, t1.chunks), kend = max(t0.kend, t1.kend);
+        for (int c = 0; c < chunks && ok; ++c, ++vc) {
+          const int st = vc % SV;
+          if (vc >= SV) ok = pa_wait(&v_free[st], ((vc / SV) - 1) & 1, gave_up);
+          if (!ok) break;
+          // The products read whole groups of 16 keys.  Rows past the last key
+          // meet zero weights, but 0 x NaN would not vanish: the last chunk
+          // lands on a barrier of its own and its group is filled up with zeros
+          // before the stage is handed over.
+          const int valid = min(kPaKeys, kend - c * kPaKeys);
+          const bool fill = valid % 16 != 0;
+          uint64_t* land = fill ? &v_tail : &v_full[st];
+          if (lane == 0) {
+            mbar_arrive_expect_tx(land, C::kKvBytes);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_box(sV + st * C::kKvBytes + h * (kPaKeys * 128), &tm_v, it.kvh * D + h * 64,
+                           it.q0 + c * kPaKeys, land);
+          }
+          __syncwarp();
+          if (fill) {
+            ok = pa_wait(&v_tail, tails & 1, gave_up);
+            ++tails;
+            if (!ok) break;
+            unsigned char* rows = smem + C::kOffV + st * C::kKvBytes;
+            for (int i = lane; i < (16 - valid % 16) * (D / 8); i += 32) {
+              const int r = valid + i / (D / 8), ch = i % (D / 8);
+              *reinterpret_cast<uint4*>(rows + (ch >> 3) * (kPaKeys * 128) + r * 128 +
+                                        (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_full[st]);
+          }
+        }
+      }
+      if (!ok) {
+        for (uint32_t c = vc > SV ? vc - SV : 0; c < vc; ++c)
+          (void)mbar_wait_bounded(&v_full[c % SV], (c / SV) & 1);
+      }
+    } else if (warp == 14) {
+      // ================================================================ items
+      const int first = pa_tiles_of(a, G, lane);
+      const uint32_t N = gridDim.x;
+      for (uint32_t m = 0, run = 0;; ++m, run += N) {
+        const int slot = m % kPaItems;
+        if (m >= kPaItems) ok = pa_wait(&item_free[slot], ((m / kPaItems) - 1) & 1, gave_up);
+        if (!ok) break;
+        // one item from each run of N, forwards and backwards in turn
+        const bool found =
+            pa_locate(a, G, run + (m & 1 ? N - 1 - blockIdx.x : blockIdx.x), first, lane, it);
+        if (lane == 0) {
+          items[slot] = found ? make_int4(it.q0, it.n, it.kvh, it.row0) : make_int4(0, 0, 0, 0);
+          mbar_arrive(&item_full[slot]);
+        }
+        __syncwarp();
+        if (!found) break;
+      }
+    } else if (warp >= 10 && warp < 14) {
+      // ================================================================ products
+      // Per tile one warp issues S and one P V: an issuing warp is held up for
+      // hundreds of clocks by each of its commits, so the two streams are kept
+      // apart and commit nothing that another barrier already tells (the S warp,
+      // which waits for O of chunk c before S of chunk c + 1, hands chunk c's K
+      // and V stages back with plain arrivals).
+      const int t = (warp - 10) & 1;
+      const uint32_t t_s = tmem + t * kPaKeys, t_o = tmem + kPaTmemO + t * D;
+      // a descriptor's start address is address >> 4 in its low 14 bits; every
+      // operand lies below 256 KB, so offsets are added to the base's descriptor
+      uint32_t chunk0 = 0, done = 0;   // the item's first chunk; chunks of this tile so far
+      const bool leader = elect_one();
+      if (warp < 12) {
+        // with a negative scale the product is negated (A's sign bit of the
+        // descriptor), so that the maximum is always the largest score
+        const uint32_t id_s = f16_idesc<T>(kPaRows, kPaKeys) | (a.qscale < 0.f ? 1u << 13 : 0u);
+        const uint64_t q_desc = sw128_desc(sQ + t * C::kQBytes), k_desc = sw128_desc(sK);
+        uint32_t held = ~0u;           // the chunk whose V stage is to be handed back
+        for (uint32_t m = 0; ok && take(m, it); ++m) {
+          const PaTile mine = pa_tile(it, G, t), other = pa_tile(it, G, 1 - t);
+          const int chunks = max(mine.chunks, other.chunks);
+          ok = pa_wait(&q_full[t], m & 1, gave_up);
+          if (!ok) break;
+          if (mine.chunks == 0 && lane == 0) mbar_arrive(&q_free[t]);
+          for (int c = 0; c <= chunks; ++c) {
+            const uint32_t kc = chunk0 + c;
+            if (c < mine.chunks) ok = pa_wait(&k_full[kc % SK], (kc / SK) & 1, gave_up);
+            // P of the tile's last chunk is used: its stages, and S, are free
+            if (ok && done > 0 && c <= mine.chunks && (c < mine.chunks || c < chunks)) {
+              ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
+              if (ok && held != ~0u && lane == 0) mbar_arrive(&v_free[held % SV]);
+              held = ~0u;
+            }
+            if (!ok || c == chunks) break;
+            if (c < mine.chunks) {
+              tc_fence_after();
+              const uint64_t kb = k_desc + (uint64_t)(((kc % SK) * C::kKvBytes) >> 4);
+              if (leader) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t off = (kk >> 2) * (kPaKeys * 128) + (kk & 3) * 32;
+                  tc_mma(t_s, q_desc + (uint64_t)(off >> 4), kb + (uint64_t)(off >> 4), id_s,
+                         kk > 0);
+                }
+                tc_commit(&s_full[t]);
+                if (c + 1 == mine.chunks) tc_commit(&q_free[t]);
+              }
+              __syncwarp();
+              held = kc;
+              ++done;
+              ok = pa_wait(&s_full[t], (done - 1) & 1, gave_up);
+              if (!ok) break;
+              if (lane == 0) mbar_arrive(&k_free[kc % SK]);
+            } else {
+              // a chunk of the other tile only
+              ok = pa_wait(&k_full[kc % SK], (kc / SK) & 1, gave_up) &&
+                   pa_wait(&v_full[kc % SV], (kc / SV) & 1, gave_up);
+              if (!ok) break;
+              if (lane == 0) {
+                mbar_arrive(&k_free[kc % SK]);
+                mbar_arrive(&v_free[kc % SV]);
+              }
+            }
+          }
+          chunk0 = uniform(chunk0 + chunks);
+        }
+      } else {
+        const uint32_t id_o = f16_idesc<T>(kPaRows, D) | (1u << 16);   // B (V) MN-major
+        const uint64_t v_desc = pa_v_desc(sV);
+        for (uint32_t m = 0; ok && take(m, it); ++m) {
+          const PaTile mine = pa_tile(it, G, t), other = pa_tile(it, G, 1 - t);
+          for (int c = 0; c < mine.chunks; ++c, ++done) {
+            const uint32_t vc = chunk0 + c;
+            ok = pa_wait(&v_full[vc % SV], (vc / SV) & 1, gave_up);
+            const uint64_t vb = v_desc + (uint64_t)(((vc % SV) * C::kKvBytes) >> 4);
+            const int steps = (min(kPaKeys, mine.kend - c * kPaKeys) + 15) / 16;
+            auto product = [&](int kk, bool add) {
+              tc_mma_ts(t_o, t_s + kPaTmemP + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), id_o,
+                        add ? 1u : 0u);
+            };
+            // the second 64 keys' weights are ready first
+            ok = ok && pa_wait(&p_full[t][1], done & 1, gave_up);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              if (steps == 8) {
+#pragma unroll
+                for (int kk = 4; kk < 8; ++kk) product(kk, c > 0 || kk > 4);
+              } else {
+#pragma unroll 1
+                for (int kk = 4; kk < steps; ++kk) product(kk, c > 0 || kk > 4);
+              }
+            }
+            __syncwarp();
+            ok = pa_wait(&p_full[t][0], done & 1, gave_up);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              if (steps > 4) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) product(kk, true);
+              } else {
+#pragma unroll 1
+                for (int kk = 0; kk < steps; ++kk) product(kk, c > 0 || kk > 0);
+              }
+              tc_commit(&o_done[t]);
+            }
+            __syncwarp();
+          }
+          chunk0 = uniform(chunk0 + max(mine.chunks, other.chunks));
+        }
+      }
     }
   }
   if (!ok && lane == 0) raise_error(a.err, kErrTimeout);
@@ -582,7 +744,7 @@ cudaError_t launch_t(const PromptArgs& a, cudaStream_t stream) {
       a.dtype == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const cuuint64_t T_ = (cuuint64_t)a.num_tokens;
   const cuuint32_t G = (cuuint32_t)(a.Hq / a.Hkv);
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   // q as [token][head][element], a box of 128 / G tokens x G heads x 64 elements
   const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, T_};
   const cuuint64_t qs[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2};
@@ -597,10 +759,16 @@ cudaError_t launch_t(const PromptArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = encode_tensor_map(&tv, type, 2, a.v, kd, vs, kb, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
+  // out as q, a box of a warp's 32 rows
+  const cuuint64_t os[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.out_stride * 2};
+  const cuuint32_t ob[3] = {64, G, 32u / G};
+  e = encode_tensor_map(&to, type, 3, a.out, qd, os, ob, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
   // at most this many items exist
   const int64_t most = ((int64_t)a.num_tokens * (int)G / kPaItemRows + a.B) * a.Hkv;
+  if (most > INT32_MAX) return cudaErrorInvalidValue;
   const int grid = (int)std::min<int64_t>(a.num_sms, most);
-  return launch_pdl(kern, dim3(grid), dim3(kPaThreads), C::kSmem, stream, tq, tk, tv, a);
+  return launch_pdl(kern, dim3(grid), dim3(kPaThreads), C::kSmem, stream, tq, tk, tv, to, a);
 }
 
 }  // namespace
