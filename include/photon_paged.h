@@ -333,7 +333,9 @@ size_t photon_paged_decode_int4_workspace_size(const photon_paged_shape_t* shape
  * an fp16 rounding plus its fp16 residual.  The batch's blocks are cut into
  * equal runs, one per resident warp, so partition_size is ignored.  Layouts of
  * q, out, tables and lengths, errors and workspace rules as
- * photon_paged_decode. */
+ * photon_paged_decode; num_seqs * num_kv_heads * (max_blocks_per_seq + 16) must
+ * stay below 2^30 and num_blocks * num_kv_heads below 2^31
+ * (PHOTON_ERR_UNSUPPORTED). */
 photon_status_t photon_paged_decode_int4(const void* q, const void* k_cache, const void* v_cache,
                                          const int32_t* block_tables,
                                          const int32_t* context_lens, float scale, void* out,

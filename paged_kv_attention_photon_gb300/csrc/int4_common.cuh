@@ -34,7 +34,7 @@ struct CacheWriteInt4Args {
   void* k_cache;
   void* v_cache;
   uint32_t* err;
-  int T, Hkv, D, NB, dtype;
+  int T, Hkv, D, NB, dtype, num_sms;
 };
 cudaError_t launch_cache_write_int4(const CacheWriteInt4Args& a, cudaStream_t stream);
 
@@ -57,18 +57,20 @@ struct DecodeInt4Args {
   const int32_t* block_tables;
   const int32_t* context_lens;
   void* out;
-  int2* ws_pair;   // [B][Hkv] first partial slot and number of partials
+  int2* ws_pair;   // [B][Hkv] first partial slot (the next is `team` on) and number of partials
   float2* ws_ml;   // [slot][G] running max (log2 domain) and sum of weights
   float* ws_o;     // [slot][G][D] unnormalised weighted V sum
   uint32_t* err;
   float qscale;    // scale * log2(e): scores are kept in the log2 domain
   int B, Hq, Hkv, D, NB, MBS, dtype;
   int num_sms, max_warps;
+  int team;        // warps that walk the same blocks, one KV head each: 8, 4, 2 or 1
   cudaEvent_t ev_start, ev_stop;   // optional timing hook around the kernels
 };
 cudaError_t launch_paged_decode_int4(const DecodeInt4Args& a, cudaStream_t stream);
 // Most warps the decode's attention grid has (the partials' slots are counted
 // from it, so the workspace does not depend on the device).
-constexpr int kInt4MaxWarps = 152 * 20;
+constexpr int kInt4MaxWarps = 152 * 16;
+constexpr int kInt4CtaWarps = 8;
 
 }  // namespace photon

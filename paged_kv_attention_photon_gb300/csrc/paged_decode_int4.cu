@@ -25,13 +25,17 @@
 // movmatrix; p_j step_j enters as its fp16 rounding plus the residual: for
 // G <= 4 the residual rides in the unused columns 4 .. 7 of the same product.
 //
-// Work: the batch's (sequence, KV head, block) triples in that order are one
-// line of units of 16 keys, cut into equal runs, one per warp; a warp has its
-// own ring of cp.async stages and no barrier with any other warp.  A run may
-// span several (sequence, KV head) pairs; a pair that lies in one run is
-// written out directly, the others leave (m, l, o) partials, merged by a
-// second kernel.  Every warp gets the same number of units whatever the mix of
-// lengths, without a queue or atomics, so results do not depend on timing.
+// Work: a team of up to 8 neighbouring warps takes as many neighbouring KV
+// heads, a warp each, through the same blocks, so that what it reads of a block
+// is contiguous in the pool: 8 records are 8.7 KB, one is 1088 bytes.  The
+// batch's (sequence, head group, block) triples in that order are one line,
+// cut into equal runs, one per team; each (sequence, head group) counts
+// kI4PairCost blocks more than it has, for what beginning and ending it costs.
+// A warp has its own ring of cp.async stages and no barrier with any other
+// warp.  A pair that lies in one run is written out directly, the others leave
+// (m, l, o) partials, merged by a second kernel.  Runs are equal whatever the
+// mix of lengths, without a queue or atomics, so results do not depend on
+// timing.
 #include <math.h>
 
 #include <algorithm>
@@ -41,20 +45,28 @@
 namespace photon {
 namespace {
 
-constexpr int kI4Warps = 4;               // warps per CTA
+constexpr int kI4Warps = kInt4CtaWarps;   // warps per CTA
 constexpr int kI4Threads = 32 * kI4Warps;
-constexpr int kI4MinUnits = 4;            // shortest run of a warp, in units
+// What beginning and ending a pair (its q rows, the sums over the warp, the
+// output or a partial) costs a warp, in blocks of keys.  Batch-256 mix with 2,
+// 3, 5, 8: 83, 78, 70, 69 us; 64 long contexts 40.1, 37.7, 37.7, 38.6 us.
+constexpr int kI4PairCost = 6;
+// Shortest run of a team on the line (4 contexts of up to 2048 tokens: 6 and
+// 8: 9.0 and 9.6 us).
+constexpr int kI4MinRun = 6;
 // Running maximum before the first key: below the scores, and finite, so that
 // no exponent is inf - inf.
 constexpr float kI4NoMax = -3e38f;
+constexpr int kI4StageUnits = 2;          // consecutive blocks of a pair in a stage
 
 template <int D>
 struct I4Cfg {
   static constexpr int kRec = int4_record_bytes(D);
   static constexpr int kUnit = 2 * kRec;                 // K record, V record
-  static constexpr int kStages = D == 128 ? 6 : 8;
-  static constexpr int kCtas = D == 128 ? 4 : 5;          // per SM
-  static constexpr int kSmem = kI4Warps * kStages * kUnit;
+  static constexpr int kStageBytes = kI4StageUnits * kUnit;
+  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kCtas = 2;                        // per SM (registers)
+  static constexpr int kSmem = kI4Warps * kStages * kStageBytes;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -67,15 +79,24 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// A raise of the exponent is exact: 2^(e - 127) from a biased exponent.
+// First product of a sum: D = A B.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// 2^(e - 127) from a biased exponent.
 __device__ __forceinline__ float pow2_biased(int e) {
   return __uint_as_float((uint32_t)min(max(e, 1), 254) << 23);
 }
 
-// A warp's place on the line of units: unit `blk` of KV head kvh of sequence b,
-// whose context has n blocks.
+// A team's place on the line: block `blk` of head group hg of sequence b, whose
+// context has n blocks; block 0 is at `first` on the line.
 struct I4Cursor {
-  int b, kvh, blk, n, ctx;
+  int b, hg, blk, n, ctx, first;
 };
 
 template <typename T, int D, bool kFull>
@@ -84,38 +105,54 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
   using C = I4Cfg<D>;
   constexpr int NW = D / 32;        // code words of a lane per row (or row pair)
   extern __shared__ __align__(16) unsigned char i4_smem[];
-  __shared__ long long pre[kI4Threads];      // units before a thread's sequences
-  __shared__ long long warp_sum[kI4Warps];
+  __shared__ int pre[kI4Threads];      // where a thread's sequences begin on the line
+  __shared__ int ctx_first[kI4Threads];   // the lengths, when a thread has one sequence
+  __shared__ int warp_sum[kI4Warps];
 
-  pdl_launch_dependents();
+  {
+    // while the kernel before runs out: the lengths, tables and q rows, spread
+    // over the CTAs, into L2, a line a thread (hints; what that kernel still
+    // writes is read after the wait)
+    const size_t line = (size_t)blockIdx.x * kI4Threads + threadIdx.x, at = line * 128;
+    if (at < (size_t)a.B * 4) prefetch_l2(reinterpret_cast<const char*>(a.context_lens) + at);
+    if (at < (size_t)a.B * a.MBS * 4) prefetch_l2(reinterpret_cast<const char*>(a.block_tables) + at);
+    if (at < (size_t)a.B * a.Hq * D * 2) prefetch_l2(static_cast<const char*>(a.q) + at);
+  }
   pdl_wait_primary();
+  pdl_launch_dependents();   // after the wait: the merge kernel reads the lengths ahead of its own
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int G = a.Hq / a.Hkv;
   const int span = a.MBS * kBlockSize;
-  auto ctx_of = [&](int b) -> int {
-    const int c = __ldg(a.context_lens + b);
-    return c > 0 && c <= span ? c : 0;   // the merge kernel flags rejected lengths
-  };
-  auto blocks_of = [](int ctx) -> int { return (ctx + kBlockSize - 1) / kBlockSize; };
-
-  // ---- the line of units: thread i sums sequences [i c, (i + 1) c)
+  // the contexts' lengths; the merge kernel flags rejected ones
   const int per_thread = (a.B + kI4Threads - 1) / kI4Threads;
-  long long mine = 0;
+  auto load_ctx = [&](int b) -> int {
+    const int c = __ldg(a.context_lens + b);
+    return c > 0 && c <= span ? c : 0;
+  };
+  auto ctx_of = [&](int b) -> int { return per_thread == 1 ? ctx_first[b] : load_ctx(b); };
+  auto blocks_of = [](int ctx) -> int { return (ctx + kBlockSize - 1) / kBlockSize; };
+  auto pair_len = [](int blocks) -> int { return blocks ? blocks + kI4PairCost : 0; };
+
+  // ---- the line: thread i sums sequences [i c, (i + 1) c)
+  int mine = 0;
   for (int i = 0; i < per_thread; ++i) {
     const int b = tid * per_thread + i;
-    if (b < a.B) mine += blocks_of(ctx_of(b));
+    const int ctx = b < a.B ? load_ctx(b) : 0;
+    if (i == 0) ctx_first[tid] = ctx;
+    mine += pair_len(blocks_of(ctx));
   }
-  mine *= a.Hkv;
-  long long incl = mine;
+  const int groups = a.Hkv / a.team;   // head groups
+  mine *= groups;
+  int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  long long before = 0, total = 0;
+  int before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kI4Warps; ++w) {
     if (w < warp) before += warp_sum[w];
@@ -123,43 +160,49 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
   }
   pre[tid] = before + incl - mine;
   __syncthreads();
-  const long long W = (long long)gridDim.x * kI4Warps;
-  long long per = (total + W - 1) / W;
-  if (per < kI4MinUnits) per = kI4MinUnits;
-  const long long w_id = (long long)blockIdx.x * kI4Warps + warp;
-  const long long u0 = w_id * per;
-  if (u0 >= total) return;
-  int count = (int)(u0 + per <= total ? per : total - u0);
+  const int teams = (int)gridDim.x * kI4Warps / a.team;
+  const int per = max((total + teams - 1) / teams, kI4MinRun);
+  const int w_id = (int)blockIdx.x * kI4Warps + warp;
+  const int team = w_id / a.team, member = w_id - team * a.team;
+  if (total == 0 || team > (total - 1) / per) return;
+  const int run_begin = team * per, run_end = min(run_begin + per, total);
 
-  // ---- the run's first unit: the last thread whose sequences begin at or
+  // ---- the run's first pair: the last thread whose sequences begin at or
   // before it, then a walk over that thread's sequences
   I4Cursor cur;
   {
     int owner = 0;
 #pragma unroll
     for (int i = 0; i < kI4Warps; ++i) {
-      const unsigned at = __ballot_sync(0xffffffffu, pre[i * 32 + lane] <= u0);
+      const unsigned at = __ballot_sync(0xffffffffu, pre[i * 32 + lane] <= run_begin);
       if (at) owner = i * 32 + 31 - __clz(at);
     }
-    long long left = u0 - pre[owner];
+    int left = run_begin - pre[owner];
     cur.b = owner * per_thread;
-    while (true) {   // ends inside the owner's sequences: u0 < total
+    while (true) {   // ends inside the owner's sequences: run_begin < total
       cur.ctx = ctx_of(cur.b);
       cur.n = blocks_of(cur.ctx);
-      const long long units = (long long)cur.n * a.Hkv;
-      if (left < units || cur.b + 1 >= a.B) break;
-      left -= units;
+      const int len = pair_len(cur.n) * groups;
+      if (left < len || cur.b + 1 >= a.B) break;
+      left -= len;
       ++cur.b;
     }
-    cur.kvh = (int)(left / cur.n);
-    cur.blk = (int)(left - (long long)cur.kvh * cur.n);
+    const int len = pair_len(cur.n);
+    cur.hg = left / len;
+    left -= cur.hg * len;
+    cur.first = run_begin - left + kI4PairCost;
+    cur.blk = max(0, left - kI4PairCost);
   }
-  // to the next unit; past the last sequence the cursor stays (no unit is left)
-  auto advance = [&](I4Cursor& c) {
-    if (++c.blk < c.n) return;
+  // blocks of the cursor's pair that are still in the run
+  auto blocks_left = [&](const I4Cursor& c) -> int {
+    return min(c.n, run_end - c.first) - c.blk;
+  };
+  // to the next pair; past the last sequence there is none
+  auto next_pair = [&](I4Cursor& c) {
     c.blk = 0;
-    if (++c.kvh < a.Hkv) return;
-    c.kvh = 0;
+    c.first += c.n + kI4PairCost;
+    if (++c.hg < groups) return;
+    c.hg = 0;
     do {
       if (++c.b >= a.B) {
         c.n = 0;
@@ -169,46 +212,75 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
       c.n = blocks_of(c.ctx);
     } while (c.n == 0);
   };
+  // the run may begin or end in what a pair costs beside its blocks
+  if (blocks_left(cur) <= 0) return;
 
-  // ---- the ring
-  unsigned char* ring = i4_smem + warp * (C::kStages * C::kUnit);
-  const uint32_t ring_addr = smem_addr(ring);
-  const unsigned char* kpool = static_cast<const unsigned char*>(a.k_cache);
-  const unsigned char* vpool = static_cast<const unsigned char*>(a.v_cache);
+  // ---- the ring: a stage takes up to two consecutive blocks of one pair
+  unsigned char* ring = i4_smem + warp * (C::kStages * C::kStageBytes);
+  const uint32_t ring_addr = smem_addr(ring) + 16 * lane;
+  // this lane's places in a record's codes, and in the pairs of a K record
+  // (lanes 0 .. 3) and a V record (4 .. 7)
+  const unsigned char* k_codes = static_cast<const unsigned char*>(a.k_cache) + 16 * lane;
+  const unsigned char* v_codes = static_cast<const unsigned char*>(a.v_cache) + 16 * lane;
+  const unsigned char* pairs = (lane < 4 ? k_codes : v_codes - 64) + 8 * D;
+  const uint32_t pairs_to = lane < 4 ? 8 * D : C::kRec + 8 * D - 64;
+  // The next 32 stages' records, one stage a lane: record numbers of its two
+  // blocks; kGone for a block that is not in the pool, kNone for no block.
   I4Cursor fetch = cur;
-  int to_fetch = count, table = -1, table_b = -1, table_at = -1;
-  uint32_t absent = 0;   // bit s: the block in stage s is not in the pool
+  int stages_found = 0, issued = 0;
+  bool more = true;   // blocks of the run are left to find
+  constexpr uint32_t kGone = 0xfffffffeu, kNone = 0xffffffffu;
+  uint32_t rec0 = kNone, rec1 = kNone;
+  auto find = [&]() {
+    int have = 0;
+    rec0 = rec1 = kNone;
+    while (have < 32 && more) {
+      const int units = blocks_left(fetch);
+      const int i = kI4StageUnits * (lane - have);
+      const int32_t* entry = a.block_tables + (size_t)fetch.b * a.MBS + fetch.blk + i;
+      const int kvh = fetch.hg * a.team + member;
+      if (i >= 0 && i < units) {
+        const int p0 = __ldg(entry), p1 = i + 1 < units ? __ldg(entry + 1) : 0;
+        rec0 = (unsigned)p0 < (unsigned)a.NB ? (uint32_t)(p0 * a.Hkv + kvh) : kGone;
+        if (i + 1 < units)
+          rec1 = (unsigned)p1 < (unsigned)a.NB ? (uint32_t)(p1 * a.Hkv + kvh) : kGone;
+        if (rec0 == kGone || rec1 == kGone) raise_error(a.err, kErrBlock);
+      }
+      const int taken = min(units, kI4StageUnits * (32 - have));
+      have += (taken + kI4StageUnits - 1) / kI4StageUnits;
+      fetch.blk += taken;
+      if (taken == units) {
+        next_pair(fetch);
+        more = fetch.n > 0 && blocks_left(fetch) > 0;
+      }
+    }
+    stages_found += have;
+  };
+  uint32_t absent = 0;   // bit 2 s + i: block i of stage s is not in the pool
   auto issue = [&](int s) {
-    if (to_fetch > 0) {
-      // lane i holds the table's entry for block table_at + i
-      const int at = fetch.blk & ~31;
-      if (table_b != fetch.b || table_at != at) {
-        table_b = fetch.b;
-        table_at = at;
-        table = at + lane < fetch.n ? __ldg(a.block_tables + (size_t)fetch.b * a.MBS + at + lane)
-                                    : -1;
-      }
-      const int phys = __shfl_sync(0xffffffffu, table, fetch.blk & 31);
-      if (phys >= 0 && phys < a.NB) {
-        const size_t off = ((size_t)phys * a.Hkv + fetch.kvh) * C::kRec;
-        const uint32_t dst = ring_addr + s * C::kUnit;
+    if ((issued & 31) == 0 && more) find();
+    if (issued < stages_found) {
+      const uint32_t dst = ring_addr + s * C::kStageBytes;
 #pragma unroll
-        for (int i = 0; i < 8 * D; i += 512) {
-          const int o = i + 16 * lane;
-          cp_async16(dst + o, kpool + off + o);
-          cp_async16(dst + C::kRec + o, vpool + off + o);
+      for (int i = 0; i < kI4StageUnits; ++i) {
+        const uint32_t rec = __shfl_sync(0xffffffffu, i ? rec1 : rec0, issued & 31);
+        const uint32_t bit = 1u << (2 * s + i);
+        if (rec < kGone) {
+          const size_t off = (size_t)rec * C::kRec;
+          const unsigned char* kp = k_codes + off;
+          const unsigned char* vp = v_codes + off;
+#pragma unroll
+          for (int o = 0; o < 8 * D; o += 512) {
+            cp_async16(dst + i * C::kUnit + o, kp + o);
+            cp_async16(dst + i * C::kUnit + C::kRec + o, vp + o);
+          }
+          if (lane < 8) cp_async16(dst + i * C::kUnit + pairs_to, pairs + off);
+          absent &= ~bit;
+        } else {
+          absent |= bit;
         }
-        if (lane < 8) {   // the 64 bytes of pairs of each
-          const int o = 8 * D + 16 * (lane & 3);
-          cp_async16(dst + (lane < 4 ? 0 : C::kRec) + o, (lane < 4 ? kpool : vpool) + off + o);
-        }
-        absent &= ~(1u << s);
-      } else {
-        if (lane == 0) raise_error(a.err, kErrBlock);
-        absent |= 1u << s;
       }
-      --to_fetch;
-      advance(fetch);
+      ++issued;
     }
     cp_async_commit();
   };
@@ -218,8 +290,9 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
   // ---- a pair's state.  Columns (slots) 2t and 2t + 1 of the score fragment
   // are this lane's; with G <= 4 column 4 + s repeats slot s.
   uint32_t bq[NW][2][2];   // Q^T fragments: column g, products 2j and 2j + 1 of word j
-  float c1[2], c2[2];      // score = step (acc c1) + lo c2
+  float c1[2], c2[2];      // score = (step acc + lo c2) c1, c1 > 0
   float m[2], l[2], z[2];  // running max, sum of weights, sum of weights x lo of V
+  float limit[2];          // (m + 8) / c1: what a score / c1 may reach before m moves
   float o[NW][2][4];       // O^T: dims (D / 8) g + 4j + 2h (rows g) and + 1 (rows g + 8)
   float vs = 0.f;          // power of two that the V steps are brought near 1 with
   auto begin_pair = [&]() {
@@ -229,7 +302,7 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
     for (int i = 0; i < NW * 8; ++i) x[i] = 0.f;
     if (s < G) {
       const T* row = static_cast<const T*>(a.q) +
-                     ((size_t)cur.b * a.Hq + (size_t)cur.kvh * G + s) * D + (D / 4) * t;
+                     ((size_t)cur.b * a.Hq + (size_t)(cur.hg * a.team + member) * G + s) * D + (D / 4) * t;
 #pragma unroll
       for (int i = 0; i < NW; ++i) Elem<T>::widen(__ldg(reinterpret_cast<const uint4*>(row) + i), x + 8 * i);
     }
@@ -247,7 +320,10 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
     // the row is scaled by a power of two to [2^14, 2^15): fp16 then holds
     // every fp16 or bf16 q, and its 16th, to 2^-25 of that
     const int ex = (int)((__float_as_uint(big) >> 23) & 255u);
-    const float sc = pow2_biased(268 - ex);   // 2^(14 - (ex - 127))
+    const float up = pow2_biased(268 - ex);   // 2^(14 - (ex - 127))
+    // with a negative scale q is turned round, so that the largest score is
+    // the largest sum; a zero scale is a tiny one (every weight is 1)
+    const float sc = a.qscale < 0.f ? -up : up;
     const float s16 = sc * 0.0625f;
 #pragma unroll
     for (int j = 0; j < NW; ++j)
@@ -257,14 +333,16 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
         bq[j][h][0] = Mma<__half>::pack(w[0] * sc, w[4] * sc);
         bq[j][h][1] = Mma<__half>::pack(w[1] * s16, w[5] * s16);
       }
-    // 2^24 of the codes; 1 / sc is exact
-    const float k1 = a.qscale * (16777216.f * (1.f / sc)), k2 = a.qscale * sum;
+    // acc = 2^-24 sc (q . n), so lo enters as lo sum(q) 2^-24 sc; 1 / up is exact
+    const float k1 = fmaxf(fabsf(a.qscale), 1e-37f) * (16777216.f * (1.f / up));
+    const float k2 = sum * (sc * 5.9604645e-8f);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int col = 2 * t + i;
       c1[i] = __shfl_sync(0xffffffffu, k1, (kFull ? col : col & 3) * 4);
       c2[i] = __shfl_sync(0xffffffffu, k2, (kFull ? col : col & 3) * 4);
       m[i] = kI4NoMax;
+      limit[i] = -INFINITY;
       l[i] = z[i] = 0.f;
     }
 #pragma unroll
@@ -286,48 +364,70 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
     }
   };
 
-  auto attend = [&](const unsigned char* kr, int valid) {
-    const unsigned char* vr = kr + C::kRec;
-    // K: rows g and g + 8
-    uint32_t k0[NW], k8[NW];
-    words(kr + g * (D / 2) + t * (D / 8), k0);
-    words(kr + (g + 8) * (D / 2) + t * (D / 8), k8);
-    const uint32_t kp0 = *reinterpret_cast<const uint32_t*>(kr + 8 * D + 4 * g);
-    const uint32_t kp8 = *reinterpret_cast<const uint32_t*>(kr + 8 * D + 4 * g + 32);
-    const uint32_t vp0 = *reinterpret_cast<const uint32_t*>(vr + 8 * D + 4 * g);
-    const uint32_t vp8 = *reinterpret_cast<const uint32_t*>(vr + 8 * D + 4 * g + 32);
-    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+  // One stage: 32 keys, of which `keys` are in the context; bit i of `gone`:
+  // block i is not there (both only matter to the last stage of a pair, or
+  // with a bad table).
+  auto attend = [&](const unsigned char* st, int keys, uint32_t gone) {
+    float y[kI4StageUnits][4];   // score / c1 of keys g (0, 1) and g + 8 (2, 3), slots 2t, 2t + 1
+    float step0[kI4StageUnits], step8[kI4StageUnits], low0[kI4StageUnits], low8[kI4StageUnits];
 #pragma unroll
-    for (int j = 0; j < NW; ++j) {
-      const uint32_t x = k0[j], y = k8[j], x8 = x >> 8, y8 = y >> 8;
-      const uint32_t f0[4] = {x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u};
-      const uint32_t f1[4] = {x8 & 0x000f000fu, y8 & 0x000f000fu, x8 & 0x00f000f0u,
-                              y8 & 0x00f000f0u};
-      Mma<__half>::run(sa, f0, bq[j][0][0], bq[j][0][1]);
-      Mma<__half>::run(sb, f1, bq[j][1][0], bq[j][1][1]);
-    }
-    const bool ok0 = g < valid, ok8 = g + 8 < valid;
-    const float ks0 = Bits16<T>::to_f32(kp0 & 0xffffu), kl0 = Bits16<T>::to_f32(kp0 >> 16);
-    const float ks8 = Bits16<T>::to_f32(kp8 & 0xffffu), kl8 = Bits16<T>::to_f32(kp8 >> 16);
-    float x[4];
+    for (int u = 0; u < kI4StageUnits; ++u) {
+      const unsigned char* kr = st + u * C::kUnit;
+      uint32_t k0[NW], k8[NW];   // K: rows g and g + 8
+      words(kr + g * (D / 2) + t * (D / 8), k0);
+      words(kr + (g + 8) * (D / 2) + t * (D / 8), k8);
+      const uint32_t kp0 = *reinterpret_cast<const uint32_t*>(kr + 8 * D + 4 * g);
+      const uint32_t kp8 = *reinterpret_cast<const uint32_t*>(kr + 8 * D + 4 * g + 32);
+      const uint32_t vp0 = *reinterpret_cast<const uint32_t*>(kr + C::kRec + 8 * D + 4 * g);
+      const uint32_t vp8 = *reinterpret_cast<const uint32_t*>(kr + C::kRec + 8 * D + 4 * g + 32);
+      float acc[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float raw = fmaf(i < 2 ? ks0 : ks8, (sa[i] + sb[i]) * c1[i & 1],
-                             (i < 2 ? kl0 : kl8) * c2[i & 1]);
-      x[i] = (i < 2 ? ok0 : ok8) ? raw : -INFINITY;
+      for (int j = 0; j < NW; ++j) {
+        const uint32_t x = k0[j], w = k8[j], x8 = x >> 8, w8 = w >> 8;
+        const uint32_t f0[4] = {x & 0x000f000fu, w & 0x000f000fu, x & 0x00f000f0u,
+                                w & 0x00f000f0u};
+        const uint32_t f1[4] = {x8 & 0x000f000fu, w8 & 0x000f000fu, x8 & 0x00f000f0u,
+                                w8 & 0x00f000f0u};
+        if (j == 0)
+          mma_first(acc, f0, bq[j][0][0], bq[j][0][1]);
+        else
+          Mma<__half>::run(acc, f0, bq[j][0][0], bq[j][0][1]);
+        Mma<__half>::run(acc, f1, bq[j][1][0], bq[j][1][1]);
+      }
+      const float ks0 = Bits16<T>::to_f32(kp0 & 0xffffu), kl0 = Bits16<T>::to_f32(kp0 >> 16);
+      const float ks8 = Bits16<T>::to_f32(kp8 & 0xffffu), kl8 = Bits16<T>::to_f32(kp8 >> 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        y[u][i] = fmaf(i < 2 ? ks0 : ks8, acc[i], (i < 2 ? kl0 : kl8) * c2[i & 1]);
+      step0[u] = Bits16<T>::to_f32(vp0 & 0xffffu);
+      step8[u] = Bits16<T>::to_f32(vp8 & 0xffffu);
+      low0[u] = Bits16<T>::to_f32(vp0 >> 16);
+      low8[u] = Bits16<T>::to_f32(vp8 >> 16);
     }
-    const float vs0 = ok0 ? Bits16<T>::to_f32(vp0 & 0xffffu) : 0.f;
-    const float vs8 = ok8 ? Bits16<T>::to_f32(vp8 & 0xffffu) : 0.f;
-    const float vl0 = ok0 ? Bits16<T>::to_f32(vp0 >> 16) : 0.f;
-    const float vl8 = ok8 ? Bits16<T>::to_f32(vp8 >> 16) : 0.f;
+    if (keys < 16 * kI4StageUnits || gone) {
+      // what lies behind the context may hold anything
+#pragma unroll
+      for (int u = 0; u < kI4StageUnits; ++u) {
+        const int valid = (gone >> u) & 1u ? 0 : keys - 16 * u;
+        if (g >= valid) {
+          y[u][0] = y[u][1] = -INFINITY;
+          step0[u] = low0[u] = 0.f;
+        }
+        if (g + 8 >= valid) {
+          y[u][2] = y[u][3] = -INFINITY;
+          step8[u] = low8[u] = 0.f;
+        }
+      }
+    }
     // The maximum only moves when a score passes it by more than 2^8 (then
     // weights stay below 2^8), the V steps' power of two when a step passes
     // 8; what is summed so far is rescaled then.  Both cancel in O / l.
-    const bool over = fmaxf(x[0], x[2]) > m[0] + 8.f || fmaxf(x[1], x[3]) > m[1] + 8.f ||
-                      fmaxf(vs0, vs8) * vs > 8.f;
-    if (__any_sync(0xffffffffu, over)) {
-      float n0 = fmaxf(m[0], fmaxf(x[0], x[2])), n1 = fmaxf(m[1], fmaxf(x[1], x[3]));
-      float sm = fmaxf(vs0, vs8);
+    const float y0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
+    const float y1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
+    const float top = fmaxf(fmaxf(step0[0], step8[0]), fmaxf(step0[1], step8[1]));
+    if (__any_sync(0xffffffffu, y0 > limit[0] || y1 > limit[1] || top * vs > 8.f)) {
+      float n0 = fmaxf(m[0], y0 * c1[0]), n1 = fmaxf(m[1], y1 * c1[1]);
+      float sm = top;
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
@@ -344,6 +444,8 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
       }
       m[0] = n0;
       m[1] = n1;
+      limit[0] = (n0 + 8.f) / c1[0];
+      limit[1] = (n1 + 8.f) / c1[1];
       l[0] *= r0, z[0] *= r0;
       l[1] *= r1, z[1] *= r1;
 #pragma unroll
@@ -353,48 +455,59 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[j][h][i] *= (i & 1 ? r1 : r0) * up;
     }
-    float w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p = softmax_exp2(x[i] - m[i & 1]);   // 0 for masked rows
-      l[i & 1] += p;
-      z[i & 1] = fmaf(p, i < 2 ? vl0 : vl8, z[i & 1]);
-      w[i] = p * ((i < 2 ? vs0 : vs8) * vs);
-    }
-    const uint32_t h01 = Mma<__half>::pack(w[0], w[1]), h23 = Mma<__half>::pack(w[2], w[3]);
-    const float2 r01 = Mma<__half>::unpack(h01), r23 = Mma<__half>::unpack(h23);
-    const uint32_t e01 = Mma<__half>::pack(w[0] - r01.x, w[1] - r01.y);
-    const uint32_t e23 = Mma<__half>::pack(w[2] - r23.x, w[3] - r23.y);
-    // P^T fragments: the rounding, and its residual in columns 4 .. 7 (their
-    // scores repeat columns 0 .. 3) or, with eight slots, in a second product
-    const bool upper = !kFull && t >= 2;
-    const uint32_t b0 = movmatrix_trans(upper ? e01 : h01), b1 = movmatrix_trans(upper ? e23 : h23);
-    uint32_t d0 = 0u, d1 = 0u;
-    if constexpr (kFull) {
-      d0 = movmatrix_trans(e01);
-      d1 = movmatrix_trans(e23);
-    }
-    // V: row pairs t and t + 4
-    uint32_t v0[NW], v4[NW];
-    words(vr + t * D + g * (D / 8), v0);
-    words(vr + (t + 4) * D + g * (D / 8), v4);
+    for (int u = 0; u < kI4StageUnits; ++u) {
+      const unsigned char* vr = st + u * C::kUnit + C::kRec;
+      uint32_t v0[NW], v4[NW];   // V: row pairs t and t + 4
+      words(vr + t * D + g * (D / 8), v0);
+      words(vr + (t + 4) * D + g * (D / 8), v4);
+      float w[4];
 #pragma unroll
-    for (int j = 0; j < NW; ++j) {
-      const uint32_t p = v0[j], q = v4[j], p8 = p >> 8, q8 = q >> 8;
-      const uint32_t f0[4] = {p & 0x000f000fu, p & 0x00f000f0u, q & 0x000f000fu, q & 0x00f000f0u};
-      const uint32_t f1[4] = {p8 & 0x000f000fu, p8 & 0x00f000f0u, q8 & 0x000f000fu,
-                              q8 & 0x00f000f0u};
-      Mma<__half>::run(o[j][0], f0, b0, b1);
-      Mma<__half>::run(o[j][1], f1, b0, b1);
+      for (int i = 0; i < 4; ++i) {
+        const float p = softmax_exp2(fmaf(y[u][i], c1[i & 1], -m[i & 1]));   // 0 for masked rows
+        l[i & 1] += p;
+        z[i & 1] = fmaf(p, i < 2 ? low0[u] : low8[u], z[i & 1]);
+        w[i] = p * ((i < 2 ? step0[u] : step8[u]) * vs);
+      }
+      // P^T fragments: the fp16 rounding, and its residual in columns 4 .. 7
+      // (their scores repeat columns 0 .. 3) or, with eight slots, in a
+      // second product
+      uint32_t h01 = Mma<__half>::pack(w[0], w[1]), h23 = Mma<__half>::pack(w[2], w[3]);
+      const float2 r01 = Mma<__half>::unpack(h01), r23 = Mma<__half>::unpack(h23);
+      uint32_t b0, b1, d0 = 0u, d1 = 0u;
       if constexpr (kFull) {
-        Mma<__half>::run(o[j][0], f0, d0, d1);
-        Mma<__half>::run(o[j][1], f1, d0, d1);
+        b0 = movmatrix_trans(h01);
+        b1 = movmatrix_trans(h23);
+        d0 = movmatrix_trans(Mma<__half>::pack(w[0] - r01.x, w[1] - r01.y));
+        d1 = movmatrix_trans(Mma<__half>::pack(w[2] - r23.x, w[3] - r23.y));
+      } else {
+        const float rest = t >= 2 ? 1.f : 0.f;
+        b0 = movmatrix_trans(
+            Mma<__half>::pack(fmaf(-rest, r01.x, w[0]), fmaf(-rest, r01.y, w[1])));
+        b1 = movmatrix_trans(
+            Mma<__half>::pack(fmaf(-rest, r23.x, w[2]), fmaf(-rest, r23.y, w[3])));
+      }
+#pragma unroll
+      for (int j = 0; j < NW; ++j) {
+        // rows g: nibble 0 (2) alone; rows g + 8: it and the next one, n + 16 n',
+        // parted at the end: a mask less per word
+        const uint32_t p = v0[j], q = v4[j];
+        const uint32_t p8 = __byte_perm(p, 0u, 0x4341), q8 = __byte_perm(q, 0u, 0x4341);
+        const uint32_t f0[4] = {p & 0x000f000fu, p & 0x00ff00ffu, q & 0x000f000fu,
+                                q & 0x00ff00ffu};
+        const uint32_t f1[4] = {p8 & 0x000f000fu, p8, q8 & 0x000f000fu, q8};
+        Mma<__half>::run(o[j][0], f0, b0, b1);
+        Mma<__half>::run(o[j][1], f1, b0, b1);
+        if constexpr (kFull) {
+          Mma<__half>::run(o[j][0], f0, d0, d1);
+          Mma<__half>::run(o[j][1], f1, d0, d1);
+        }
       }
     }
   };
 
   // the pair's sums over the warp; then out, or a partial
-  auto end_pair = [&](long long pair_u0) {
+  auto end_pair = [&]() {
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
@@ -410,20 +523,32 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if constexpr (!kFull) o[j][h][i] += __shfl_xor_sync(0xffffffffu, o[j][h][i], 2);
-          o[j][h][i] = fmaf(o[j][h][i] * (i < 2 ? 16777216.f : 1048576.f), unscale, z[i & 1]);
         }
-    const int pair = cur.b * a.Hkv + cur.kvh;
-    const long long w_first = pair_u0 / per, w_last = (pair_u0 + cur.n - 1) / per;
-    if (w_id == w_first && lane == 0)
-      a.ws_pair[pair] = make_int2((int)w_first + pair, (int)(w_last - w_first) + 1);
+#pragma unroll
+    for (int j = 0; j < NW; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // rows g + 8 hold the even dim's sum and 16 times the odd one's
+          const float even = o[j][h][i], odd = o[j][h][2 + i] - even;
+          o[j][h][i] = fmaf(even * 16777216.f, unscale, z[i]);
+          o[j][h][2 + i] = fmaf(odd * 1048576.f, unscale, z[i]);
+        }
+    // the pair's partials: one for each team whose run touches it; along the
+    // line either the team or the pair moves on, so their sum numbers them
+    const int kvh = cur.hg * a.team + member, pair = cur.b * groups + cur.hg;
+    const int t_first = cur.first / per, t_last = (cur.first + cur.n - 1) / per;
+    if (team == t_first && lane == 0)
+      a.ws_pair[cur.b * a.Hkv + kvh] =
+          make_int2((t_first + pair) * a.team + member, t_last - t_first + 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int s = 2 * t + i;
       if (s >= G || (!kFull && t >= 2)) continue;
-      if (w_first == w_last) {
+      if (t_first == t_last) {
         const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
-        T* dst = static_cast<T*>(a.out) + ((size_t)cur.b * a.Hq + (size_t)cur.kvh * G + s) * D +
-                 (D / 8) * g;
+        T* dst = static_cast<T*>(a.out) + ((size_t)cur.b * a.Hq + (size_t)kvh * G + s) * D + (D / 8) * g;
 #pragma unroll
         for (int j = 0; j < NW; j += 2)
           *reinterpret_cast<uint4*>(dst + 4 * j) =
@@ -432,7 +557,7 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
                          Mma<T>::pack(o[j + 1][0][i] * inv, o[j + 1][0][2 + i] * inv),
                          Mma<T>::pack(o[j + 1][1][i] * inv, o[j + 1][1][2 + i] * inv));
       } else {
-        const size_t row = (size_t)(w_id + pair) * G + s;
+        const size_t row = ((size_t)(team + pair) * a.team + member) * G + s;
         if (g == 0) a.ws_ml[row] = make_float2(m[i], l[i]);
         float4* dst = reinterpret_cast<float4*>(a.ws_o + row * D + (D / 8) * g);
 #pragma unroll
@@ -442,53 +567,53 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
     }
   };
 
-  long long u = u0, pair_u0 = u0 - cur.blk;
   int stage = 0;
-  begin_pair();
-  for (; count > 0; --count, ++u) {
-    cp_async_wait<C::kStages - 2>();
-    __syncwarp();
-    const int left = cur.ctx - cur.blk * kBlockSize;
-    const int valid = (absent >> stage) & 1u ? 0 : min(left, kBlockSize);
-    attend(ring + stage * C::kUnit, valid);
-    __syncwarp();   // every lane has read the stage before it is filled again
-    const bool last = cur.blk + 1 == cur.n;
-    if (last || count == 1) {
-      end_pair(pair_u0);
-      if (count > 1) {
-        pair_u0 += cur.n;
-        advance(cur);
-        begin_pair();
-      }
-    } else {
-      ++cur.blk;
+  while (true) {   // pairs
+    begin_pair();
+    int units = blocks_left(cur);
+    int keys = min(cur.ctx - cur.blk * kBlockSize, units * kBlockSize);
+    for (; units > 0; units -= kI4StageUnits, keys -= kI4StageUnits * kBlockSize) {
+      cp_async_wait<C::kStages - 2>();
+      __syncwarp();
+      attend(ring + stage * C::kStageBytes, keys, (absent >> (2 * stage)) & 3u);
+      __syncwarp();   // every lane has read the stage before it is filled again
+      issue(stage == 0 ? C::kStages - 1 : stage - 1);
+      stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
-    issue(stage == 0 ? C::kStages - 1 : stage - 1);
-    stage = stage + 1 == C::kStages ? 0 : stage + 1;
+    end_pair();
+    next_pair(cur);
+    if (cur.n == 0 || blocks_left(cur) <= 0) break;
   }
   cp_async_wait<0>();
 }
 
-// One CTA per (sequence, q head): out = sum_p w_p o_p / sum_p w_p l_p with
-// w_p = 2^(m_p - max m) over the pair's partials, and the zero rows of empty
-// sequences.  A warp takes every fourth group of 8 partials, all loaded at
-// once, so up to 32 partials cost one round trip.
-constexpr int kI4MergeRows = 8;
+// out = sum_p w_p o_p / sum_p w_p l_p with w_p = 2^(m_p - max m) over the
+// partials of a (sequence, q head), and the zero rows of empty sequences.
+// kSplit warps take an item, each every kSplit-th group of 8 partials, loaded
+// at once.  4 when the items are few (their partials are then many: up to 32
+// cost one round trip), 1 when they fill the device (batch-256 mix, 8192
+// items, most of them written by the attention kernel).
+constexpr int kI4MergeRows = 8, kI4MergeWarps = 4;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kI4Threads) paged_decode_int4_merge_kernel(const DecodeInt4Args a) {
+template <typename T, int D, int kSplit>
+__global__ void __launch_bounds__(32 * kI4MergeWarps)
+    paged_decode_int4_merge_kernel(const DecodeInt4Args a) {
   constexpr int EPL = D / 32;
-  __shared__ float sm[kI4Warps], sl[kI4Warps], so[kI4Warps][D];
+  __shared__ float sm[kI4MergeWarps], sl[kI4MergeWarps], so[kSplit > 1 ? kI4MergeWarps : 1][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
+  const int part = warp % kSplit;
+  const int item = (int)blockIdx.x * (kI4MergeWarps / kSplit) + warp / kSplit;
+  if (item >= a.B * a.Hq) return;   // (kSplit == 1, or the whole CTA)
+  const int b = item / a.Hq, hq = item - b * a.Hq;
   const int G = a.Hq / a.Hkv;
   pdl_launch_dependents();
-  pdl_wait_primary();
+  // the attention kernel has passed its own wait: the lengths are there
   const int ctx = __ldg(a.context_lens + b);
-  T* out = static_cast<T*>(a.out) + (size_t)blockIdx.x * D;
+  pdl_wait_primary();
+  T* out = static_cast<T*>(a.out) + (size_t)item * D;
   if (ctx <= 0 || ctx > a.MBS * kBlockSize) {
-    if (ctx != 0 && threadIdx.x == 0 && hq == 0) raise_error(a.err, kErrContext);
-    if (threadIdx.x < D / 8) reinterpret_cast<uint4*>(out)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    if (ctx != 0 && lane == 0 && part == 0 && hq == 0) raise_error(a.err, kErrContext);
+    if (part == 0 && lane < D / 8) reinterpret_cast<uint4*>(out)[lane] = make_uint4(0, 0, 0, 0);
     return;
   }
   const int2 pr = a.ws_pair[b * a.Hkv + hq / G];
@@ -497,13 +622,13 @@ __global__ void __launch_bounds__(kI4Threads) paged_decode_int4_merge_kernel(con
   float M = kI4NoMax, L = 0.f, O[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) O[e] = 0.f;
-  for (int p0 = warp * kI4MergeRows; p0 < pr.y; p0 += kI4Warps * kI4MergeRows) {
+  for (int p0 = part * kI4MergeRows; p0 < pr.y; p0 += kSplit * kI4MergeRows) {
     float v[kI4MergeRows][EPL];
     float2 ml[kI4MergeRows];
 #pragma unroll
     for (int u = 0; u < kI4MergeRows; ++u) {
       const bool in = p0 + u < pr.y;
-      const size_t row = row0 + (size_t)(in ? p0 + u : p0) * G;
+      const size_t row = row0 + (size_t)(in ? p0 + u : p0) * G * a.team;
       ml[u] = a.ws_ml[row];
       if (!in) ml[u].y = 0.f;
 #pragma unroll
@@ -527,25 +652,32 @@ __global__ void __launch_bounds__(kI4Threads) paged_decode_int4_merge_kernel(con
       for (int e = 0; e < EPL; ++e) O[e] = fmaf(w, v[u][e], O[e]);
     }
   }
-  if (lane == 0) {
-    sm[warp] = M;
-    sl[warp] = L;
-  }
+  if constexpr (kSplit == 1) {
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) so[warp][lane * EPL + e] = O[e];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float mx = sm[0];
-#pragma unroll
-    for (int w = 1; w < kI4Warps; ++w) mx = fmaxf(mx, sm[w]);
-    float sum = 0.f, x = 0.f;
-#pragma unroll
-    for (int w = 0; w < kI4Warps; ++w) {
-      const float k = exp2f(sm[w] - mx);
-      sum = fmaf(k, sl[w], sum);
-      x = fmaf(k, so[w][threadIdx.x], x);
+    for (int e = 0; e < EPL; e += 2)
+      *reinterpret_cast<uint32_t*>(out + lane * EPL + e) = Mma<T>::pack(O[e] * inv, O[e + 1] * inv);
+  } else {
+    if (lane == 0) {
+      sm[warp] = M;
+      sl[warp] = L;
     }
-    out[threadIdx.x] = Elem<T>::narrow(sum > 0.f || sum != sum ? x / sum : 0.f);
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) so[warp][lane * EPL + e] = O[e];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float mx = sm[0];
+#pragma unroll
+      for (int w = 1; w < kI4MergeWarps; ++w) mx = fmaxf(mx, sm[w]);
+      float sum = 0.f, x = 0.f;
+#pragma unroll
+      for (int w = 0; w < kI4MergeWarps; ++w) {
+        const float k = exp2f(sm[w] - mx);
+        sum = fmaf(k, sl[w], sum);
+        x = fmaf(k, so[w][threadIdx.x], x);
+      }
+      out[threadIdx.x] = Elem<T>::narrow(sum > 0.f || sum != sum ? x / sum : 0.f);
+    }
   }
 }
 
@@ -572,8 +704,15 @@ cudaError_t launch_int4(const DecodeInt4Args& a, cudaStream_t stream) {
   if (a.ev_start) cudaEventRecord(a.ev_start, stream);
   e = launch_pdl(kern, dim3(grid), dim3(kI4Threads), C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_decode_int4_merge_kernel<T, D>, dim3(a.B * a.Hq), dim3(kI4Threads), 0,
-                 stream, a);
+  // from two items a resident warp on, a warp an item (batch-256 mix 62.9 against
+  // 67.8 us); 1024 items of 64 long contexts 36.8 against 34.4 us
+  const int items = a.B * a.Hq;
+  e = items >= 16 * a.num_sms
+          ? launch_pdl(paged_decode_int4_merge_kernel<T, D, 1>,
+                       dim3((items + kI4MergeWarps - 1) / kI4MergeWarps), dim3(32 * kI4MergeWarps),
+                       0, stream, a)
+          : launch_pdl(paged_decode_int4_merge_kernel<T, D, kI4MergeWarps>, dim3(items),
+                       dim3(32 * kI4MergeWarps), 0, stream, a);
   if (e != cudaSuccess) return e;
   if (a.ev_stop) cudaEventRecord(a.ev_stop, stream);
   return cudaSuccess;

@@ -623,9 +623,10 @@ Int4Layout int4_layout(const photon_paged_shape_t* s) {
   Int4Layout w{};
   const size_t pairs = (size_t)s->num_seqs * s->num_kv_heads;
   const size_t G = s->num_q_heads / s->num_kv_heads;
-  // warps that can have work at all, in whole CTAs of 4
+  // warps that can have work at all, in whole CTAs
   const size_t units = pairs * (size_t)s->max_blocks_per_seq;
-  w.max_warps = (int)std::min<size_t>(photon::kInt4MaxWarps, round_up(std::max<size_t>(units, 1), 4));
+  w.max_warps = (int)std::min<size_t>(photon::kInt4MaxWarps,
+                                      round_up(std::max<size_t>(units, 1), photon::kInt4CtaWarps));
   const size_t rows = (pairs + w.max_warps) * G;
   w.off_ml = round_up(pairs * sizeof(int2), 256);
   w.off_o = w.off_ml + round_up(rows * sizeof(float2), 256);
@@ -673,6 +674,7 @@ photon_status_t photon_cache_write_int4(const void* k, int64_t k_stride, const v
   a.D = shape->head_dim;
   a.NB = shape->num_blocks;
   a.dtype = shape->dtype;
+  if ((st = num_sms(&a.num_sms)) != PHOTON_OK) return st;
   return photon::launch_cache_write_int4(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PHOTON_OK
              : PHOTON_ERR_CUDA;
@@ -727,8 +729,12 @@ photon_status_t photon_paged_decode_int4(const void* q, const void* k_cache, con
   if (st != PHOTON_OK) return st;
   if (!std::isfinite(scale)) return PHOTON_ERR_INVALID_ARG;
   if (shape->num_seqs == 0) return PHOTON_OK;
-  // (sequence, head) pairs are numbered in 32 bits
-  if ((int64_t)shape->num_seqs * shape->num_q_heads > INT_MAX / 2) return PHOTON_ERR_UNSUPPORTED;
+  // (sequence, head) pairs, blocks of all contexts and records are numbered in 32 bits
+  if ((int64_t)shape->num_seqs * shape->num_q_heads > INT_MAX / 2 ||
+      (int64_t)shape->num_seqs * shape->num_kv_heads >
+          INT_MAX / 2 / ((int64_t)shape->max_blocks_per_seq + 16) ||
+      (int64_t)shape->num_blocks * shape->num_kv_heads > INT_MAX)
+    return PHOTON_ERR_UNSUPPORTED;
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out)
     return PHOTON_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(block_tables) ||
@@ -761,6 +767,8 @@ photon_status_t photon_paged_decode_int4(const void* q, const void* k_cache, con
   a.MBS = shape->max_blocks_per_seq;
   a.dtype = shape->dtype;
   a.max_warps = wl.max_warps;
+  a.team = photon::kInt4CtaWarps;
+  while (a.Hkv % a.team) a.team /= 2;
   a.ev_start = g_ev_start.load(std::memory_order_acquire);
   a.ev_stop = g_ev_stop.load(std::memory_order_acquire);
   if (!a.ev_start || !a.ev_stop) a.ev_start = a.ev_stop = nullptr;

@@ -18,14 +18,23 @@
 namespace photon {
 namespace {
 
-__device__ __forceinline__ void load8(const float* p, float* f) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+// 8 elements as they lie in memory, and widened.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
 }
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* f) {
-  Elem<T>::widen(*reinterpret_cast<const uint4*>(p), f);
+__device__ __forceinline__ void widen8(const Raw8<T>& r, float* f) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    Elem<T>::widen(r.v[i], f + i * Elem<T>::kPerChunk);
 }
 __device__ __forceinline__ void store8(float* p, const float* f) {
   *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
@@ -51,7 +60,7 @@ __device__ __forceinline__ float row_max(float x) {
   return x;
 }
 
-constexpr int kQkThreads = 256;
+constexpr int kQkThreads = 128;
 constexpr int kQkHeads = 3;   // head rows a lane takes, all loaded before the first is used
 
 template <typename T, int D, bool kOneAxis>
@@ -75,22 +84,19 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkNormRo
   const int e0 = turned ? 8 * j : 2 * a.half + 16 * (j - a.half / 8);
   const int e1 = turned ? a.half + 8 * j : e0 + 8;
 
-  float x[kQkHeads][16];
-  const T* src[kQkHeads];
+  Raw8<T> raw[kQkHeads][2];
+  const T* qrow = static_cast<const T*>(a.q) + t * a.q_stride;
+  const T* krow = static_cast<const T*>(a.k) + t * a.k_stride - (int64_t)a.Hq * D;
 #pragma unroll
   for (int i = 0; i < kQkHeads; ++i) {
-    const int h = h0 + i * kGroups;
-    const bool is_k = h >= a.Hq;
-    src[i] = static_cast<const T*>(is_k ? a.k : a.q) +
-             (is_k ? t * a.k_stride + (int64_t)(h - a.Hq) * D : t * a.q_stride + (int64_t)h * D);
-    if (h < heads) {
-      load8(src[i] + e0, x[i]);
-      load8(src[i] + e1, x[i] + 8);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[i][e] = 0.f;
-    }
+    const int h = min(h0 + i * kGroups, heads - 1);   // past the last head: loaded, not used
+    const T* src = (h >= a.Hq ? krow : qrow) + h * D;
+    raw[i][0] = load8(src + e0);
+    raw[i][1] = load8(src + e1);
   }
+
+  T* qdst = static_cast<T*>(a.q_out) + t * a.q_out_stride;
+  T* kdst = static_cast<T*>(a.k_out) + t * a.k_out_stride - (int64_t)a.Hq * D;
 
   // (cos, sin) of the lane's 8 pairs
   float2 cs[8];
@@ -134,9 +140,12 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkNormRo
     const int h = h0 + i * kGroups;
     const bool is_k = h >= a.Hq;
     const T* weight = static_cast<const T*>(is_k ? a.k_weight : a.q_weight);
+    float x[16];
+    widen8<T>(raw[i][0], x);
+    widen8<T>(raw[i][1], x + 8);
     float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) ss = fmaf(x[i][e], x[i][e], ss);
+    for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
     ss = row_sum<kLanes>(ss);
     float mean = ss * (1.f / D), eps = a.eps;
     // squares that left fp32's range: the row is brought near 1 by a power of
@@ -145,7 +154,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkNormRo
     if (__any_sync(0xffffffffu, far_off)) {
       float big = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) big = fmaxf(big, fabsf(x[i][e]));
+      for (int e = 0; e < 16; ++e) big = fmaxf(big, fabsf(x[e]));
       big = row_max<kLanes>(big);
       const int ex = (int)((__float_as_uint(big) >> 23) & 255u);   // biased exponent
       // 2^-exponent, at most 2^100 (below that the squares are in range again)
@@ -153,13 +162,13 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkNormRo
       float s2 = 0.f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float y = x[i][e] * sc;
+        const float y = x[e] * sc;
         s2 = fmaf(y, y, s2);
       }
       s2 = row_sum<kLanes>(s2);
       if (far_off && weight) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[i][e] *= sc;
+        for (int e = 0; e < 16; ++e) x[e] *= sc;
         mean = s2 * (1.f / D);
         eps = eps * sc * sc;
       }
@@ -168,20 +177,18 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkNormRo
     if (weight) {
       const float r = 1.f / sqrtf(mean + eps);
       float w[16];
-      load8(weight + e0, w);
-      load8(weight + e1, w + 8);
+      widen8<T>(load8(weight + e0), w);
+      widen8<T>(load8(weight + e1), w + 8);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[i][e] = x[i][e] * r * w[e];
+      for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
     }
     float z[16];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      z[e] = turned ? x[i][e] * cs[e].x - x[i][8 + e] * cs[e].y : x[i][e];
-      z[8 + e] = turned ? x[i][8 + e] * cs[e].x + x[i][e] * cs[e].y : x[i][8 + e];
+      z[e] = turned ? x[e] * cs[e].x - x[8 + e] * cs[e].y : x[e];
+      z[8 + e] = turned ? x[8 + e] * cs[e].x + x[e] * cs[e].y : x[8 + e];
     }
-    T* dst = static_cast<T*>(is_k ? a.k_out : a.q_out) +
-             (is_k ? t * a.k_out_stride + (int64_t)(h - a.Hq) * D
-                   : t * a.q_out_stride + (int64_t)h * D);
+    T* dst = (is_k ? kdst : qdst) + h * D;
     store8(dst + e0, z);
     store8(dst + e1, z + 8);
   }

@@ -93,6 +93,8 @@ def test_decode_refusals(lib):
         assert call(s, **{name: None}) == INVALID
         assert call(s, **{name: FAKE + 8}) == MISALIGNED
     assert call(_shape(num_seqs=65535, num_q_heads=60000, num_kv_heads=30000)) == UNSUPPORTED
+    assert call(_shape(num_seqs=4096, max_blocks_per_seq=1 << 16)) == UNSUPPORTED
+    assert call(_shape(num_blocks=1 << 28)) == UNSUPPORTED
 
 
 def _qk(lib, shape, axes=None, q=FAKE, qs=0, k=FAKE, ks=0, qw=FAKE, kw=FAKE, eps=1e-6, pos=FAKE,

@@ -407,3 +407,10 @@ def test_write_then_decode():
         assert np.array_equal(c.dev[1].cpu().numpy(), c.kp)
         assert np.array_equal(c.dev[2].cpu().numpy(), c.vp)
         c.check()
+
+
+def test_decode_of_empty_contexts_only():
+    c = Decode(89, [0, 0, 0], 4, 2, 64, W.DTYPE_F16)
+    c.run()
+    ok_status()
+    assert not c.got().any()
