@@ -8,8 +8,7 @@
 // q . k_j) v_j: S = Q K^T, P = 2^(S - m), O += P V per chunk of 128 keys with
 // a running maximum m and sum l, so scores never leave the SM.  4 Hq d
 // sum n (n + 1) / 2 flops against 2 n (Hq + Hkv) d elements: the tensor cores
-// bound it, with the exponentials close behind (16384 of them per 128 x 128
-// tile at 16 a clock take about as long as the tile's two products).
+// bound it.
 //
 // A persistent CTA per SM takes items of 256 query rows of one (prompt, KV
 // head) -- row r is (token r / G, head r % G), so one K/V chunk serves the
@@ -19,25 +18,36 @@
 //   warp 10, 11     issue S of tile 0, 1
 //   warp 12, 13     issue P V of tile 0, 1
 //   warp 14         finds the items
-// The two tiles run in antiphase: while one's softmax is on, the other's
-// products are.  Per tile, TMEM holds S (128 columns) and O (D columns); P
-// overwrites the second half of S as 16-bit pairs and is read from there as
-// the A operand.  S products have N = 128 keys: with N = 64 the operand reads of Q
-// from shared memory hold the tensor cores to two thirds of their rate.
-// Copies run ahead across items, and the next item's first S product overlaps
-// this one's epilogue.
+// Per tile, TMEM holds S (128 columns) and O (D columns); P overwrites the
+// first half of S as 16-bit pairs (at d = 64 it has columns of its own) and is
+// read from there as the A operand.  S products have N = 128 keys: with N = 64
+// the operand reads of Q from shared memory hold the tensor cores to two
+// thirds of their rate.  An issuing warp is held up for hundreds of clocks by
+// each of its commits, hence four of them and two commits a chunk; issued from
+// inside one elected lane's branch a product costs 50 clocks, predicated in
+// the whole warp 75 to 95.  Copies run ahead across items, and the next item's
+// first S product overlaps this one's epilogue.
+//
+// Measured (16 q, 8 kv heads, d = 128, bf16): 1 x 16384 tokens 0.73 ms = 1509
+// TFLOP/s, 80 % of the measured dense rate; 16 x 1024 71 us = 972 TFLOP/s.
+// What bounds it is a tile's own cycle, about 3200 clocks a chunk: S until the
+// softmax sees it (512 clocks of tensor time, 950 in all), the softmax (1250),
+// P V of the last 64 keys until S may go over P (650).  The two tiles' cycles
+// overlap; the tensor pipe is active 62 % of the time.  At d = 64 (4 x 4096,
+// 32 q, 8 kv heads: 0.30 ms, 905 TFLOP/s) the products are half as long and the
+// softmaxes of the two tiles bound each other.
 //
 // Items are numbered tile by tile from the prompts' far ends (the longest key
 // ranges) to their beginnings, and dealt to the CTAs forwards and backwards in
-// turn, so that all finish close together; each CTA finds its items from the lengths alone
-// (pa_locate), without a queue.
+// turn, so that all finish close together; each CTA finds its items from the
+// lengths alone (pa_locate), without a queue.
 //
 // Barriers complete once per use; use i has parity i & 1:
 //   k_full, v_full[st]   a chunk landed      k_free, v_free[st]  both tiles are done with it
 //   q_full[t]            Q tile landed       q_free[t]           the item's last S product is done
 //   s_full[t]            S written           p_full[t][h]        P of 64 keys written
 //   o_done[t]            O += P V done; the tile's next S may overwrite P
-//   turn[t]              tile t's weights of a chunk are written
+//   s_free[t]            S is read (only where P has columns of its own)
 //   item_full, item_free[i]  an item is known; every role has read it
 #include <math.h>
 
@@ -57,9 +67,9 @@ constexpr int kPaThreads = 512;        // four warpgroups; warp 15 has no role
 // Registers a thread: 512 x 128 at launch, dealt anew to the softmax
 // warpgroups and the other two (160 + 160 + 96 + 96 = 4 x 128).
 constexpr int kPaSoftmaxRegs = 160, kPaOtherRegs = 96;
-constexpr uint32_t kPaTmemP = 64;       // P of a tile: the second half of its S columns
 constexpr uint32_t kPaTmemO = 256;      // S of tile t: columns [128 t, 128 t + 128); then the O's
 constexpr float kPaRescaleLog2 = 8.f;
+constexpr float kPaNoMax = -3e38f;      // before the first key; finite, so that no exponent is inf - inf
 constexpr int kPaItems = 4;             // items found ahead
 constexpr int kPaRoles = 14;            // warps that work on an item
 
@@ -67,12 +77,11 @@ template <int D>
 struct PaCfg {
   static constexpr int kKStages = D == 128 ? 2 : 3;
   static constexpr int kVStages = D == 128 ? 2 : 3;
-  // The tiles' softmaxes take turns, so that one's runs while the other's
-  // products do (left alone they fall into step: 1 x 16384 tokens 811 us).
-  // At d = 128 the turn covers the maximum too (703 us, the weights alone
-  // 774 us); at d = 64, where the products are half as long, only the weights
-  // (4 x 4096 tokens 334 us, with the maximum 369 us).
-  static constexpr bool kTurnFirst = D == 128;
+  // P in columns of its own where there is room beside S (256) and O (2 D): the
+  // next S product then waits for the scores to be read, not for P V.
+  static constexpr bool kPApart = D == 64;
+  static constexpr uint32_t kTmemP = kPApart ? 256 + 2 * D : 0;   // tile 0's; else over S
+  static constexpr uint32_t kTmemPStep = kPApart ? kPaKeys / 2 : kPaKeys;
   static constexpr int kQBytes = kPaRows * D * 2;
   static constexpr int kKvBytes = kPaKeys * D * 2;
   static constexpr int kOffK = kPaTiles * kQBytes;
@@ -222,8 +231,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   constexpr int SK = C::kKStages, SV = C::kVStages;
   extern __shared__ unsigned char pa_smem_raw[];
   __shared__ __align__(8) uint64_t k_full[SK], k_free[SK], v_full[SV], v_free[SV],
-      q_full[kPaTiles], q_free[kPaTiles], s_full[kPaTiles], p_full[kPaTiles][2], o_done[kPaTiles],
-      v_tail, turn[kPaTiles], item_full[kPaItems], item_free[kPaItems];
+      q_full[kPaTiles], q_free[kPaTiles], s_full[kPaTiles], s_free[kPaTiles], p_full[kPaTiles][2], o_done[kPaTiles],
+      v_tail, item_full[kPaItems], item_free[kPaItems];
   __shared__ int4 items[kPaItems];   // (first token, tokens, KV head, first row); tokens 0: the end
   __shared__ uint32_t tmem_slot;
   __shared__ int gave_up_word;
@@ -252,10 +261,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       mbar_init(&q_full[t], 1);
       mbar_init(&q_free[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t][0], 4);   // one arrival per softmax warp
+      mbar_init(&s_free[t], 4);      // one arrival per softmax warp
+      mbar_init(&p_full[t][0], 4);
       mbar_init(&p_full[t][1], 4);
       mbar_init(&o_done[t], 1);
-      mbar_init(&turn[t], 4);     // one arrival per softmax warp
     }
     mbar_init(&v_tail, 1);
     for (int i = 0; i < kPaItems; ++i) {
@@ -315,12 +324,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_base + t * kPaKeys;
     const uint32_t t_o = tmem + lane_base + kPaTmemO + t * D;
+    const uint32_t t_p = tmem + lane_base + C::kTmemP + t * C::kTmemPStep;
     unsigned char* stage = smem + C::kOffO + warp * 4096;
     const float qscale = a.qscale;
     // a zero scale as a tiny one: every weight is 1 and -inf stays -inf
     const float qmul = fmaxf(fabsf(qscale), 1e-37f);
     uint32_t done = 0;                                // chunks of this tile so far
-    uint32_t turns = 0;                               // of them, chunks that both tiles have
     PaItem next;
     bool have = take(0, next);
     for (uint32_t m = 1; ok && have; ++m) {
@@ -330,48 +339,43 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         have = take(m, next);
         continue;
       }
-      // chunks that both tiles work on (the first tile's key range is the shorter one)
-      const int both = min(mine.chunks, pa_tile(it, G, 1 - t).chunks);
       const int first_row = it.row0 + t * kPaRows;
       const int my_pos = (first_row + min(trow, mine.rows - 1)) / G;
       const int warp_row = (warp & 3) * 32;
       const int pos_min = (first_row + min(warp_row, mine.rows - 1)) / G;
       const int pos_max = (first_row + min(warp_row + 31, mine.rows - 1)) / G;
-      float m_run = -INFINITY, l_run = 0.f;
+      float m_run = kPaNoMax, l_run = 0.f;
       for (int c = 0; c < mine.chunks; ++c, ++done) {
-        // The tiles take turns on chunks that both have: tile 1 after tile 0,
-        // tile 0's next after tile 1.
-        auto my_turn = [&]() -> bool {
-          if (c < both && (t == 1 || turns > 0))
-            ok = pa_wait(&turn[1 - t], (t == 1 ? turns : turns - 1) & 1, gave_up);
-          return ok;
-        };
         ok = pa_wait(&s_full[t], done & 1, gave_up);
         if (!ok) break;
-        if (C::kTurnFirst && !my_turn()) break;
         tc_fence_after();
         const int key0 = c * kPaKeys;
-        // scores of 64 of the chunk's keys, -inf where they lie past the row
-        float s[64];
-        auto scores = [&](int half) {
+        const bool second = key0 + 64 <= pos_max;   // a row of the warp sees the second 64 keys
+        auto signal = [&](uint64_t* bar) {          // this warp's tensor-memory accesses are done
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
+        };
+        if (C::kPApart && done > 0) {
+          // the product of chunk c - 1 has used its P (it mostly has)
+          ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        // Half a chunk at a time: scores, maximum, weights.  One instance of
+        // the code (unrolled twice it no longer stays in the instruction
+        // cache, and the rarely taken masks then cost thousands of clocks).
+#pragma unroll 1
+        for (int half = 0; half < (second ? 2 : 1); ++half) {
+          const int k0 = key0 + 64 * half;
+          float s[64];
           tmem_ld64(t_s + 64 * half, s);
-          const int lim = my_pos - key0 - 64 * half;   // the row's last key of these
-          if (key0 + 64 * half + 63 > pos_min) {
+          if (C::kPApart && (half == 1 || !second)) signal(&s_free[t]);
+          if (k0 + 63 > pos_min) {
+            const int lim = my_pos - k0;   // the row's last key of these
 #pragma unroll
             for (int j = 0; j < 64; ++j) s[j] = j > lim ? -INFINITY : s[j];
           }
-        };
-        // The second half's scores stay in registers while the maximum is
-        // settled; the first half's are read again after them (128 scores a
-        // thread would spill).  P takes the columns of the second half, so
-        // what is still to be read is not overwritten.  One instance of each
-        // piece of code: unrolled twice it no longer stays in the instruction
-        // cache, and the rarely taken masks then cost thousands of clocks.
-        const bool second = key0 + 64 <= pos_max;   // a row of the warp sees keys there
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int half = 0; half < (second ? 2 : 1); ++half) {
-          scores(half);
           float m8[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) m8[k] = fmaxf(s[k], s[8 + k]);
@@ -379,50 +383,44 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           for (int j = 16; j < 64; j += 16)
 #pragma unroll
             for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], s[j + k], s[j + 8 + k]);
-          mx = fmax3(mx, fmax3(m8[0], m8[1], m8[2]),
-                     fmax3(fmaxf(m8[3], m8[4]), fmaxf(m8[5], m8[6]), m8[7]));
-        }
-        // The running maximum only moves when a score passes it by more than
-        // 2^8, and only then is O rescaled: weights stay below 2^8, and the
-        // stale maximum cancels in O / l.
-        mx *= qmul;
-        const bool moved = mx > m_run + kPaRescaleLog2;
-        const float corr = moved ? softmax_exp2(m_run - mx) : 1.f;   // 0 on the first chunk
-        l_run *= corr;
-        if (moved) m_run = mx;
-        if (c > 0 && __any_sync(0xffffffffu, moved)) {
-          // the product of chunk c - 1 still adds to O
-          ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int col = 0; col < D; col += 32) {
-            float o[32];
-            tmem_ld32(t_o + col, o);
+          const float mx = qmul * fmaxf(fmax3(m8[0], m8[1], m8[2]),
+                                        fmax3(fmaxf(m8[3], m8[4]), fmaxf(m8[5], m8[6]), m8[7]));
+          // The running maximum only moves when a score passes it by more than
+          // 2^8, and only then is what is there rescaled: weights stay below
+          // 2^8, and the stale maximum cancels in O / l.
+          const bool moved = mx > m_run + kPaRescaleLog2;
+          if (__any_sync(0xffffffffu, moved)) {
+            const float corr = moved ? softmax_exp2(m_run - mx) : 1.f;   // 0 on the first chunk
+            l_run *= corr;
+            if (moved) m_run = mx;
+            if (half == 1) {   // the first half's weights, not handed over yet
+              float w[32];
+              tmem_ld32(t_p, w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= corr;
-            tmem_st32(t_o + col, o);
-          }
-          tc_fence_before();
-        }
-        if (!C::kTurnFirst && !my_turn()) break;
-        // weights, as 16-bit pairs, the second half's first
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        if (!second) {
-          if (mine.kend - key0 > 64) {   // another warp's rows see keys there
-            float zero[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) zero[j] = 0.f;
-            tmem_st32(t_s + kPaTmemP + 32, zero);
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[t][1]);
-        }
+              for (int j = 0; j < 32; ++j) {
+                const float2 f = Mma<T>::unpack(__float_as_uint(w[j]));
+                w[j] = __uint_as_float(Mma<T>::pack(f.x * corr, f.y * corr));
+              }
+              tmem_st32(t_p, w);
+            }
+            if (c > 0) {
+              // the product of chunk c - 1 still adds to O
+              ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll 1
-        for (int half = second ? 1 : 0; half >= 0; --half) {
-          if (second && half == 0) scores(0);
-          float w[32];
+              for (int col = 0; col < D; col += 32) {
+                float o[32];
+                tmem_ld32(t_o + col, o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] *= corr;
+                tmem_st32(t_o + col, o);
+              }
+            }
+          }
+          if (half == 1) signal(&p_full[t][0]);
+          // weights as 16-bit pairs, over scores that are read
+          float w[32], sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             float x0, x1;
@@ -431,16 +429,20 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             add_f32x2(sum[(j & 1) * 2], sum[(j & 1) * 2 + 1], p0, p1);
             w[j] = __uint_as_float(Mma<T>::pack(p0, p1));
           }
-          tmem_st32(t_s + kPaTmemP + 32 * half, w);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[t][half]);
+          tmem_st32(t_p + 32 * half, w);
+          l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
-        l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (c < both) {
-          if (lane == 0) mbar_arrive(&turn[t]);
-          ++turns;
+        if (!ok) break;
+        if (!second) {
+          if (mine.kend - key0 > 64) {   // another warp's rows see keys there
+            float zero[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) zero[j] = 0.f;
+            tmem_st32(t_p + 32, zero);
+          }
+          signal(&p_full[t][0]);
         }
+        signal(&p_full[t][1]);
       }
       if (!ok) break;
       have = take(m, next);   // while the last product runs
@@ -612,6 +614,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       // and V stages back with plain arrivals).
       const int t = (warp - 10) & 1;
       const uint32_t t_s = tmem + t * kPaKeys, t_o = tmem + kPaTmemO + t * D;
+      const uint32_t t_p = tmem + C::kTmemP + t * C::kTmemPStep;
       // a descriptor's start address is address >> 4 in its low 14 bits; every
       // operand lies below 256 KB, so offsets are added to the base's descriptor
       uint32_t chunk0 = 0, done = 0;   // the item's first chunk; chunks of this tile so far
@@ -621,24 +624,20 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         // descriptor), so that the maximum is always the largest score
         const uint32_t id_s = f16_idesc<T>(kPaRows, kPaKeys) | (a.qscale < 0.f ? 1u << 13 : 0u);
         const uint64_t q_desc = sw128_desc(sQ + t * C::kQBytes), k_desc = sw128_desc(sK);
-        uint32_t held = ~0u;           // the chunk whose V stage is to be handed back
         for (uint32_t m = 0; ok && take(m, it); ++m) {
           const PaTile mine = pa_tile(it, G, t), other = pa_tile(it, G, 1 - t);
           const int chunks = max(mine.chunks, other.chunks);
           ok = pa_wait(&q_full[t], m & 1, gave_up);
           if (!ok) break;
           if (mine.chunks == 0 && lane == 0) mbar_arrive(&q_free[t]);
-          for (int c = 0; c <= chunks; ++c) {
+          for (int c = 0; c < chunks; ++c) {
             const uint32_t kc = chunk0 + c;
-            if (c < mine.chunks) ok = pa_wait(&k_full[kc % SK], (kc / SK) & 1, gave_up);
-            // P of the tile's last chunk is used: its stages, and S, are free
-            if (ok && done > 0 && c <= mine.chunks && (c < mine.chunks || c < chunks)) {
-              ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
-              if (ok && held != ~0u && lane == 0) mbar_arrive(&v_free[held % SV]);
-              held = ~0u;
-            }
-            if (!ok || c == chunks) break;
-            if (c < mine.chunks) {
+            ok = pa_wait(&k_full[kc % SK], (kc / SK) & 1, gave_up);
+            if (ok && c < mine.chunks) {
+              // S of the tile's last chunk is read, and P over it used
+              if (done > 0)
+                ok = pa_wait(C::kPApart ? &s_free[t] : &o_done[t], (done - 1) & 1, gave_up);
+              if (!ok) break;
               tc_fence_after();
               const uint64_t kb = k_desc + (uint64_t)(((kc % SK) * C::kKvBytes) >> 4);
               if (leader) {
@@ -652,68 +651,74 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 if (c + 1 == mine.chunks) tc_commit(&q_free[t]);
               }
               __syncwarp();
-              held = kc;
               ++done;
               ok = pa_wait(&s_full[t], (done - 1) & 1, gave_up);
-              if (!ok) break;
-              if (lane == 0) mbar_arrive(&k_free[kc % SK]);
-            } else {
-              // a chunk of the other tile only
-              ok = pa_wait(&k_full[kc % SK], (kc / SK) & 1, gave_up) &&
-                   pa_wait(&v_full[kc % SV], (kc / SV) & 1, gave_up);
-              if (!ok) break;
-              if (lane == 0) {
-                mbar_arrive(&k_free[kc % SK]);
-                mbar_arrive(&v_free[kc % SV]);
-              }
             }
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&k_free[kc % SK]);
           }
           chunk0 = uniform(chunk0 + chunks);
         }
       } else {
         const uint32_t id_o = f16_idesc<T>(kPaRows, D) | (1u << 16);   // B (V) MN-major
         const uint64_t v_desc = pa_v_desc(sV);
+        constexpr uint32_t kNothing = ~0u;
+        uint32_t held = kNothing;   // the chunk whose V stage is to be handed back
         for (uint32_t m = 0; ok && take(m, it); ++m) {
           const PaTile mine = pa_tile(it, G, t), other = pa_tile(it, G, 1 - t);
-          for (int c = 0; c < mine.chunks; ++c, ++done) {
+          const int chunks = max(mine.chunks, other.chunks);
+          for (int c = 0; c < chunks; ++c) {
             const uint32_t vc = chunk0 + c;
+            if (held != kNothing) {
+              ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
+              if (!ok) break;
+              if (lane == 0) mbar_arrive(&v_free[held % SV]);
+              held = kNothing;
+            }
             ok = pa_wait(&v_full[vc % SV], (vc / SV) & 1, gave_up);
+            if (!ok) break;
+            if (c >= mine.chunks) {   // a chunk of the other tile only
+              if (lane == 0) mbar_arrive(&v_free[vc % SV]);
+              continue;
+            }
             const uint64_t vb = v_desc + (uint64_t)(((vc % SV) * C::kKvBytes) >> 4);
             const int steps = (min(kPaKeys, mine.kend - c * kPaKeys) + 15) / 16;
             auto product = [&](int kk, bool add) {
-              tc_mma_ts(t_o, t_s + kPaTmemP + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), id_o,
+              tc_mma_ts(t_o, t_p + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), id_o,
                         add ? 1u : 0u);
             };
-            // the second 64 keys' weights are ready first
-            ok = ok && pa_wait(&p_full[t][1], done & 1, gave_up);
+            // 64 keys at a time, as their weights become ready
+            ok = pa_wait(&p_full[t][0], done & 1, gave_up);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              if (steps >= 4) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) product(kk, c > 0 || kk > 0);
+              } else {
+#pragma unroll 1
+                for (int kk = 0; kk < steps; ++kk) product(kk, c > 0 || kk > 0);
+              }
+            }
+            __syncwarp();
+            ok = pa_wait(&p_full[t][1], done & 1, gave_up);
             if (!ok) break;
             tc_fence_after();
             if (leader) {
               if (steps == 8) {
 #pragma unroll
-                for (int kk = 4; kk < 8; ++kk) product(kk, c > 0 || kk > 4);
+                for (int kk = 4; kk < 8; ++kk) product(kk, true);
               } else {
 #pragma unroll 1
-                for (int kk = 4; kk < steps; ++kk) product(kk, c > 0 || kk > 4);
-              }
-            }
-            __syncwarp();
-            ok = pa_wait(&p_full[t][0], done & 1, gave_up);
-            if (!ok) break;
-            tc_fence_after();
-            if (leader) {
-              if (steps > 4) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) product(kk, true);
-              } else {
-#pragma unroll 1
-                for (int kk = 0; kk < steps; ++kk) product(kk, c > 0 || kk > 0);
+                for (int kk = 4; kk < steps; ++kk) product(kk, true);
               }
               tc_commit(&o_done[t]);
             }
             __syncwarp();
+            held = vc;
+            ++done;
           }
-          chunk0 = uniform(chunk0 + max(mine.chunks, other.chunks));
+          chunk0 = uniform(chunk0 + chunks);
         }
       }
     }
