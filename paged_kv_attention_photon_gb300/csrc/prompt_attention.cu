@@ -61,6 +61,7 @@ namespace {
 
 constexpr int kPaRows = 128;            // query rows of a tile = TMEM lanes
 constexpr int kPaKeys = 128;            // keys of a chunk
+constexpr int kPaHalf = 64;             // keys of an S product, of a softmax step and of a P V product
 constexpr int kPaTiles = 2;
 constexpr int kPaItemRows = kPaTiles * kPaRows;
 constexpr int kPaThreads = 512;        // four warpgroups; warp 15 has no role
@@ -77,11 +78,6 @@ template <int D>
 struct PaCfg {
   static constexpr int kKStages = D == 128 ? 2 : 3;
   static constexpr int kVStages = D == 128 ? 2 : 3;
-  // P in columns of its own where there is room beside S (256) and O (2 D): the
-  // next S product then waits for the scores to be read, not for P V.
-  static constexpr bool kPApart = D == 64;
-  static constexpr uint32_t kTmemP = kPApart ? 256 + 2 * D : 0;   // tile 0's; else over S
-  static constexpr uint32_t kTmemPStep = kPApart ? kPaKeys / 2 : kPaKeys;
   static constexpr int kQBytes = kPaRows * D * 2;
   static constexpr int kKvBytes = kPaKeys * D * 2;
   static constexpr int kOffK = kPaTiles * kQBytes;
@@ -231,7 +227,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   constexpr int SK = C::kKStages, SV = C::kVStages;
   extern __shared__ unsigned char pa_smem_raw[];
   __shared__ __align__(8) uint64_t k_full[SK], k_free[SK], v_full[SV], v_free[SV],
-      q_full[kPaTiles], q_free[kPaTiles], s_full[kPaTiles], s_free[kPaTiles], p_full[kPaTiles][2], o_done[kPaTiles],
+      q_full[kPaTiles], q_free[kPaTiles], s_full[kPaTiles][2], p_full[kPaTiles][2], o_done[kPaTiles][2],
       v_tail, item_full[kPaItems], item_free[kPaItems];
   __shared__ int4 items[kPaItems];   // (first token, tokens, KV head, first row); tokens 0: the end
   __shared__ uint32_t tmem_slot;
@@ -260,11 +256,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     for (int t = 0; t < kPaTiles; ++t) {
       mbar_init(&q_full[t], 1);
       mbar_init(&q_free[t], 1);
-      mbar_init(&s_full[t], 1);
-      mbar_init(&s_free[t], 4);      // one arrival per softmax warp
-      mbar_init(&p_full[t][0], 4);
-      mbar_init(&p_full[t][1], 4);
-      mbar_init(&o_done[t], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&s_full[t][h], 1);
+        mbar_init(&p_full[t][h], 4);   // one arrival per softmax warp
+        mbar_init(&o_done[t][h], 1);
+      }
     }
     mbar_init(&v_tail, 1);
     for (int i = 0; i < kPaItems; ++i) {
@@ -324,7 +320,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_base + t * kPaKeys;
     const uint32_t t_o = tmem + lane_base + kPaTmemO + t * D;
-    const uint32_t t_p = tmem + lane_base + C::kTmemP + t * C::kTmemPStep;
     unsigned char* stage = smem + C::kOffO + warp * 4096;
     const float qscale = a.qscale;
     // a zero scale as a tiny one: every weight is 1 and -inf stays -inf
@@ -346,109 +341,87 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const int pos_max = (first_row + min(warp_row + 31, mine.rows - 1)) / G;
       float m_run = kPaNoMax, l_run = 0.f;
       for (int c = 0; c < mine.chunks; ++c, ++done) {
-        ok = pa_wait(&s_full[t], done & 1, gave_up);
-        if (!ok) break;
-        tc_fence_after();
         const int key0 = c * kPaKeys;
-        const bool second = key0 + 64 <= pos_max;   // a row of the warp sees the second 64 keys
-        auto signal = [&](uint64_t* bar) {          // this warp's tensor-memory accesses are done
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar);
-        };
-        if (C::kPApart && done > 0) {
-          // the product of chunk c - 1 has used its P (it mostly has)
-          ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
-          if (!ok) break;
-          tc_fence_after();
-        }
+        const bool second = key0 + kPaHalf <= pos_max;   // a row of the warp sees the second half
         // Half a chunk at a time: scores, maximum, weights.  One instance of
         // the code (unrolled twice it no longer stays in the instruction
         // cache, and the rarely taken masks then cost thousands of clocks).
 #pragma unroll 1
-        for (int half = 0; half < (second ? 2 : 1); ++half) {
-          const int k0 = key0 + 64 * half;
-          float s[64];
-          tmem_ld64(t_s + 64 * half, s);
-          if (C::kPApart && (half == 1 || !second)) signal(&s_free[t]);
-          if (k0 + 63 > pos_min) {
-            const int lim = my_pos - k0;   // the row's last key of these
+        for (int half = 0; half < 2; ++half) {
+          ok = pa_wait(&s_full[t][half], done & 1, gave_up);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t t_h = t_s + kPaHalf * half;
+          if (half == 0 || second) {
+            const int k0 = key0 + kPaHalf * half;
+            float s[64];
+            tmem_ld64(t_h, s);
+            if (k0 + kPaHalf - 1 > pos_min) {
+              const int lim = my_pos - k0;   // the row's last key of these
 #pragma unroll
-            for (int j = 0; j < 64; ++j) s[j] = j > lim ? -INFINITY : s[j];
-          }
-          float m8[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) m8[k] = fmaxf(s[k], s[8 + k]);
-#pragma unroll
-          for (int j = 16; j < 64; j += 16)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], s[j + k], s[j + 8 + k]);
-          const float mx = qmul * fmaxf(fmax3(m8[0], m8[1], m8[2]),
-                                        fmax3(fmaxf(m8[3], m8[4]), fmaxf(m8[5], m8[6]), m8[7]));
-          // The running maximum only moves when a score passes it by more than
-          // 2^8, and only then is what is there rescaled: weights stay below
-          // 2^8, and the stale maximum cancels in O / l.
-          const bool moved = mx > m_run + kPaRescaleLog2;
-          if (__any_sync(0xffffffffu, moved)) {
-            const float corr = moved ? softmax_exp2(m_run - mx) : 1.f;   // 0 on the first chunk
-            l_run *= corr;
-            if (moved) m_run = mx;
-            if (half == 1) {   // the first half's weights, not handed over yet
-              float w[32];
-              tmem_ld32(t_p, w);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float2 f = Mma<T>::unpack(__float_as_uint(w[j]));
-                w[j] = __uint_as_float(Mma<T>::pack(f.x * corr, f.y * corr));
-              }
-              tmem_st32(t_p, w);
+              for (int j = 0; j < 64; ++j) s[j] = j > lim ? -INFINITY : s[j];
             }
-            if (c > 0) {
-              // the product of chunk c - 1 still adds to O
-              ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
-              if (!ok) break;
-              tc_fence_after();
+            float m8[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m8[k] = fmaxf(s[k], s[8 + k]);
+#pragma unroll
+            for (int j = 16; j < 64; j += 16)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], s[j + k], s[j + 8 + k]);
+            const float mx = qmul * fmaxf(fmax3(m8[0], m8[1], m8[2]),
+                                          fmax3(fmaxf(m8[3], m8[4]), fmaxf(m8[5], m8[6]), m8[7]));
+            // The running maximum only moves when a score passes it by more
+            // than 2^8, and only then is O rescaled: weights stay below 2^8,
+            // and the stale maximum cancels in O / l.
+            const bool moved = mx > m_run + kPaRescaleLog2;
+            if (__any_sync(0xffffffffu, moved)) {
+              const float corr = moved ? softmax_exp2(m_run - mx) : 1.f;   // 0 at first
+              l_run *= corr;
+              if (moved) m_run = mx;
+              if (c > 0 || half > 0) {
+                // the product of the half before still adds to O
+                ok = pa_wait(&o_done[t][1 - half], (half ? done : done - 1) & 1, gave_up);
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll 1
-              for (int col = 0; col < D; col += 32) {
-                float o[32];
-                tmem_ld32(t_o + col, o);
+                for (int col = 0; col < D; col += 32) {
+                  float o[32];
+                  tmem_ld32(t_o + col, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= corr;
-                tmem_st32(t_o + col, o);
+                  for (int i = 0; i < 32; ++i) o[i] *= corr;
+                  tmem_st32(t_o + col, o);
+                }
               }
             }
-          }
-          if (half == 1) signal(&p_full[t][0]);
-          // weights as 16-bit pairs, over scores that are read
-          float w[32], sum[4] = {0.f, 0.f, 0.f, 0.f};
+            // weights as 16-bit pairs, over scores that are read
+            float w[32], sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float x0, x1;
-            fma_f32x2(x0, x1, s[2 * j], s[2 * j + 1], qmul, -m_run);
-            const float p0 = softmax_exp2(x0), p1 = softmax_exp2(x1);
-            add_f32x2(sum[(j & 1) * 2], sum[(j & 1) * 2 + 1], p0, p1);
-            w[j] = __uint_as_float(Mma<T>::pack(p0, p1));
-          }
-          tmem_st32(t_p + 32 * half, w);
-          l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        }
-        if (!ok) break;
-        if (!second) {
-          if (mine.kend - key0 > 64) {   // another warp's rows see keys there
+            for (int j = 0; j < 32; ++j) {
+              float x0, x1;
+              fma_f32x2(x0, x1, s[2 * j], s[2 * j + 1], qmul, -m_run);
+              const float p0 = softmax_exp2(x0), p1 = softmax_exp2(x1);
+              add_f32x2(sum[(j & 1) * 2], sum[(j & 1) * 2 + 1], p0, p1);
+              w[j] = __uint_as_float(Mma<T>::pack(p0, p1));
+            }
+            tmem_st32(t_h, w);
+            l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          } else if (mine.kend - key0 > kPaHalf) {   // another warp's rows see keys there
             float zero[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) zero[j] = 0.f;
-            tmem_st32(t_p + 32, zero);
+            tmem_st32(t_h, zero);
           }
-          signal(&p_full[t][0]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[t][half]);
         }
-        signal(&p_full[t][1]);
+        if (!ok) break;
       }
       if (!ok) break;
       have = take(m, next);   // while the last product runs
       if (!ok) break;
       // ---- O / l
-      ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
+      ok = pa_wait(&o_done[t][1], (done - 1) & 1, gave_up);
       if (!ok) break;
       tc_fence_after();
       // Through shared memory in the copies' swizzled layout.  A warp whose 32
@@ -614,7 +587,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       // and V stages back with plain arrivals).
       const int t = (warp - 10) & 1;
       const uint32_t t_s = tmem + t * kPaKeys, t_o = tmem + kPaTmemO + t * D;
-      const uint32_t t_p = tmem + C::kTmemP + t * C::kTmemPStep;
       // a descriptor's start address is address >> 4 in its low 14 bits; every
       // operand lies below 256 KB, so offsets are added to the base's descriptor
       uint32_t chunk0 = 0, done = 0;   // the item's first chunk; chunks of this tile so far
@@ -622,7 +594,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       if (warp < 12) {
         // with a negative scale the product is negated (A's sign bit of the
         // descriptor), so that the maximum is always the largest score
-        const uint32_t id_s = f16_idesc<T>(kPaRows, kPaKeys) | (a.qscale < 0.f ? 1u << 13 : 0u);
+        const uint32_t id_s = f16_idesc<T>(kPaRows, kPaHalf) | (a.qscale < 0.f ? 1u << 13 : 0u);
         const uint64_t q_desc = sw128_desc(sQ + t * C::kQBytes), k_desc = sw128_desc(sK);
         for (uint32_t m = 0; ok && take(m, it); ++m) {
           const PaTile mine = pa_tile(it, G, t), other = pa_tile(it, G, 1 - t);
@@ -634,25 +606,29 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             const uint32_t kc = chunk0 + c;
             ok = pa_wait(&k_full[kc % SK], (kc / SK) & 1, gave_up);
             if (ok && c < mine.chunks) {
-              // S of the tile's last chunk is read, and P over it used
-              if (done > 0)
-                ok = pa_wait(C::kPApart ? &s_free[t] : &o_done[t], (done - 1) & 1, gave_up);
-              if (!ok) break;
-              tc_fence_after();
               const uint64_t kb = k_desc + (uint64_t)(((kc % SK) * C::kKvBytes) >> 4);
-              if (leader) {
+              for (int h = 0; h < 2; ++h) {
+                // P of the last chunk's half, which lies over S, is used
+                if (done > 0) ok = pa_wait(&o_done[t][h], (done - 1) & 1, gave_up);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t off = (kk >> 2) * (kPaKeys * 128) + (kk & 3) * 32;
-                  tc_mma(t_s, q_desc + (uint64_t)(off >> 4), kb + (uint64_t)(off >> 4), id_s,
-                         kk > 0);
+                  for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t at = (kk & 3) * 32;
+                    tc_mma(t_s + h * kPaHalf,
+                           q_desc + (uint64_t)(((kk >> 2) * (kPaRows * 128) + at) >> 4),
+                           kb + (uint64_t)(((kk >> 2) * (kPaKeys * 128) + h * (kPaHalf * 128) + at) >> 4),
+                           id_s, kk > 0);
+                  }
+                  tc_commit(&s_full[t][h]);
+                  if (h == 1 && c + 1 == mine.chunks) tc_commit(&q_free[t]);
                 }
-                tc_commit(&s_full[t]);
-                if (c + 1 == mine.chunks) tc_commit(&q_free[t]);
+                __syncwarp();
               }
-              __syncwarp();
+              if (!ok) break;
               ++done;
-              ok = pa_wait(&s_full[t], (done - 1) & 1, gave_up);
+              ok = pa_wait(&s_full[t][1], (done - 1) & 1, gave_up);
             }
             if (!ok) break;
             if (lane == 0) mbar_arrive(&k_free[kc % SK]);
@@ -670,7 +646,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           for (int c = 0; c < chunks; ++c) {
             const uint32_t vc = chunk0 + c;
             if (held != kNothing) {
-              ok = pa_wait(&o_done[t], (done - 1) & 1, gave_up);
+              ok = pa_wait(&o_done[t][1], (done - 1) & 1, gave_up);
               if (!ok) break;
               if (lane == 0) mbar_arrive(&v_free[held % SV]);
               held = kNothing;
@@ -683,38 +659,30 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             }
             const uint64_t vb = v_desc + (uint64_t)(((vc % SV) * C::kKvBytes) >> 4);
             const int steps = (min(kPaKeys, mine.kend - c * kPaKeys) + 15) / 16;
-            auto product = [&](int kk, bool add) {
-              tc_mma_ts(t_o, t_p + kk * 8, vb + (uint64_t)((kk * 2048) >> 4), id_o,
-                        add ? 1u : 0u);
-            };
-            // 64 keys at a time, as their weights become ready
-            ok = pa_wait(&p_full[t][0], done & 1, gave_up);
-            if (!ok) break;
-            tc_fence_after();
-            if (leader) {
-              if (steps >= 4) {
+            // 64 keys at a time, as their weights become ready; a half without
+            // keys has nothing to add, only its barrier to complete
+            for (int h = 0; h < 2; ++h) {
+              ok = pa_wait(&p_full[t][h], done & 1, gave_up);
+              if (!ok) break;
+              tc_fence_after();
+              auto product = [&](int kk) {
+                tc_mma_ts(t_o, t_s + h * kPaHalf + kk * 8,
+                          vb + (uint64_t)((h * (kPaHalf * 128) + kk * 2048) >> 4), id_o,
+                          c > 0 || h > 0 || kk > 0 ? 1u : 0u);
+              };
+              if (leader) {
+                if (steps >= 4 * h + 4) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) product(kk, c > 0 || kk > 0);
-              } else {
+                  for (int kk = 0; kk < 4; ++kk) product(kk);
+                } else {
 #pragma unroll 1
-                for (int kk = 0; kk < steps; ++kk) product(kk, c > 0 || kk > 0);
+                  for (int kk = 0; kk < steps - 4 * h; ++kk) product(kk);
+                }
+                tc_commit(&o_done[t][h]);
               }
+              __syncwarp();
             }
-            __syncwarp();
-            ok = pa_wait(&p_full[t][1], done & 1, gave_up);
             if (!ok) break;
-            tc_fence_after();
-            if (leader) {
-              if (steps == 8) {
-#pragma unroll
-                for (int kk = 4; kk < 8; ++kk) product(kk, true);
-              } else {
-#pragma unroll 1
-                for (int kk = 4; kk < steps; ++kk) product(kk, true);
-              }
-              tc_commit(&o_done[t]);
-            }
-            __syncwarp();
             held = vc;
             ++done;
           }
