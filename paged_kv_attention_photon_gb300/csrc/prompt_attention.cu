@@ -82,7 +82,7 @@ struct PaCfg {
   static constexpr int kKvBytes = kPaKeys * D * 2;
   static constexpr int kOffK = kPaTiles * kQBytes;
   static constexpr int kOffV = kOffK + kKStages * kKvBytes;
-  static constexpr int kOffO = kOffV + kVStages * kKvBytes;   // 4 KB a softmax warp: 32 rows x 64
+  static constexpr int kOffO = kOffV + kVStages * kKvBytes;   // a softmax warp's 2 x 2 KB: 32 rows x 32
   static constexpr int kSmem = kOffO + kPaTiles * 4 * 4096 + 1024;   // + alignment to a swizzle atom
 };
 
@@ -117,9 +117,10 @@ __device__ __forceinline__ void tma_store_box3(const CUtensorMap* map, int x, in
       "r"(x), "r"(y), "r"(z), "r"(src)
       : "memory");
 }
-// This thread's bulk stores have read their shared memory.
+// This thread's bulk stores, all but the N newest, have read their shared memory.
+template <int N>
 __device__ __forceinline__ void bulk_store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // Bounded wait for a barrier phase, by a whole warp; false after kWaitLimitNs,
@@ -204,14 +205,14 @@ __device__ __forceinline__ bool pa_locate(const PromptArgs& a, int G, uint32_t L
 struct PaTile {
   int rows, kend, chunks;
 };
-__device__ __forceinline__ PaTile pa_tile(const PaItem& it, int G, int t) {
+__device__ __forceinline__ PaTile pa_tile(const PaItem& it, int g2, int t) {   // g2 = log2(G)
   PaTile p;
   const int first = it.row0 + t * kPaRows;
-  p.rows = min(kPaRows, it.n * G - first);
+  p.rows = min(kPaRows, (it.n << g2) - first);
   if (p.rows <= 0) {
     p.rows = p.kend = p.chunks = 0;
   } else {
-    p.kend = (first + p.rows - 1) / G + 1;
+    p.kend = ((first + p.rows - 1) >> g2) + 1;
     p.chunks = (p.kend + kPaKeys - 1) / kPaKeys;
   }
   return p;
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   // uniform registers
   auto uniform = [](uint32_t x) -> uint32_t { return __shfl_sync(0xffffffffu, x, 0); };
   const int tid = threadIdx.x, warp = (int)uniform(tid >> 5), lane = tid & 31;
-  const int G = a.Hq / a.Hkv;
+  const int G = a.Hq / a.Hkv, g2 = __ffs(G) - 1;   // a power of two
 
   if (tid == 0) {
     gave_up_word = 0;
@@ -329,16 +330,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     bool have = take(0, next);
     for (uint32_t m = 1; ok && have; ++m) {
       it = next;
-      const PaTile mine = pa_tile(it, G, t);
+      const PaTile mine = pa_tile(it, g2, t);
       if (mine.rows == 0) {
         have = take(m, next);
         continue;
       }
       const int first_row = it.row0 + t * kPaRows;
-      const int my_pos = (first_row + min(trow, mine.rows - 1)) / G;
+      const int my_pos = (first_row + min(trow, mine.rows - 1)) >> g2;
       const int warp_row = (warp & 3) * 32;
-      const int pos_min = (first_row + min(warp_row, mine.rows - 1)) / G;
-      const int pos_max = (first_row + min(warp_row + 31, mine.rows - 1)) / G;
+      const int pos_min = (first_row + min(warp_row, mine.rows - 1)) >> g2;
+      const int pos_max = (first_row + min(warp_row + 31, mine.rows - 1)) >> g2;
       float m_run = kPaNoMax, l_run = 0.f;
       for (int c = 0; c < mine.chunks; ++c, ++done) {
         const int key0 = c * kPaKeys;
@@ -425,21 +426,30 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       if (!ok) break;
       tc_fence_after();
       // Through shared memory in the copies' swizzled layout.  A warp whose 32
-      // rows all belong to the prompt hands them to a tensor copy, which runs
-      // on while the next item begins; at a prompt's end 8 lanes write 128
-      // bytes of a row (rows past it belong to others).
+      // rows all belong to the prompt hands them to tensor copies, which run
+      // on while the next item begins; at a prompt's end 4 lanes write 64
+      // bytes of a row (rows past it belong to others).  32 columns a turn:
+      // the loop is short enough that its code is fetched once, and a buffer
+      // is filled while the other one's copy reads.
       const float inv = 1.f / l_run;
       const bool whole = warp_row + 32 <= mine.rows;
       T* dst = static_cast<T*>(a.out) + (int64_t)it.q0 * a.out_stride + (int64_t)it.kvh * G * D;
 #pragma unroll 1
-      for (int col = 0; col < D; col += 64) {
-        float o[64];
-        tmem_ld64(t_o + col, o);
-        if (lane == 0) bulk_store_wait_read();   // the staging rows' last copy has read them
+      for (int col = 0; col < D; col += 32) {
+        // 32 rows x 32 elements in one of the warp's two buffers
+        float o[32];
+        tmem_ld32(t_o + col, o);
+        unsigned char* buf = stage + (col & 32) * 64;
+        if (lane == 0) {   // the buffer's last copy has read it
+          if (whole)
+            bulk_store_wait_read<1>();
+          else
+            bulk_store_wait_read<0>();   // no copies of this item's to count
+        }
         __syncwarp();
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch)
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((ch ^ (lane & 7)) << 4)) =
+        for (int ch = 0; ch < 4; ++ch)
+          *reinterpret_cast<uint4*>(buf + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) =
               make_uint4(Mma<T>::pack(o[ch * 8] * inv, o[ch * 8 + 1] * inv),
                          Mma<T>::pack(o[ch * 8 + 2] * inv, o[ch * 8 + 3] * inv),
                          Mma<T>::pack(o[ch * 8 + 4] * inv, o[ch * 8 + 5] * inv),
@@ -448,25 +458,26 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           fence_async_smem();
           __syncwarp();
           if (lane == 0)
-            tma_store_box3(&tm_o, col, it.kvh * G, it.q0 + (first_row + warp_row) / G,
-                           smem_addr(stage));
+            tma_store_box3(&tm_o, col, it.kvh * G, it.q0 + ((first_row + warp_row) >> g2),
+                           smem_addr(buf));
         } else {
           __syncwarp();
 #pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3), ch = lane & 7;
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2), ch = lane & 3;
+            const uint4 v =
+                *reinterpret_cast<const uint4*>(buf + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
             const int row = first_row + warp_row + r;
             if (warp_row + r < mine.rows)
-              *reinterpret_cast<uint4*>(dst + (int64_t)(row / G) * a.out_stride + (row % G) * D +
-                                        col + ch * 8) = v;
+              *reinterpret_cast<uint4*>(dst + (int64_t)(row >> g2) * a.out_stride +
+                                        (row & (G - 1)) * D + col + ch * 8) = v;
           }
           __syncwarp();
         }
       }
       tc_fence_before();   // O is read before the next item's products (p_full orders them)
     }
-    if (lane == 0) bulk_store_wait_read();   // before the CTA's shared memory goes
+    if (lane == 0) bulk_store_wait_read<0>();   // before the CTA's shared memory goes
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaOtherRegs));
     if (warp == 8) {
@@ -474,7 +485,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       uint32_t kc = 0;                      // chunks so far
       uint32_t q_count[kPaTiles] = {0, 0};   // Q tiles asked for so far
       for (uint32_t m = 0; ok && take(m, it); ++m) {
-        const PaTile t0 = pa_tile(it, G, 0), t1 = pa_tile(it, G, 1);
+        const PaTile t0 = pa_tile(it, g2, 0), t1 = pa_tile(it, g2, 1);
         const int chunks = max(t0.chunks, t1.chunks);
         for (int c = 0; c < chunks && ok; ++c, ++kc) {
           const int st = kc % SK;
@@ -503,7 +514,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
               tma_load_box3(sQ + t * C::kQBytes + h * (kPaRows * 128), &tm_q, h * 64, it.kvh * G,
-                            it.q0 + (it.row0 + t * kPaRows) / G, &q_full[t]);
+                            it.q0 + ((it.row0 + t * kPaRows) >> g2), &q_full[t]);
           }
           __syncwarp();
         }
@@ -519,7 +530,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       // ================================================================ V copies
       uint32_t vc = 0, tails = 0;
       for (uint32_t m = 0; ok && take(m, it); ++m) {
-        const PaTile t0 = pa_tile(it, G, 0), t1 = pa_tile(it, G, 1);
+        const PaTile t0 = pa_tile(it, g2, 0), t1 = pa_tile(it, g2, 1);
         const int chunks = max(t0.chunks, t1.chunks), kend = max(t0.kend, t1.kend);
         for (int c = 0; c < chunks && ok; ++c, ++vc) {
           const int st = vc % SV;
@@ -597,7 +608,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const uint32_t id_s = f16_idesc<T>(kPaRows, kPaHalf) | (a.qscale < 0.f ? 1u << 13 : 0u);
         const uint64_t q_desc = sw128_desc(sQ + t * C::kQBytes), k_desc = sw128_desc(sK);
         for (uint32_t m = 0; ok && take(m, it); ++m) {
-          const PaTile mine = pa_tile(it, G, t), other = pa_tile(it, G, 1 - t);
+          const PaTile mine = pa_tile(it, g2, t), other = pa_tile(it, g2, 1 - t);
           const int chunks = max(mine.chunks, other.chunks);
           ok = pa_wait(&q_full[t], m & 1, gave_up);
           if (!ok) break;
@@ -641,7 +652,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         constexpr uint32_t kNothing = ~0u;
         uint32_t held = kNothing;   // the chunk whose V stage is to be handed back
         for (uint32_t m = 0; ok && take(m, it); ++m) {
-          const PaTile mine = pa_tile(it, G, t), other = pa_tile(it, G, 1 - t);
+          const PaTile mine = pa_tile(it, g2, t), other = pa_tile(it, g2, 1 - t);
           const int chunks = max(mine.chunks, other.chunks);
           for (int c = 0; c < chunks; ++c) {
             const uint32_t vc = chunk0 + c;
@@ -734,8 +745,8 @@ cudaError_t launch_t(const PromptArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // out as q, a box of a warp's 32 rows
   const cuuint64_t os[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.out_stride * 2};
-  const cuuint32_t ob[3] = {64, G, 32u / G};
-  e = encode_tensor_map(&to, type, 3, a.out, qd, os, ob, CU_TENSOR_MAP_SWIZZLE_128B);
+  const cuuint32_t ob[3] = {32, G, 32u / G};
+  e = encode_tensor_map(&to, type, 3, a.out, qd, os, ob, CU_TENSOR_MAP_SWIZZLE_64B);
   if (e != cudaSuccess) return e;
   // at most this many items exist
   const int64_t most = ((int64_t)a.num_tokens * (int)G / kPaItemRows + a.B) * a.Hkv;
