@@ -316,7 +316,8 @@ photon_status_t photon_cache_write_int4(const void* k, int64_t k_stride, const v
 
 /* photon_paged_gather over a 4-bit cache: k_dense, v_dense ([num_seqs][Hkv]
  * [max_blocks_per_seq * block_size][d], the storage type) receive the values
- * lo + n * step, rounded once, of each context's rows, and zeros after. */
+ * lo + n * step, rounded once (past the type's range: an infinity), of each
+ * context's rows, and zeros after. */
 photon_status_t photon_paged_gather_int4(const void* k_cache, const void* v_cache,
                                          const int32_t* block_tables,
                                          const int32_t* context_lens, void* k_dense,

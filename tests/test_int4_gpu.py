@@ -171,6 +171,32 @@ def test_gather(dtype, d):
     assert not got[5, :, 16:32].any() and got[5, :, 32:50].any() and not got[4].any()
 
 
+@pytest.mark.parametrize("dtype,tiny", [(W.DTYPE_F16, 2.0 ** -24), (W.DTYPE_BF16, 2.0 ** -30)])
+def test_gather_rounds_once(dtype, tiny):
+    """Values halfway between two of the storage type's but for a lo far below them."""
+    rng = np.random.default_rng(31)
+    d, n = 64, 256
+    x = rng.uniform(tiny, 4.0, (n, 1, d))
+    x[:, 0, 0] = np.where(np.arange(n) % 2, tiny, -tiny)
+    x[:, 0, 1] = rng.uniform(0.5, 4.0, n)
+    x = I.narrow(np.clip(x, x[:, :, :1], x[:, :, 1:2]), dtype)
+    codes, step, lo = I.quantise(x, dtype)
+    pool = np.zeros((n // 16, 1, I.record_bytes(d)), dtype=np.uint8)
+    for which in (True, False):
+        for t in range(n):
+            I.store_row(pool, which, d, t // 16, 0, t % 16, codes[t, 0], step[t, 0], lo[t, 0])
+        shape = shape_for(seqs=1, hq=1, hkv=1, d=d, nb=n // 16, mbs=n // 16, dtype=dtype)
+        table = dev(np.arange(n // 16, dtype=np.int32)[None])
+        out = [torch.zeros((1, 1, n, d), dtype=torch.int16, device="cuda") for _ in range(2)]
+        P.photon_paged_gather_int4(dev(pool), dev(pool), table, dev(np.array([n], np.int32)), *out,
+                                   shape)
+        ok_status()
+        exact = I.values(codes, step, lo, dtype)[:, 0]
+        first = exact.astype(np.float32).astype(np.float64)
+        assert (I.narrow(first, dtype) != I.narrow(exact, dtype)).any()   # rounding twice shows
+        assert np.array_equal(host(out[0 if which else 1], x).reshape(n, d), I.narrow(exact, dtype))
+
+
 class Decode:
     """One decode call's device buffers; the output starts as -1 bits, the workspace as NaNs."""
 
