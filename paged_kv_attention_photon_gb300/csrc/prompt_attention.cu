@@ -18,24 +18,30 @@
 //   warp 10, 11     issue S of tile 0, 1
 //   warp 12, 13     issue P V of tile 0, 1
 //   warp 14         finds the items
-// Per tile, TMEM holds S (128 columns) and O (D columns); P overwrites the
-// first half of S as 16-bit pairs (at d = 64 it has columns of its own) and is
-// read from there as the A operand.  S products have N = 128 keys: with N = 64
-// the operand reads of Q from shared memory hold the tensor cores to two
-// thirds of their rate.  An issuing warp is held up for hundreds of clocks by
-// each of its commits, hence four of them and two commits a chunk; issued from
-// inside one elected lane's branch a product costs 50 clocks, predicated in
-// the whole warp 75 to 95.  Copies run ahead across items, and the next item's
-// first S product overlaps this one's epilogue.
+// Per tile, TMEM holds S (128 columns) and O (D columns).  S, softmax and P V
+// go by halves of 64 keys, each half with its own barriers: P of a half lies
+// over its S as 16-bit pairs and is read from there as the A operand, so the
+// softmax of one half runs while S or P V of the other does.  (With S of all 128
+// keys at once the tensor cores reach their rate on it, but a chunk is one long
+// chain: 1 x 16384 tokens 0.73 ms against 0.64 ms by halves.  At d = 64 TMEM has
+// room for a P apart from S; by halves that is slower, 4 x 4096 tokens 0.356 ms
+// against 0.30 to 0.33 ms.)  An issuing warp is held up for hundreds of clocks by
+// each of its commits, hence four of them; issued from inside one elected
+// lane's branch a product costs 50 clocks, predicated in the whole warp 75 to
+// 95.  Copies run ahead across items, and the next item's first S products
+// overlap this one's epilogue.
 //
-// Measured (16 q, 8 kv heads, d = 128, bf16): 1 x 16384 tokens 0.73 ms = 1509
-// TFLOP/s, 80 % of the measured dense rate; 16 x 1024 71 us = 972 TFLOP/s.
-// What bounds it is a tile's own cycle, about 3200 clocks a chunk: S until the
-// softmax sees it (512 clocks of tensor time, 950 in all), the softmax (1250),
-// P V of the last 64 keys until S may go over P (650).  The two tiles' cycles
-// overlap; the tensor pipe is active 62 % of the time.  At d = 64 (4 x 4096,
-// 32 q, 8 kv heads: 0.30 ms, 905 TFLOP/s) the products are half as long and the
-// softmaxes of the two tiles bound each other.
+// Measured (16 q, 8 kv heads, d = 128, back to back): 1 x 16384 tokens, bf16, 0.635
+// ms = 1732 TFLOP/s, 92 % of the measured dense rate; 16 x 1024, fp16, 63.7 us =
+// 1080 TFLOP/s.  At d = 64 (32 q, 8 kv heads, fp16) 4 x 4096 tokens take 0.30 to
+// 0.33 ms = 840 to 920 TFLOP/s: the products are half as long for the same
+// softmax, which bounds it.  In short prompts the items do: ending one and
+// starting the next costs a tile about 3000 clocks (the last P V 120, the
+// output's four turns of 430, the next item and its first S 750), when a chunk
+// of 128 keys takes about 2200.  Asking for the next item's Q ahead of time (a
+// prefetch into L2) made 16 x 1024 slower, 66.5 against 64.9 us; coalesced
+// stores from shared memory in place of the output's tensor copies 66.9 against
+// 63.7 us.
 //
 // Items are numbered tile by tile from the prompts' far ends (the longest key
 // ranges) to their beginnings, and dealt to the CTAs forwards and backwards in
@@ -45,9 +51,8 @@
 // Barriers complete once per use; use i has parity i & 1:
 //   k_full, v_full[st]   a chunk landed      k_free, v_free[st]  both tiles are done with it
 //   q_full[t]            Q tile landed       q_free[t]           the item's last S product is done
-//   s_full[t]            S written           p_full[t][h]        P of 64 keys written
-//   o_done[t]            O += P V done; the tile's next S may overwrite P
-//   s_free[t]            S is read (only where P has columns of its own)
+//   s_full[t][h]         S of 64 keys        p_full[t][h]        their P written
+//   o_done[t][h]         O += P V of 64 keys done; the next chunk's S may overwrite P
 //   item_full, item_free[i]  an item is known; every role has read it
 #include <math.h>
 
@@ -593,9 +598,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       // ================================================================ products
       // Per tile one warp issues S and one P V: an issuing warp is held up for
       // hundreds of clocks by each of its commits, so the two streams are kept
-      // apart and commit nothing that another barrier already tells (the S warp,
-      // which waits for O of chunk c before S of chunk c + 1, hands chunk c's K
-      // and V stages back with plain arrivals).
+      // apart and commit nothing that another barrier already tells (a K stage
+      // goes back once S is seen, a V stage once O is, by plain arrivals).
       const int t = (warp - 10) & 1;
       const uint32_t t_s = tmem + t * kPaKeys, t_o = tmem + kPaTmemO + t * D;
       // a descriptor's start address is address >> 4 in its low 14 bits; every
