@@ -17,8 +17,8 @@
 // double division for them made the write 87 us where it is now 24.2.
 //
 // Measured (8 heads, d = 128, bf16): 16 x 1024 tokens written in 24.2 us (85 MB,
-// 3.5 TB/s: the arithmetic, not the memory), the same read back in 15.5 us (5.5
-// TB/s, 81 % of the measured copy rate); 64 tokens in 2.0 us, a launch's time.
+// 3.5 TB/s: the arithmetic, not the memory), the same read back in 15.9 us (5.4
+// TB/s, 79 % of the measured copy rate); 64 tokens in 2.0 us, a launch's time.
 #include <algorithm>
 
 #include "int4_common.cuh"
@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(kWriteThreads, kWriteCtas)
 }
 
 // p + lo, inexact in 32 bits, rounded to odd: rounded once more to 16 bits it
-// is the exact sum's rounding.  Rare, and a call.
-__device__ __noinline__ float sum_to_odd(float p, float lo) {
+// is the exact sum's rounding.
+__device__ __forceinline__ float sum_to_odd(float p, float lo) {
   const float s = p + lo, back = s - p, off = (p - (s - back)) + (lo - back);
   const uint32_t b = __float_as_uint(s);
   if (off == 0.f || (b & 1u) || !isfinite(s)) return s;
@@ -297,6 +297,7 @@ __global__ void __launch_bounds__(32 * kGatherWarps) gather_int4_kernel(GatherIn
     }
   }
   const int64_t to = (((int64_t)b * a.Hkv + h) * a.MBS + blk) * (kBlockSize * D) + r0 * D + 8 * j;
+  uint32_t odd = 0u;   // bit 2 i + which: a row that is rounded below
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     T* dst = static_cast<T*>(which ? a.v_dense : a.k_dense) + to;
@@ -306,25 +307,39 @@ __global__ void __launch_bounds__(32 * kGatherWarps) gather_int4_kernel(GatherIn
       const float step = Bits16<T>::to_f32(pair & 0xffffu), lo = Bits16<T>::to_f32(pair >> 16);
       // an integer below 2^23 in the fraction of 2^23, less 2^23: the code as
       // fp32 without a conversion
-      uint32_t o[4];
       // lo + n step has a few more bits than 16 for a lo of some size, and is
       // exact in 32; below step / 256 it need not be
-      if (lo != 0.f && fabsf(lo) * 256.f < step) {
+      if (lo != 0.f && fabsf(lo) * 256.f < step) odd |= 1u << (2 * i + which);
+      uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = Mma<T>::pack(sum_to_odd((float)((c >> (8 * e)) & 15u) * step, lo),
-                              sum_to_odd((float)((c >> (8 * e + 4)) & 15u) * step, lo));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float n0 = __uint_as_float(0x4b000000u | ((c >> (8 * e)) & 15u)) - 8388608.f;
-          const float n1 = __uint_as_float(0x4b000000u | ((c >> (8 * e + 4)) & 15u)) - 8388608.f;
-          o[e] = Mma<T>::pack(fmaf(n0, step, lo), fmaf(n1, step, lo));
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float n0 = __uint_as_float(0x4b000000u | ((c >> (8 * e)) & 15u)) - 8388608.f;
+        const float n1 = __uint_as_float(0x4b000000u | ((c >> (8 * e + 4)) & 15u)) - 8388608.f;
+        o[e] = Mma<T>::pack(fmaf(n0, step, lo), fmaf(n1, step, lo));
       }
       // rows behind the context: code, step and lo are 0, and so are the values
       __stcs(reinterpret_cast<uint4*>(dst + i * (32 / kLanes) * D),
              make_uint4(o[0], o[1], o[2], o[3]));
+    }
+  }
+  // once more for the rare rows, from memory (kept out of the loop above, where
+  // it costs registers: 16.3 against 15.9 us)
+  while (odd) {
+    const int bit = __ffs(odd) - 1, i = bit >> 1, which = bit & 1;
+    odd &= odd - 1;
+    const int row = i * (32 / kLanes) + r0;
+    const unsigned char* rp = which ? vr : kr;
+    const uint32_t pair = __ldg(reinterpret_cast<const uint32_t*>(rp + 8 * D) + row);
+    const float step = Bits16<T>::to_f32(pair & 0xffffu), lo = Bits16<T>::to_f32(pair >> 16);
+    T* dst = static_cast<T*>(which ? a.v_dense : a.k_dense) + to + i * (32 / kLanes) * D;
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e) {
+      // elements 2e and 2e + 1: a byte of the K row, of word e / 2 of the V pair
+      const unsigned char* p = which ? rp + (row >> 1) * D + 8 * j + 4 * (e >> 1) + 2 * (row & 1) + (e & 1)
+                                     : rp + row * (D / 2) + 4 * j + e;
+      const uint32_t c = __ldg(p);
+      reinterpret_cast<uint32_t*>(dst)[e] = Mma<T>::pack(
+          sum_to_odd((float)(c & 15u) * step, lo), sum_to_odd((float)(c >> 4) * step, lo));
     }
   }
 }

@@ -36,6 +36,17 @@
 // (m, l, o) partials, merged by a second kernel.  Runs are equal whatever the
 // mix of lengths, without a queue or atomics, so results do not depend on
 // timing.
+//
+// Measured (8 kv heads, d = 128, fp16; event times): 64 contexts of 128 .. 8192
+// tokens 34.7 us = 4.0 TB/s of the codes and pairs, 59 % of the measured copy
+// rate; a batch-256 mix at 32 q heads 63.3 us = 61 %; 4 short contexts 9.2 us.
+// What bounds it: the first data comes 4 us after the call's start and the merge
+// takes 3.5 us; between them 5.5 TB/s, the rate of the copies themselves: with
+// no arithmetic at all the first version of this split took 34.5 us where it
+// took 37.0.  The short contexts are two launches and a merge.  Other ways to
+// bring the records in, at the same three: bulk copies per warp 33.7, 74.8, 9.5
+// us; bulk copies into one ring a team 35.0, 74.3, 9.7; one warp per run of
+// one KV head, without teams, 37.2, 69.5, 9.3.
 #include <math.h>
 
 #include <algorithm>
