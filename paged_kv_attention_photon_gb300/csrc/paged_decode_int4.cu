@@ -328,8 +328,9 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
       sum += __shfl_xor_sync(0xffffffffu, sum, off);
     }
-    // the row is scaled by a power of two to [2^14, 2^15): fp16 then holds
-    // every fp16 or bf16 q, and its 16th, to 2^-25 of that
+    // the row's largest element is scaled by a power of two to [2^14, 2^15): fp16
+    // then holds q and its 16th exactly down to 2^-24 of the largest, and what
+    // is smaller to 2^-25, less than 2^-35 of it
     const int ex = (int)((__float_as_uint(big) >> 23) & 255u);
     const float up = pow2_biased(268 - ex);   // 2^(14 - (ex - 127))
     // with a negative scale q is turned round, so that the largest score is
