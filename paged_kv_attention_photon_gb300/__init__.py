@@ -208,14 +208,21 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_raw_stream = _raw_device = None
+
+
 def _current_stream() -> int:
     """torch.cuda.current_stream().cuda_stream, without building the Stream
     object where torch offers the bare handle (3 us of a 10 us call)."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None or not torch.cuda.is_initialized():
-        return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+    global _raw_stream, _raw_device
+    if _raw_stream is None:
+        import torch
+        raw, device = (getattr(torch._C, name, None)
+                       for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if raw is None or device is None or not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        _raw_stream, _raw_device = raw, device
+    return _raw_stream(_raw_device())
 
 
 def _stream(stream) -> Optional[int]:
@@ -224,6 +231,26 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+_calls = None
+
+
+def _native():
+    """The module of csrc/python/binding.cpp, bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        lib = _load()
+        if not os.path.exists(_build.BINDING_PATH):
+            raise ImportError(f"{_build.BINDING_PATH} is missing: build it with "
+                              "paged_kv_attention_photon_gb300.build() (needs nvcc)")
+        from . import _binding
+        for name in ("photon_cache_write_int4", "photon_paged_gather_int4",
+                     "photon_paged_decode_int4", "photon_qk_norm_rope",
+                     "photon_prompt_attention"):
+            _binding.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
+        _calls = _binding
+    return _calls
 
 
 def _check(status: int, where: str) -> None:
@@ -371,19 +398,20 @@ def photon_cache_write_int4(k, k_stride: int, v, v_stride: int, slot_mapping, nu
                             k_cache, v_cache, shape: PagedShape, stream=None) -> None:
     """Quantising cache write into 4-bit pools (uint8 tensors); the strides are
     elements from one token's rows to the next one's, 0 = packed."""
-    _check(_load().photon_cache_write_int4(_ptr(k), int(k_stride), _ptr(v), int(v_stride),
-                                           _ptr(slot_mapping), int(num_tokens), _ptr(k_cache),
-                                           _ptr(v_cache), ctypes.byref(shape), _stream(stream)),
-           "photon_cache_write_int4")
+    status = (_calls or _native()).photon_cache_write_int4(
+        k, k_stride, v, v_stride, slot_mapping, num_tokens, k_cache, v_cache, shape,
+        _stream(stream))
+    if status:
+        raise PhotonError(status, "photon_cache_write_int4")
 
 
 def photon_paged_gather_int4(k_cache, v_cache, block_tables, context_lens, k_dense, v_dense,
                              shape: PagedShape, stream=None) -> None:
     """The contexts' rows of 4-bit pools as values of the storage type."""
-    _check(_load().photon_paged_gather_int4(_ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                                            _ptr(context_lens), _ptr(k_dense), _ptr(v_dense),
-                                            ctypes.byref(shape), _stream(stream)),
-           "photon_paged_gather_int4")
+    status = (_calls or _native()).photon_paged_gather_int4(
+        k_cache, v_cache, block_tables, context_lens, k_dense, v_dense, shape, _stream(stream))
+    if status:
+        raise PhotonError(status, "photon_paged_gather_int4")
 
 
 def photon_paged_decode_int4_workspace_size(shape: PagedShape) -> int:
@@ -394,12 +422,11 @@ def photon_paged_decode_int4(q, k_cache, v_cache, block_tables, context_lens, sc
                              workspace, workspace_bytes: int, shape: PagedShape,
                              stream=None) -> None:
     """Paged decode over 4-bit K/V pools (uint8 tensors)."""
-    _check(_load().photon_paged_decode_int4(_ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                            _ptr(block_tables), _ptr(context_lens),
-                                            float(scale), _ptr(out), _ptr(workspace),
-                                            int(workspace_bytes), ctypes.byref(shape),
-                                            _stream(stream)),
-           "photon_paged_decode_int4")
+    status = (_calls or _native()).photon_paged_decode_int4(
+        q, k_cache, v_cache, block_tables, context_lens, scale, out, workspace, workspace_bytes,
+        shape, _stream(stream))
+    if status:
+        raise PhotonError(status, "photon_paged_decode_int4")
 
 
 def photon_qk_norm_rope(q, q_stride: int, k, k_stride: int, q_weight, k_weight, eps: float,
@@ -408,11 +435,11 @@ def photon_qk_norm_rope(q, q_stride: int, k, k_stride: int, q_weight, k_weight, 
                         shape: PagedShape, stream=None) -> None:
     """Per-head RMS norm of q and k (weight None: no norm) and their rotation by
     position, on one axis or several; strides in elements, 0 = packed."""
-    _check(_load().photon_qk_norm_rope(
-        _ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(q_weight), _ptr(k_weight),
-        float(eps), _ptr(positions), _ptr(rope_cos_sin), int(max_positions),
-        ctypes.byref(axes), int(num_tokens), _ptr(q_out), int(q_out_stride), _ptr(k_out),
-        int(k_out_stride), ctypes.byref(shape), _stream(stream)), "photon_qk_norm_rope")
+    status = (_calls or _native()).photon_qk_norm_rope(
+        q, q_stride, k, k_stride, q_weight, k_weight, eps, positions, rope_cos_sin, max_positions,
+        axes, num_tokens, q_out, q_out_stride, k_out, k_out_stride, shape, _stream(stream))
+    if status:
+        raise PhotonError(status, "photon_qk_norm_rope")
 
 
 def photon_prompt_attention(q, q_stride: int, k, k_stride: int, v, v_stride: int, query_start,
@@ -420,10 +447,11 @@ def photon_prompt_attention(q, q_stride: int, k, k_stride: int, v, v_stride: int
                             out_stride: int, shape: PagedShape, stream=None) -> None:
     """Causal attention of packed whole prompts over their own K and V rows;
     strides in elements from token to token, 0 = packed."""
-    _check(_load().photon_prompt_attention(
-        _ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(v), int(v_stride),
-        _ptr(query_start), int(num_tokens), int(max_query_len), float(scale), _ptr(out),
-        int(out_stride), ctypes.byref(shape), _stream(stream)), "photon_prompt_attention")
+    status = (_calls or _native()).photon_prompt_attention(
+        q, q_stride, k, k_stride, v, v_stride, query_start, num_tokens, max_query_len, scale, out,
+        out_stride, shape, _stream(stream))
+    if status:
+        raise PhotonError(status, "photon_prompt_attention")
 
 
 def photon_paged_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, scale: float,

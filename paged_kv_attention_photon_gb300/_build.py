@@ -1,4 +1,5 @@
-"""Build libphoton_paged.so in-tree with nvcc for sm_103a (GB300).
+"""Build libphoton_paged.so in-tree with nvcc for sm_103a (GB300), and the Python
+module _binding.so beside it.
 
 One object per translation unit, compiled in parallel, then linked into a
 shared library next to this file.  Rebuilds only when a source is newer than
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from typing import List, Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libphoton_paged.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+BINDING_SRC = os.path.join(CSRC, "python", "binding.cpp")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -41,14 +45,14 @@ def sources() -> List[str]:
 
 
 def _deps() -> List[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -72,9 +76,20 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
             sys.stderr.write(r.stderr)
         return obj
 
+    def compile_binding() -> str:
+        out = BINDING_PATH + f".tmp{os.getpid()}"
+        cmd = [nvcc, "-O2", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-I" + INCLUDE,
+               "-I" + sysconfig.get_paths()["include"], "-o", out, BINDING_SRC]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"the Python binding failed (it needs Python's headers):\n{r.stderr}")
+        return out
+
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(2, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        os.replace(binding.result(), BINDING_PATH)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH_FLAGS + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

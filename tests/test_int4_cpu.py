@@ -27,7 +27,7 @@ def _shape(**over):
 
 
 BAD_SHAPES = [(dict(dtype=P.F32), UNSUPPORTED), (dict(head_dim=96), UNSUPPORTED),
-              (dict(block_size=32), UNSUPPORTED), (dict(num_q_heads=24), UNSUPPORTED),
+              (dict(block_size=32), UNSUPPORTED), (dict(num_q_heads=40), UNSUPPORTED),
               (dict(num_q_heads=12), INVALID), (dict(num_seqs=-1), INVALID)]
 
 
@@ -193,3 +193,38 @@ def test_oracle_round_trip(dtype, keys):
     built = I.build_pools(5, contexts=[21], hkv=hkv, d=d, dtype=dtype)
     back = I.load_rows(built[0 if keys else 1], keys, d, built[2][0], 21, dtype)
     assert np.isfinite(back).all() and np.abs(back).max() > 1
+
+
+def test_calls_convert_their_arguments(lib):
+    """The entry points of the compiled binding: what it takes for an address, a number and a
+    structure, and what it refuses; num_tokens 0 launches nothing."""
+    shape, axes = _shape(), P.RopeAxes.make([64])
+
+    def call(q=FAKE, tokens=0, eps=1e-6, weight=None, sh=shape, ax=axes, stream=0):
+        P.photon_qk_norm_rope(q, 0, FAKE, np.int64(0), weight, FAKE, eps, FAKE, FAKE, 16, ax,
+                              tokens, FAKE2, 0, FAKE2, 0, sh, stream)
+
+    class Held:
+        def data_ptr(self):
+            return FAKE
+
+    for ok in (dict(), dict(q=Held()), dict(q=None), dict(q=2 ** 64 - 16), dict(tokens=np.int32(0)),
+               dict(tokens=0.0), dict(eps=1), dict(eps=np.float32(0.5)), dict(weight=Held())):
+        call(**ok)
+    for error, bad in ((AttributeError, dict(q="address")), (OverflowError, dict(q=2 ** 64)),
+                       (OverflowError, dict(tokens=2 ** 31)), (OverflowError, dict(tokens=-2 ** 31 - 1)),
+                       (TypeError, dict(tokens=None)), (TypeError, dict(eps=None)),
+                       (TypeError, dict(sh=None)), (TypeError, dict(sh=axes)),
+                       (TypeError, dict(ax=bytes(3))), (AttributeError, dict(stream="s"))):
+        with pytest.raises(error):
+            call(**bad)
+    with pytest.raises(P.PhotonError) as e:
+        call(eps=float("inf"))
+    assert e.value.status == INVALID
+    with pytest.raises(OverflowError):     # a workspace's size has no sign
+        P.photon_paged_decode_int4(FAKE, FAKE, FAKE, FAKE, FAKE, 0.1, FAKE2, FAKE, -1, shape, 0)
+    native = P._native()
+    with pytest.raises(TypeError):
+        native.photon_qk_norm_rope(1, 2)
+    with pytest.raises(ValueError):
+        native.bind("photon_other", 1)
