@@ -233,7 +233,7 @@ class Decode:
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (4, 1), (8, 1), (24, 3)])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (4, 1), (8, 1), (12, 3)])
 def test_decode(dtype, d, hq, hkv):
     c = Decode(31 + hq, [0, 1, 15, 16, 17, 63, 64, 65, 300, 1, 0, 129], hq, hkv, d, dtype)
     for _ in range(2):   # the workspace's last contents do not matter
@@ -245,6 +245,16 @@ def test_decode(dtype, d, hq, hkv):
 @pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (8, 1, 128)])
 def test_decode_one_long_context(hq, hkv, d):
     c = Decode(41, [20011], hq, hkv, d, W.DTYPE_F16)
+    c.run()
+    ok_status()
+    c.check()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 8, 128), (16, 16, 64), (64, 8, 64), (12, 6, 64),
+                                      (12, 12, 128)])
+def test_decode_many_heads(hq, hkv, d):
+    """8, 4 and 2 KV heads of a block read together."""
+    c = Decode(37, [0, 33, 700, 16, 1], hq, hkv, d, W.DTYPE_F16)
     c.run()
     ok_status()
     c.check()

@@ -194,6 +194,33 @@ def test_rejected_prompts():
     assert (c.raw()[30:] == -1).all()
 
 
+def test_offsets_past_32_bits():
+    """Rows 4 MB apart: the last ones lie more than 4 GiB behind the first."""
+    c = Case([1000, 0, 110], 4, 2, 64, W.DTYPE_F16, fused=True)
+    width, c.stride = c.all.shape[1] * c.d, 1 << 21
+    big = torch.empty((c.T, c.stride), dtype=torch.float16, device="cuda")
+    big[:, :width] = c.on[0].reshape(c.T, width)
+    out = big[:, width:width + c.hq * c.d]
+    out.fill_(0)
+    at = [big, big[:, c.hq * c.d:], big[:, (c.hq + c.hkv) * c.d:]]
+    P.photon_prompt_attention(at[0], c.stride, at[1], c.stride, at[2], c.stride, c.on_starts, c.T,
+                              c.longest, c.scale, out, c.stride, c.shape)
+    c.out.copy_(out.contiguous().view(torch.int16).reshape(c.out.shape))
+    c.check()
+
+
+def test_two_streams_at_once():
+    cases = [Case([300, 90, 700], 8, 4, 128, W.DTYPE_F16), Case([500] * 4, 8, 2, 64, W.DTYPE_BF16)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, stream in zip(cases, streams):
+            c.run(stream)
+    torch.cuda.synchronize()
+    for c in cases:
+        c.check()
+
+
 def test_captured_and_on_another_stream():
     c = Case([100, 60], 4, 2, 64, W.DTYPE_F16, tail=40)
     e = Case([90], 8, 1, 128, W.DTYPE_BF16)

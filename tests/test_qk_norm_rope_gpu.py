@@ -177,6 +177,20 @@ def test_zero_rows_and_rows_that_are_not_finite():
     assert np.array_equal(bad, want) and np.isfinite(got[1]).all()
 
 
+def test_offsets_past_32_bits():
+    """Rows 4 MB apart, in place: the last ones lie more than 4 GiB behind the first."""
+    c = Case(T=1100, hq=4, hkv=2, d=64, dtype=W.DTYPE_F16, sections=[32], seed=9)
+    stride, width = 1 << 21, 6 * 64
+    big = torch.empty((c.T, stride), dtype=torch.float16, device="cuda")
+    big[:, :width] = dev(c.fused).reshape(c.T, width)
+    k = big[:, 4 * 64:]
+    P.photon_qk_norm_rope(big, stride, k, stride, dev(c.w[0]), dev(c.w[1]), c.eps, dev(c.pos),
+                          c.table, c.max_pos, P.RopeAxes.make([32]), c.T, big, stride, k, stride,
+                          c.shape)
+    got = I.to_f64(host(big[:, :width].reshape(c.T, 6, 64), c.fused), c.dtype)
+    c.check([got[:, :4], got[:, 4:]])
+
+
 def test_captured_and_on_another_stream():
     c = Case(T=9, hq=4, hkv=2, d=64, dtype=W.DTYPE_F16, sections=[32], seed=8)
     side = torch.cuda.Stream()
