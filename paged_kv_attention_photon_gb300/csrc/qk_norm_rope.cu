@@ -12,10 +12,10 @@
 // pair are in one lane and only the sum of squares crosses lanes (2 or 3
 // shuffles).  A warp takes one token, so the (cos, sin) row is loaded once
 // for all of the warp's heads, and three head rows a lane, all loaded before
-// the first is used (with one row a lane in flight: 69 us where it is 35.9).
+// the first is used (with one row a lane in flight: 69 us where it is 35.0).
 //
-// Measured (16 q, 8 kv heads, d = 128, bf16): 16 x 1024 tokens in 35.9 us = 5.6
-// TB/s, 83 % of the measured copy rate; 64 tokens in 2.6 us, a launch's time.
+// Measured (16 q, 8 kv heads, d = 128, bf16): 16 x 1024 tokens in 35.0 us = 5.8
+// TB/s, 85 % of the measured copy rate; 64 tokens in 2.6 us, a launch's time.
 #include "photon_common.cuh"
 #include "qk_norm_rope.cuh"
 
@@ -64,7 +64,9 @@ __device__ __forceinline__ float row_max(float x) {
   return x;
 }
 
-constexpr int kQkThreads = 128;
+// 32, 64, 96, 128, 256: 16 x 1024 tokens in 37.2, 34.6, 35.6, 35.4, 38.5 us, 6190 f32
+// tokens on three axes in 24.2, 24.8, 25.1, 25.3, 26.8
+constexpr int kQkThreads = 64;
 constexpr int kQkHeads = 3;   // head rows a lane takes, all loaded before the first is used
 
 template <typename T, int D, bool kOneAxis>
