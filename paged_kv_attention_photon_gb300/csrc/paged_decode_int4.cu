@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
 #pragma unroll
     for (int i = 0; i < NW * 8; ++i) {
       big = fmaxf(big, fabsf(x[i]));
-      sum += x[i];
+      sum = fmaf(x[i], 9.765625e-4f, sum);   // 2^-10 of it: a row of bf16's largest stays finite
     }
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
     const int ex = (int)((__float_as_uint(big) >> 23) & 255u);
     const float up = pow2_biased(268 - ex);   // 2^(14 - (ex - 127))
     // with a negative scale q is turned round, so that the largest score is
-    // the largest sum; a zero scale is a tiny one (every weight is 1)
+    // the largest sum
     const float sc = a.qscale < 0.f ? -up : up;
     const float s16 = sc * 0.0625f;
 #pragma unroll
@@ -345,9 +345,13 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
         bq[j][h][0] = Mma<__half>::pack(w[0] * sc, w[4] * sc);
         bq[j][h][1] = Mma<__half>::pack(w[1] * s16, w[5] * s16);
       }
-    // acc = 2^-24 sc (q . n), so lo enters as lo sum(q) 2^-24 sc; 1 / up is exact
-    const float k1 = fmaxf(fabsf(a.qscale), 1e-37f) * (16777216.f * (1.f / up));
-    const float k2 = sum * (sc * 5.9604645e-8f);
+    // acc = 2^-24 sc (q . n), so lo enters as lo sum(q) 2^-24 sc; 1 / up is exact.
+    // The factor stays positive and finite, whatever the scale and q: with a
+    // zero scale or a zero row every weight is 1, but the -inf of a key that
+    // is not there has to remain one (-inf x 0 is NaN), and so has a score of 0
+    // (0 x inf).
+    const float k1 = fminf(fmaxf((fabsf(a.qscale) * 16777216.f) * (1.f / up), 1e-37f), 1.7014118e38f);
+    const float k2 = sum * (sc * 6.1035156e-5f);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int col = 2 * t + i;

@@ -450,3 +450,39 @@ def test_decode_of_empty_contexts_only():
     c.run()
     ok_status()
     assert not c.got().any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", [0.0, 1e-20, -1e-20, 0.125])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (8, 1, 128)])
+def test_decode_zero_and_tiny_queries(dtype, scale, hq, hkv, d):
+    """Rows of q that are zero, or (bf16) far below 1: every weight is 1 or nearly so, and keys
+    that are not there weigh nothing, whatever part of the last 32 they are."""
+    c = Decode(97, [5, 16, 33, 64, 70, 200], hq, hkv, d, dtype)
+    c.scale = scale
+    q = I.to_f64(c.q, dtype)
+    q[:, 1::2] = 0.0
+    q[1:4, ::2] *= 2.0 ** -60
+    c.q = I.narrow(q, dtype)
+    c.up()
+    c.run()
+    ok_status()
+    c.check()
+    c.bt[5, 3] = c.kp.shape[0]     # and a block that is not in the pool
+    c.up()
+    c.run()
+    assert P.photon_get_last_device_error() == (6, 1)
+    assert np.isfinite(c.got()).all()
+
+
+@pytest.mark.parametrize("size", [2.0 ** 112, 2.0 ** 118, 2.0 ** 121])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (8, 1, 128)])
+def test_decode_queries_near_the_types_largest(size, hq, hkv, d):
+    """bf16 rows whose scale brings the scores back to ordinary ones."""
+    c = Decode(101, [40, 17, 129], hq, hkv, d, W.DTYPE_BF16)
+    c.q = I.narrow(np.abs(I.to_f64(c.q, c.dtype)) * size, c.dtype)
+    c.scale /= size
+    c.up()
+    c.run()
+    ok_status()
+    c.check()
