@@ -24,6 +24,13 @@
 // swizzle, no ldmatrix.  P^T is the score fragment packed and transposed with
 // movmatrix; p_j step_j enters as its fp16 rounding plus the residual: for
 // G <= 4 the residual rides in the unused columns 4 .. 7 of the same product.
+// fp16 ends at 2^-24, and what p_j step_j loses there the sums of p_j and p_j
+// lo_j still count, so that many keys of little weight each (the tail behind a
+// first key that holds nearly all) would pull the output towards their lo: by
+// up to keys x 2^-25 of half a row's range, 1.5e-3 with 13900 keys at e^-17.
+// So columns 4 .. 7 hold 2^14 times the residual, and with G = 8, where both
+// go to the same sums, the weights fill fp16's upper end instead (kOne,
+// kSlack): nothing above 2^-39 (G = 8: 2^-37) of the largest weight is lost.
 //
 // Work: a team of up to 8 neighbouring warps takes as many neighbouring KV
 // heads, a warp each, through the same blocks, so that what it reads of a block
@@ -69,6 +76,7 @@ constexpr int kI4MinRun = 6;
 // no exponent is inf - inf.
 constexpr float kI4NoMax = -3e38f;
 constexpr int kI4StageUnits = 2;          // consecutive blocks of a pair in a stage
+constexpr float kI4Rest = 16384.f;        // columns 4 .. 7: the residuals times this
 
 template <int D>
 struct I4Cfg {
@@ -115,6 +123,10 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
     paged_decode_int4_kernel(const DecodeInt4Args a) {
   using C = I4Cfg<D>;
   constexpr int NW = D / 32;        // code words of a lane per row (or row pair)
+  // Weights stay below 2^kSlack, V steps, once a power of two has brought the
+  // largest below kOne, below kMost; their product is below 2^15 (G = 8), 2^11.
+  constexpr float kSlack = kFull ? 2.f : 8.f;
+  constexpr float kOne = kFull ? 4096.f : 1.f, kMost = kFull ? 8192.f : 8.f;
   extern __shared__ __align__(16) unsigned char i4_smem[];
   __shared__ int pre[kI4Threads];      // where a thread's sequences begin on the line
   __shared__ int ctx_first[kI4Threads];   // the lengths, when a thread has one sequence
@@ -303,9 +315,9 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
   uint32_t bq[NW][2][2];   // Q^T fragments: column g, products 2j and 2j + 1 of word j
   float c1[2], c2[2];      // score = (step acc + lo c2) c1, c1 > 0
   float m[2], l[2], z[2];  // running max, sum of weights, sum of weights x lo of V
-  float limit[2];          // (m + 8) / c1: what a score / c1 may reach before m moves
+  float limit[2];          // (m + kSlack) / c1: what a score / c1 may reach before m moves
   float o[NW][2][4];       // O^T: dims (D / 8) g + 4j + 2h (rows g) and + 1 (rows g + 8)
-  float vs = 0.f;          // power of two that the V steps are brought near 1 with
+  float vs = 0.f;          // power of two that the V steps are brought near kOne with
   auto begin_pair = [&]() {
     const int s = kFull ? g : g & 3;
     float x[NW * 8];
@@ -435,13 +447,13 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
         }
       }
     }
-    // The maximum only moves when a score passes it by more than 2^8 (then
-    // weights stay below 2^8), the V steps' power of two when a step passes
-    // 8; what is summed so far is rescaled then.  Both cancel in O / l.
+    // The maximum only moves when a score passes it by more than kSlack (then
+    // weights stay below 2^kSlack), the V steps' power of two when a step passes
+    // kMost; what is summed so far is rescaled then.  Both cancel in O / l.
     const float y0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
     const float y1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
     const float top = fmaxf(fmaxf(step0[0], step8[0]), fmaxf(step0[1], step8[1]));
-    if (__any_sync(0xffffffffu, y0 > limit[0] || y1 > limit[1] || top * vs > 8.f)) {
+    if (__any_sync(0xffffffffu, y0 > limit[0] || y1 > limit[1] || top * vs > kMost)) {
       float n0 = fmaxf(m[0], y0 * c1[0]), n1 = fmaxf(m[1], y1 * c1[1]);
       float sm = top;
 #pragma unroll
@@ -452,16 +464,16 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
       }
       const float r0 = softmax_exp2(m[0] - n0), r1 = softmax_exp2(m[1] - n1);
       float up = 1.f;
-      if (sm * vs > 1.f) {
-        // 2^-(exponent of sm + 1)
-        const float next = pow2_biased(253 - (int)((__float_as_uint(sm) >> 23) & 255u));
+      if (sm * vs > kOne) {
+        // kOne x 2^-(exponent of sm + 1)
+        const float next = pow2_biased(253 + (kFull ? 12 : 0) - (int)((__float_as_uint(sm) >> 23) & 255u));
         up = next * (1.f / vs);
         vs = next;
       }
       m[0] = n0;
       m[1] = n1;
-      limit[0] = (n0 + 8.f) / c1[0];
-      limit[1] = (n1 + 8.f) / c1[1];
+      limit[0] = (n0 + kSlack) / c1[0];
+      limit[1] = (n1 + kSlack) / c1[1];
       l[0] *= r0, z[0] *= r0;
       l[1] *= r1, z[1] *= r1;
 #pragma unroll
@@ -497,11 +509,11 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
         d0 = movmatrix_trans(Mma<__half>::pack(w[0] - r01.x, w[1] - r01.y));
         d1 = movmatrix_trans(Mma<__half>::pack(w[2] - r23.x, w[3] - r23.y));
       } else {
-        const float rest = t >= 2 ? 1.f : 0.f;
+        const float mul = t >= 2 ? kI4Rest : 1.f, rest = t >= 2 ? -kI4Rest : 0.f;
         b0 = movmatrix_trans(
-            Mma<__half>::pack(fmaf(-rest, r01.x, w[0]), fmaf(-rest, r01.y, w[1])));
+            Mma<__half>::pack(fmaf(rest, r01.x, w[0] * mul), fmaf(rest, r01.y, w[1] * mul)));
         b1 = movmatrix_trans(
-            Mma<__half>::pack(fmaf(-rest, r23.x, w[2]), fmaf(-rest, r23.y, w[3])));
+            Mma<__half>::pack(fmaf(rest, r23.x, w[2] * mul), fmaf(rest, r23.y, w[3] * mul)));
       }
 #pragma unroll
       for (int j = 0; j < NW; ++j) {
@@ -538,7 +550,10 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if constexpr (!kFull) o[j][h][i] += __shfl_xor_sync(0xffffffffu, o[j][h][i], 2);
+          if constexpr (!kFull) {
+            const float other = __shfl_xor_sync(0xffffffffu, o[j][h][i], 2);
+            o[j][h][i] = fmaf(other, 1.f / kI4Rest, o[j][h][i]);   // lanes t < 2 go on with it
+          }
         }
 #pragma unroll
     for (int j = 0; j < NW; ++j)

@@ -486,3 +486,50 @@ def test_decode_queries_near_the_types_largest(size, hq, hkv, d):
     c.run()
     ok_status()
     c.check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("keys", [1568, 13900])
+@pytest.mark.parametrize("hq,hkv,d", [(1, 1, 64), (4, 1, 128), (8, 1, 64), (8, 1, 128)])
+def test_decode_many_keys_of_little_weight(dtype, keys, hq, hkv, d):
+    """A first key holds nearly all of the weight and has a small V; each key behind it weighs
+    e^-17 to e^-19 and has an ordinary V.  The sequences share one table, and are so many that
+    a run of the split has as many keys as a context.
+
+    Bound: every sum of keys / 16 products of 16 keys in fp32 may lose 2^-22 of the magnitudes
+    M = sum p (|lo| + 15 step) a product; then the output's rounding."""
+    rng = np.random.default_rng(keys + hq)
+    scale = 8.0 / d
+    # constant K rows, so scores are exact: 17 (1 + s / 64) for the first key, 0 for the others
+    k = np.zeros((keys, 1, d))
+    k[0] = 2.125
+    v = rng.standard_normal((keys, 1, d))
+    v[0] *= 0.003
+    rows = [I.quantise(I.narrow(x, dtype), dtype) for x in (k, v)]
+    blocks = (keys + 15) // 16
+    pools = [np.full((blocks, 1, I.record_bytes(d)), 0xFF, dtype=np.uint8) for _ in range(2)]
+    for which, (codes, step, lo) in enumerate(rows):
+        for j in range(keys):
+            I.store_row(pools[which], which == 0, d, j // 16, 0, j % 16, codes[j, 0], step[j, 0],
+                        lo[j, 0])
+    seqs = 2600
+    q = np.ones((hq, d)) * (1 + np.arange(hq) / 64)[:, None]
+    on_q = dev(np.broadcast_to(I.narrow(q, dtype), (seqs, hq, d)))
+    table = dev(np.broadcast_to(np.arange(blocks, dtype=np.int32), (seqs, blocks)))
+    shape = shape_for(seqs=seqs, hq=hq, hkv=1, d=d, nb=blocks, mbs=blocks, dtype=dtype)
+    n = P.photon_paged_decode_int4_workspace_size(shape)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    out = torch.full((seqs, hq, d), -1, dtype=torch.int16, device="cuda")
+    P.photon_paged_decode_int4(on_q, dev(pools[0]), dev(pools[1]), table,
+                               dev(np.full(seqs, keys, np.int32)), scale, out, ws, n, shape)
+    ok_status()
+    got = I.to_f64(host(out, np.zeros((seqs, hq, d), np.float16 if dtype == W.DTYPE_F16 else np.uint16)),
+                   dtype)
+    codes, step, lo = (x[:, 0] for x in rows[1])
+    value, size = I.values(codes, step, lo, dtype), np.abs(I.to_f64(lo, dtype)) + 15 * I.to_f64(step, dtype)
+    for s in range(hq):
+        p = np.exp(scale * (I.to_f64(I.narrow(k, dtype), dtype)[:, 0] @ q[s] - 2.125 * q[s].sum()))
+        want = (p @ value) / p.sum()
+        tol = keys / 16 * 2.0 ** -22 * (p @ size)
+        tol += I.EPS[dtype] / 2 * (np.abs(want) + tol) + (2.0 ** -25 if dtype == W.DTYPE_F16 else 0.0)
+        assert (np.abs(got[:, s] - want) <= tol).all(), (np.abs(got[:, s] - want) / tol).max()
