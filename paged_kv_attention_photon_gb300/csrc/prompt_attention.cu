@@ -54,6 +54,11 @@
 //   s_full[t][h]         S of 64 keys        p_full[t][h]        their P written
 //   o_done[t][h]         O += P V of 64 keys done; the next chunk's S may overwrite P
 //   item_full, item_free[i]  an item is known; every role has read it
+// Where a wait runs out the CTA gives up, and what it has in flight still lands
+// first: copies write its shared memory, products its tensor memory, and both
+// arrive on its barriers.  Each warp waits (bounded) for its own: the copying
+// ones on the barriers of their last copies, the issuing ones on
+//   drained[i]           every product that the warp has issued is done
 #include <math.h>
 
 #include <algorithm>
@@ -234,7 +239,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   extern __shared__ unsigned char pa_smem_raw[];
   __shared__ __align__(8) uint64_t k_full[SK], k_free[SK], v_full[SV], v_free[SV],
       q_full[kPaTiles], q_free[kPaTiles], s_full[kPaTiles][2], p_full[kPaTiles][2], o_done[kPaTiles][2],
-      v_tail, item_full[kPaItems], item_free[kPaItems];
+      v_tail, item_full[kPaItems], item_free[kPaItems], drained[2 * kPaTiles];
   __shared__ int4 items[kPaItems];   // (first token, tokens, KV head, first row); tokens 0: the end
   __shared__ uint32_t tmem_slot;
   __shared__ int gave_up_word;
@@ -269,6 +274,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
     }
     mbar_init(&v_tail, 1);
+    for (int i = 0; i < 2 * kPaTiles; ++i) mbar_init(&drained[i], 1);
     for (int i = 0; i < kPaItems; ++i) {
       mbar_init(&item_full[i], 1);
       mbar_init(&item_free[i], kPaRoles);
@@ -558,8 +564,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           __syncwarp();
           if (fill) {
             ok = pa_wait(&v_tail, tails & 1, gave_up);
+            if (!ok) {
+              (void)mbar_wait_bounded(&v_tail, tails & 1);   // its copy, in flight
+              break;
+            }
             ++tails;
-            if (!ok) break;
             unsigned char* rows = smem + C::kOffV + st * C::kKvBytes;
             for (int i = lane; i < (16 - valid % 16) * (D / 8); i += 32) {
               const int r = valid + i / (D / 8), ch = i % (D / 8);
@@ -703,6 +712,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           }
           chunk0 = uniform(chunk0 + chunks);
         }
+      }
+      if (!ok) {
+        if (leader) tc_commit(&drained[warp - 10]);
+        __syncwarp();
+        (void)mbar_wait_bounded(&drained[warp - 10], 0);
       }
     }
   }
