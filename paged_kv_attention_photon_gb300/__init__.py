@@ -243,7 +243,8 @@ def _native():
         lib = _load()
         if not os.path.exists(_build.BINDING_PATH):
             raise ImportError(f"{_build.BINDING_PATH} is missing: build it with "
-                              "paged_kv_attention_photon_gb300.build() (needs nvcc)")
+                              "paged_kv_attention_photon_gb300.build() (needs nvcc and "
+                              "Python's headers)")
         from . import _binding
         for name in ("photon_cache_write_int4", "photon_paged_gather_int4",
                      "photon_paged_decode_int4", "photon_qk_norm_rope",

@@ -1,9 +1,12 @@
 """Build libphoton_paged.so in-tree with nvcc for sm_103a (GB300), and the Python
-module _binding.so beside it.
+module _binding beside it.
 
 One object per translation unit, compiled in parallel, then linked into a
 shared library next to this file.  Rebuilds only when a source is newer than
 the library.  No cmake, no torch extension machinery.
+
+The library needs nvcc alone.  The module needs Python's headers too; without
+them it is left out, and only the calls that go through it raise.
 """
 from __future__ import annotations
 
@@ -44,16 +47,30 @@ def sources() -> List[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
-def _deps() -> List[str]:
-    return sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
+def _newer(path: str, deps: List[str]) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps)
+
+
+def _headers() -> List[str]:
+    return glob.glob(os.path.join(INCLUDE, "*.h"))
+
+
+def _python_include() -> Optional[str]:
+    """The directory of Python.h, or None where it is not installed."""
+    path = sysconfig.get_paths()["include"]
+    return path if os.path.exists(os.path.join(path, "Python.h")) else None
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB_PATH, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + _headers())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING_PATH, [BINDING_SRC] + _headers())
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return library_up_to_date() and (binding_up_to_date() or _python_include() is None)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
@@ -76,26 +93,35 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
             sys.stderr.write(r.stderr)
         return obj
 
-    def compile_binding() -> str:
-        out = BINDING_PATH + f".tmp{os.getpid()}"
-        cmd = [nvcc, "-O2", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-I" + INCLUDE,
-               "-I" + sysconfig.get_paths()["include"], "-o", out, BINDING_SRC]
+    def link(objs: List[str]) -> None:
+        tmp = LIB_PATH + f".tmp{os.getpid()}"
+        cmd = [nvcc] + ARCH_FLAGS + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"the Python binding failed (it needs Python's headers):\n{r.stderr}")
-        return out
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB_PATH)
 
-    srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(2, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        binding = ex.submit(compile_binding)
-        objs = list(ex.map(compile_one, srcs))
-        os.replace(binding.result(), BINDING_PATH)
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc] + ARCH_FLAGS + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
+    def build_binding() -> None:
+        if os.path.exists(BINDING_PATH):
+            os.remove(BINDING_PATH)   # of older declarations
+        include = _python_include()
+        if include is None:
+            sys.stderr.write("Python.h is not installed: built without the Python module _binding\n")
+            return
+        tmp = BINDING_PATH + f".tmp{os.getpid()}"
+        cmd = [nvcc, "-O2", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-I" + INCLUDE,
+               "-I" + include, "-o", tmp, BINDING_SRC]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"the Python module failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BINDING_PATH)
+
+    with cf.ThreadPoolExecutor(max_workers=max(2, min(len(sources()) + 1, os.cpu_count() or 4))) as ex:
+        binding = None if not force and binding_up_to_date() else ex.submit(build_binding)
+        if force or not library_up_to_date():
+            link(list(ex.map(compile_one, sources())))
+        if binding is not None:
+            binding.result()
     return LIB_PATH
 
 
