@@ -5,8 +5,9 @@ One object per translation unit, compiled in parallel, then linked into a
 shared library next to this file.  Rebuilds only when a source is newer than
 the library.  No cmake, no torch extension machinery.
 
-The library needs nvcc alone.  The module needs Python's headers too; without
-them it is left out, and only the calls that go through it raise.
+The library needs nvcc alone.  The module needs Python's headers too and carries
+the tag of the Python it was built for; without the headers it is left out, and
+only the calls that go through it raise.
 """
 from __future__ import annotations
 
@@ -27,7 +28,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libphoton_paged.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 BINDING_SRC = os.path.join(CSRC, "python", "binding.cpp")
-BINDING_PATH = os.path.join(PKG, "_binding.so")
+BINDING_PATH = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -1,7 +1,8 @@
 """The build's own logic, with a stand-in for nvcc that writes empty outputs: the library needs
-nothing but nvcc, the Python module needs Python's headers."""
+nothing but nvcc, the Python module needs Python's headers and belongs to one Python."""
 import os
 import stat
+import sysconfig
 
 import pytest
 
@@ -63,6 +64,21 @@ def test_a_module_that_does_not_compile_leaves_the_library(place, monkeypatch):
     with pytest.raises(RuntimeError, match="binding.cpp"):
         B.build()
     assert os.path.exists(B.LIB_PATH) and not B.up_to_date()
+
+
+def test_the_module_belongs_to_one_python(place):
+    folder, calls = place
+    assert B.BINDING_PATH.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    B.build()
+    n = len(calls())
+    B.build()
+    assert len(calls()) == n
+    # another Python's module is not taken for this one's
+    os.rename(B.BINDING_PATH, folder / "_binding.cpython-399-other.so")
+    (folder / "_binding.so").write_text("")
+    assert not B.up_to_date()
+    B.build()
+    assert len(calls()) == n + 1 and os.path.exists(B.BINDING_PATH)
 
 
 def test_calls_without_the_module_say_so(place, monkeypatch):
