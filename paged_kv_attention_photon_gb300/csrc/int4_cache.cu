@@ -98,7 +98,9 @@ __device__ __noinline__ float int4_code_exact(float x, float lo, float step) {
 // their bound) all have quotients near -lo / step, so they matter in rows whose
 // -lo / step is near a border (`near`), and there only next to it; they are
 // looked at again, and so is every element of a row with a tiny lo or a step
-// of few bits (`odd`).
+// of few bits (`odd`: an fp16 subnormal; bf16 has fp32's exponents and keeps
+// all its bits, so there only what would leave fp32's own range counts.  16 x
+// 1024 bf16 rows with steps of 3e-5: 24 us, as others; through `odd` 158).
 template <typename T>
 __device__ __forceinline__ uint32_t int4_codes8(const uint4& raw, float lo, float step, float inv,
                                                 float least, bool near, bool odd) {
@@ -217,7 +219,8 @@ __global__ void __launch_bounds__(kWriteThreads, kWriteCtas)
         const float range = hi - lo, at0 = fminf(-lo * inv, 1e6f);
         const float least =
             range * (Bits16<T>::kNan == 0x7e00u ? 4.8828125e-4f : 6.103515625e-5f);
-        const bool odd = (lo != 0.f && fabsf(lo) < least) || !(step >= 6.2e-5f) ||
+        const bool odd = (lo != 0.f && fabsf(lo) < least) ||
+                         !(step >= (Bits16<T>::kNan == 0x7e00u ? 6.2e-5f : 1e-30f)) ||
                          !(range < 1e37f);
         const bool near = odd || fabsf(at0 - rintf(at0)) > 0.49f;
         codes0 = int4_codes8<T>(raw0, lo, step, inv, least, near, odd);

@@ -533,3 +533,24 @@ def test_decode_many_keys_of_little_weight(dtype, keys, hq, hkv, d):
         tol = keys / 16 * 2.0 ** -22 * (p @ size)
         tol += I.EPS[dtype] / 2 * (np.abs(want) + tol) + (2.0 ** -25 if dtype == W.DTYPE_F16 else 0.0)
         assert (np.abs(got[:, s] - want) <= tol).all(), (np.abs(got[:, s] - want) / tol).max()
+
+
+def borders(rng, d):
+    """Rows with steps of exactly 2, odd multiples of 1 lying between two codes, and others."""
+    rows = [np.concatenate([rng.integers(0, 31, d - 2), [0, 30]]) for _ in range(20)]
+    rows += [np.concatenate([rng.integers(-15, 16, d - 2), [-15, 15]]) for _ in range(20)]
+    return np.stack(rows + [rng.standard_normal(d) * 8 for _ in range(200)])
+
+
+@pytest.mark.parametrize("dtype,size", [(W.DTYPE_F16, 2.0 ** -12), (W.DTYPE_F16, 2.0 ** -20)] +
+                         [(W.DTYPE_BF16, 2.0 ** -e) for e in (12, 16, 40, 80, 98, 104, 120)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_write_small_ranges(dtype, size, d):
+    """Steps far below 1, down to where they have few bits (fp16) or fp32 ends (bf16)."""
+    x = I.narrow(borders(np.random.default_rng(int(-np.log2(size))), d)[:, None] * size, dtype)
+    T = x.shape[0]
+    slots = np.arange(T, dtype=np.int64)
+    got = run_write(x, x, slots, T // 16, dtype)
+    ok_status()
+    for a, b in zip(got, want_pools(x, x, slots, T // 16, dtype)):
+        assert np.array_equal(a, b)
