@@ -554,3 +554,33 @@ def test_write_small_ranges(dtype, size, d):
     ok_status()
     for a, b in zip(got, want_pools(x, x, slots, T // 16, dtype)):
         assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("unit", [1.0, 2.0 ** 5, 2.0 ** -3])
+def test_write_elements_that_decide_a_border_by_their_last_bits(dtype, d, unit):
+    """lo is a half-integer number of steps, so an element near 0 is next to a border: zero lies
+    on it (even code), the smallest ones above and below it by less than fp32 keeps of x - lo."""
+    tiny = 2.0 ** -24 if dtype == W.DTYPE_F16 else 2.0 ** -30 * unit
+    rows, where = [], []
+    for below in range(15):          # lo = -(below + 1/2) steps, hi = 15 steps more
+        lo = -(below + 0.5)
+        x = np.linspace(0.25, 0.45, d) * (1 if below < 14 else -1)
+        x[0], x[1] = lo, lo + 15
+        small = [tiny, -tiny, 2 * tiny, -2 * tiny, 0.0]
+        x[2:7] = np.array(small) / unit
+        x[d - 5:] = np.array(small[::-1]) / unit
+        rows.append(x * unit)
+        up, even = below + 1, below + 1 if below % 2 else below
+        where.append([up, below, up, below, even])
+    x = I.narrow(np.stack(rows)[:, None], dtype)
+    codes, step, lo = I.quantise(x, dtype)
+    assert (I.to_f64(step, dtype) == unit).all()
+    # the oracle's own quotient is in 64 bits, which hold lo + 2^-30; checked against the definition
+    assert np.array_equal(codes[:, 0, 2:7], np.array(where))
+    slots = np.arange(15, dtype=np.int64)
+    got = run_write(x, x, slots, 1, dtype)
+    ok_status()
+    for a, b in zip(got, want_pools(x, x, slots, 1, dtype)):
+        assert np.array_equal(a, b)
