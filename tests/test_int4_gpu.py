@@ -584,3 +584,58 @@ def test_write_elements_that_decide_a_border_by_their_last_bits(dtype, d, unit):
     ok_status()
     for a, b in zip(got, want_pools(x, x, slots, 1, dtype)):
         assert np.array_equal(a, b)
+
+
+def packed_pools(k, v, slots, nb, dtype):
+    """want_pools, by arrays."""
+    T, hkv, d = k.shape
+    want = []
+    kept = (slots >= 0) & (slots < nb * 16)
+    blk, row = slots[kept] // 16, slots[kept] % 16
+    for which, x in enumerate((k, v)):
+        pool = np.full((nb, hkv, I.record_bytes(d)), 0xFF, dtype=np.uint8)
+        codes, step, lo = (y[kept] for y in I.quantise(x, dtype))
+        packed = (codes[..., 0::2] | (codes[..., 1::2] << 4)).astype(np.uint8)
+        at = np.arange(d // 2)
+        if which == 0:
+            byte = row[:, None] * (d // 2) + at
+        else:
+            byte = row[:, None] // 2 * d + at // 2 * 4 + row[:, None] % 2 * 2 + at % 2
+        heads = np.arange(hkv)[None, :, None]
+        pool[blk[:, None, None], heads, byte[:, None]] = packed
+        pair = np.stack([step, lo], -1).view(np.uint8).reshape(len(blk), hkv, 4)
+        pool[blk[:, None, None], heads, 8 * d + 4 * row[:, None, None] + np.arange(4)] = pair
+        want.append(pool)
+    return want
+
+
+def test_packed_pools_are_the_oracles():
+    rng = np.random.default_rng(1)
+    for dtype in TYPES:
+        x = I.narrow(rng.standard_normal((30, 3, 64)), dtype)
+        slots = rng.permutation(48)[:30].astype(np.int64)
+        slots[[2, 5]] = -1, 48
+        for a, b in zip(packed_pools(x, x[::-1], slots, 3, dtype), want_pools(x, x[::-1], slots, 3, dtype)):
+            assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hkv", [1, 3, 5, 7, 8, 12])
+def test_write_several_rounds(dtype, d, hkv):
+    """More rows than two rounds of the grid (3 / 2 CTAs per SM of 8 warps, 512 / d rows each a
+    round), with head counts that do not divide a round: a warp's next token and head are carried on."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    round_rows = sms * 3 // 2 * 8 * (512 // d)
+    T = (2 * round_rows + round_rows // 2) // hkv + 1
+    rng = np.random.default_rng(T + d)
+    nb = T // 16 + 2
+    slots = rng.permutation(nb * 16)[:T].astype(np.int64)
+    slots[::97] = -1
+    slots[T - 2] = nb * 16          # a bad slot in the last round
+    fused = I.narrow(rng.standard_normal((T, 2 * hkv, d)) * np.exp(rng.uniform(-3, 3, (T, 1, 1))), dtype)
+    on, stride = dev(fused), 2 * hkv * d
+    got = run_write(fused[:, :hkv], fused[:, hkv:], slots, nb, dtype, stride, stride, on, on[:, hkv:])
+    assert P.photon_get_last_device_error() == (6, 2)
+    for a, b in zip(got, packed_pools(fused[:, :hkv], fused[:, hkv:], slots, nb, dtype)):
+        assert np.array_equal(a, b)
