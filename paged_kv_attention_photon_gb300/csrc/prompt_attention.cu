@@ -165,49 +165,84 @@ __device__ __forceinline__ int pa_tiles_of(const PromptArgs& a, int G, int b) {
   return ((q1 - q0) * G + kPaItemRows - 1) / kPaItemRows;
 }
 
-// The L-th item, by a whole warp; false past the last one.  Item L is KV head
-// L % Hkv of the (L / Hkv)-th (prompt, tile), taken from the highest tile
-// index of any prompt down, prompts in order within one index.  F(x), the
-// number of (prompt, tile) with tile index >= x, falls with x: the tile index
-// is the largest x with F(x) > L / Hkv.  `first` holds pa_tiles_of(lane).
-__device__ __forceinline__ bool pa_locate(const PromptArgs& a, int G, uint32_t L, int first,
-                                          int lane, PaItem& it) {
-  auto tiles = [&](int b0) { return b0 == 0 ? first : pa_tiles_of(a, G, b0 + lane); };
-  auto above = [&](int x) -> uint32_t {   // F(x)
-    int s = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) s += max(0, tiles(b0) - x);
-    return __reduce_add_sync(0xffffffffu, (unsigned)s);
-  };
-  const uint32_t i = L / (uint32_t)a.Hkv;
-  if (i >= above(0)) return false;
-  int lo = 0, hi = (a.max_query_len * G + kPaItemRows - 1) / kPaItemRows;
-  uint32_t f_hi = 0;
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    const uint32_t f = above(mid);
-    if (f > i) {
-      lo = mid;
-    } else {
-      hi = mid;
-      f_hi = f;
-    }
+// Where a warp that looks for items in rising order stands.  Item L is KV head
+// L % Hkv of the (L / Hkv)-th (prompt, tile), taken from the highest tile index
+// of any prompt down, prompts in order within one index.  F(x), the number of
+// (prompt, tile) with tile index >= x, falls with x: the tile index is the
+// largest x with F(x) > L / Hkv.  Both x and the place among x's prompts only
+// move one way, so all items of a CTA together cost a few passes over the
+// lengths for each tile index that it meets.  4096 prompts of 8 .. 32 tokens
+// (16 q, 8 kv heads, d = 128): 0.70 ms; with each item found anew it was 5.7, or
+// 18 under a max_query_len of 16384, growing with the square of the prompts.
+struct PaFinder {
+  int x;                 // tile index
+  uint32_t f, f_above;   // F(x), F(x + 1)
+  uint32_t total;        // F(0)
+  int b0;                // prompts from here on have not been looked at for x ..
+  uint32_t before;       // .. and so many before them have a tile x
+};
+
+// `first` holds pa_tiles_of(lane).
+__device__ __forceinline__ PaFinder pa_finder(const PromptArgs& a, int G, int first, int lane) {
+  int s = first, longest = first;
+  for (int b0 = 32; b0 < a.B; b0 += 32) {
+    const int t = pa_tiles_of(a, G, b0 + lane);
+    s += t;
+    longest = max(longest, t);
   }
-  int r = (int)(i - f_hi), b = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const bool in = tiles(b0) > lo;
+  PaFinder p;
+  p.x = __reduce_max_sync(0xffffffffu, longest);
+  p.total = __reduce_add_sync(0xffffffffu, (unsigned)s);
+  p.f = p.f_above = p.before = 0;
+  p.b0 = 0;
+  return p;
+}
+
+// Item L, not below the last one asked for, by a whole warp; false past the last one.
+__device__ __forceinline__ bool pa_locate(const PromptArgs& a, int G, uint32_t L, int first,
+                                          int lane, PaFinder& p, PaItem& it) {
+  auto tiles = [&](int b0) { return b0 == 0 ? first : pa_tiles_of(a, G, b0 + lane); };
+  const uint32_t i = L / (uint32_t)a.Hkv;
+  if (i >= p.total) return false;
+  if (i >= p.f) {   // a lower tile index, the largest x with F(x) > i
+    int lo = 0, hi = p.x;
+    uint32_t f_lo = p.total, f_hi = p.f;
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      int s = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) s += max(0, tiles(b0) - mid);
+      const uint32_t f = __reduce_add_sync(0xffffffffu, (unsigned)s);
+      if (f > i) {
+        lo = mid;
+        f_lo = f;
+      } else {
+        hi = mid;
+        f_hi = f;
+      }
+    }
+    p.x = lo;
+    p.f = f_lo;
+    p.f_above = f_hi;
+    p.b0 = 0;
+    p.before = 0;
+  }
+  const uint32_t rank = i - p.f_above;   // among the prompts with a tile x
+  int b = 0;
+  for (; p.b0 < a.B; p.b0 += 32) {
+    const bool in = tiles(p.b0) > p.x;
     const unsigned mask = __ballot_sync(0xffffffffu, in);
-    const int c = __popc(mask);
-    if (r < c) {
-      const bool me = in && __popc(mask & ((1u << lane) - 1)) == r;
-      b = b0 + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+    const uint32_t n = __popc(mask);
+    if (rank < p.before + n) {
+      const bool me = in && p.before + __popc(mask & ((1u << lane) - 1)) == rank;
+      b = p.b0 + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
       break;
     }
-    r -= c;
+    p.before += n;
   }
   it.q0 = __ldg(a.query_start + b);
   it.n = __ldg(a.query_start + b + 1) - it.q0;
   it.kvh = (int)(L - i * a.Hkv);
-  it.row0 = lo * kPaItemRows;
+  it.row0 = p.x * kPaItemRows;
   return true;
 }
 
@@ -588,6 +623,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     } else if (warp == 14) {
       // ================================================================ items
       const int first = pa_tiles_of(a, G, lane);
+      PaFinder finder = pa_finder(a, G, first, lane);
       const uint32_t N = gridDim.x;
       for (uint32_t m = 0, run = 0;; ++m, run += N) {
         const int slot = m % kPaItems;
@@ -595,7 +631,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (!ok) break;
         // one item from each run of N, forwards and backwards in turn
         const bool found =
-            pa_locate(a, G, run + (m & 1 ? N - 1 - blockIdx.x : blockIdx.x), first, lane, it);
+            pa_locate(a, G, run + (m & 1 ? N - 1 - blockIdx.x : blockIdx.x), first, lane, finder, it);
         if (lane == 0) {
           items[slot] = found ? make_int4(it.q0, it.n, it.kvh, it.row0) : make_int4(0, 0, 0, 0);
           mbar_arrive(&item_full[slot]);

@@ -266,3 +266,29 @@ def test_equal_to_the_paged_prefill():
                                c.T, max(lens), c.scale, out, ws, nws, shape)
     got = I.to_f64(host(c.out, c.parts()[0]), c.dtype)
     assert np.abs(got - out.double().cpu().numpy()).max() <= 4e-3
+
+
+@pytest.mark.parametrize("longest", [None, 1 << 20])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (8, 4, 128)])
+def test_a_thousand_prompts(hq, hkv, d, longest):
+    """Items found 32 prompts at a time over many rounds: short prompts, empty and rejected ones
+    in long runs, and tile indices that only a few far apart prompts have."""
+    rng = np.random.default_rng(12)
+    lens = [int(x) for x in rng.integers(1, 40, 1100)]
+    lens[64:200] = [0] * 136
+    for b, n in ((0, 300), (33, 1500), (500, 700), (501, 700), (1099, 1100)):
+        lens[b] = n
+    c = Case(lens, hq, hkv, d, W.DTYPE_F16, tail=3)
+    c.run(longest=longest)
+    c.check()
+    # all but the short ones are longer than the bound: rejected, their rows left as they were
+    c.up()
+    c.run(longest=299)
+    assert P.photon_get_last_device_error() == (6, 32)
+    keep = np.array([n < 300 for n in lens])
+    q, k, v = (I.to_f64(x, c.dtype) for x in c.parts())
+    want, bound = attention(q, k, v, c.starts, c.scale, I.EPS[c.dtype])
+    mine = np.concatenate([np.repeat(keep, lens), [False] * 3])
+    got = I.to_f64(host(c.out, c.parts()[0]), c.dtype)
+    assert (np.abs(got - want) <= bound)[mine].all()
+    assert (c.raw()[~mine] == -1).all()
