@@ -80,6 +80,12 @@ constexpr int kPaThreads = 512;        // four warpgroups; warp 15 has no role
 constexpr int kPaSoftmaxRegs = 160, kPaOtherRegs = 96;
 constexpr uint32_t kPaTmemO = 256;      // S of tile t: columns [128 t, 128 t + 128); then the O's
 constexpr float kPaRescaleLog2 = 8.f;
+// Weights are 2^(score - maximum + lift).  fp16 ends at 2^-24, and a weight that
+// it loses the sum l still counts: the many keys of little weight behind one that
+// holds nearly all would be lost together, 2^-25 of the largest |v| each.  The lift
+// uses the upper end of its range (2^7 x 2^8 < 65504) and cancels in O / l.
+template <typename T>
+constexpr float kPaLift = std::is_same<T, __half>::value ? 7.f : 0.f;
 constexpr float kPaNoMax = -3e38f;      // before the first key; finite, so that no exponent is inf - inf
 constexpr int kPaItems = 4;             // items found ahead
 constexpr int kPaRoles = 14;            // warps that work on an item
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const int warp_row = (warp & 3) * 32;
       const int pos_min = (first_row + min(warp_row, mine.rows - 1)) >> g2;
       const int pos_max = (first_row + min(warp_row + 31, mine.rows - 1)) >> g2;
-      float m_run = kPaNoMax, l_run = 0.f;
+      float m_run = kPaNoMax, l_run = 0.f;   // the running maximum less the lift
       for (int c = 0; c < mine.chunks; ++c, ++done) {
         const int key0 = c * kPaKeys;
         const bool second = key0 + kPaHalf <= pos_max;   // a row of the warp sees the second half
@@ -418,13 +424,14 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             const float mx = qmul * fmaxf(fmax3(m8[0], m8[1], m8[2]),
                                           fmax3(fmaxf(m8[3], m8[4]), fmaxf(m8[5], m8[6]), m8[7]));
             // The running maximum only moves when a score passes it by more
-            // than 2^8, and only then is O rescaled: weights stay below 2^8,
-            // and the stale maximum cancels in O / l.
-            const bool moved = mx > m_run + kPaRescaleLog2;
+            // than 2^8, and only then is O rescaled: weights stay below 2^8
+            // times the lift, and the stale maximum cancels in O / l.
+            const bool moved = mx > m_run + (kPaRescaleLog2 + kPaLift<T>);
             if (__any_sync(0xffffffffu, moved)) {
-              const float corr = moved ? softmax_exp2(m_run - mx) : 1.f;   // 0 at first
+              const float m_new = mx - kPaLift<T>;
+              const float corr = moved ? softmax_exp2(m_run - m_new) : 1.f;   // 0 at first
               l_run *= corr;
-              if (moved) m_run = mx;
+              if (moved) m_run = m_new;
               if (c > 0 || half > 0) {
                 // the product of the half before still adds to O
                 ok = pa_wait(&o_done[t][1 - half], (half ? done : done - 1) & 1, gave_up);

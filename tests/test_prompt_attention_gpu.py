@@ -292,3 +292,42 @@ def test_a_thousand_prompts(hq, hkv, d, longest):
     got = I.to_f64(host(c.out, c.parts()[0]), c.dtype)
     assert (np.abs(got - want) <= bound)[mine].all()
     assert (c.raw()[~mine] == -1).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (8, 2, 128)])
+@pytest.mark.parametrize("nats", [12.0, 17.0, 17.75])
+def test_many_keys_of_little_weight(dtype, hq, hkv, d, nats):
+    """A prompt's first key holds nearly all of the weight and has a small v; each key behind it
+    weighs e^-nats, next to what fp16 can hold, and has an ordinary v.
+
+    Bound: a weight is rounded to the storage type, eps / 2 of itself, or where fp16 ends by half
+    of 2^-24 below weights of 2^7 at least; exponentials, and sums of n / 16 products of 16 keys in
+    fp32, 2^-22 a product; then the output's rounding."""
+    n = 9000
+    c = Case([n], hq, hkv, d, dtype)
+    c.scale = 8.0 / d
+    x = I.to_f64(c.all, dtype)
+    x[:, :hq] = 1.0
+    x[:, hq:hq + hkv] = 0.0
+    x[0, hq:hq + hkv] = nats / 8                # exact: the scores are nats and 0
+    x[0, hq + hkv:] *= 0.003
+    x[1:, hq + hkv:] = np.abs(x[1:, hq + hkv:])
+    c.all = I.narrow(x, dtype)
+    c.up()
+    c.run()
+    assert P.photon_get_last_device_error()[0] == 0
+    got = I.to_f64(host(c.out, c.parts()[0]), dtype)
+    v = I.to_f64(c.all, dtype)[:, hq + hkv:]
+    w = np.full((n, 1, 1), np.exp(-nats))
+    w[0] = 1.0
+    total, size = np.cumsum(w, 0), np.cumsum(w * np.abs(v), 0)
+    want = np.cumsum(w * v, 0) / total
+    keys = np.arange(1, n + 1)[:, None, None]
+    eps = I.EPS[dtype] / 2
+    bound = (eps + 2.0 ** -20 + keys / 16 * 2.0 ** -22) * 2 * size / total
+    if dtype == W.DTYPE_F16:
+        bound += keys * 2.0 ** -32 * np.abs(v).max()
+    bound += eps * (np.abs(want) + bound) + 2.0 ** -25
+    want, bound = (np.repeat(y, hq // hkv, 1) for y in (want, bound))
+    assert (np.abs(got - want) <= bound).all(), (np.abs(got - want) / bound).max()
