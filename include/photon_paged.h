@@ -331,8 +331,10 @@ size_t photon_paged_decode_int4_workspace_size(const photon_paged_shape_t* shape
 /* photon_paged_decode over a 4-bit cache: out = softmax(scale * q . K) V with
  * the rows' values as defined above (the codes are never widened in memory),
  * fp32 accumulation on the tensor cores, the softmax weights times step fed as
- * an fp16 rounding plus its fp16 residual.  The batch's blocks are cut into
- * equal runs, one per resident warp, so partition_size is ignored.  Layouts of
+ * an fp16 rounding plus its fp16 residual (to 2^-22 of each, and 2^-38, at eight
+ * q heads per KV head 2^-36, of the largest weight times the largest step).  The
+ * batch's blocks are cut into equal runs, one per team of up to eight warps that
+ * take a KV head each, so partition_size is ignored.  Layouts of
  * q, out, tables and lengths, errors and workspace rules as
  * photon_paged_decode; num_seqs * num_kv_heads * (max_blocks_per_seq + 16) must
  * stay below 2^30 and num_blocks * num_kv_heads below 2^31
@@ -402,7 +404,8 @@ photon_status_t photon_qk_norm_rope(const void* q, int64_t q_stride, const void*
  *     out[i][h] = sum_{j <= i} softmax_j(scale * q[i][h] . k[j][kvh]) v[j][kvh]
  * over the prompt's tokens j, kvh = h / G, in fp32 arithmetic from fp16/bf16
  * operands on the tensor cores, out rounded to the stored dtype (the softmax
- * weights enter the second product rounded to the storage type).
+ * weights enter the second product rounded to the storage type; fp16 keeps them
+ * down to 2^-32 of the largest).
  *   q, out        [num_tokens] rows of num_q_heads x head_dim
  *   k, v          [num_tokens] rows of num_kv_heads x head_dim
  *   *_stride      elements from a token's row to the next one's (0: packed),

@@ -30,7 +30,7 @@
 // up to keys x 2^-25 of half a row's range, 1.5e-3 with 13900 keys at e^-17.
 // So columns 4 .. 7 hold 2^14 times the residual, and with G = 8, where both
 // go to the same sums, the weights fill fp16's upper end instead (kOne,
-// kSlack): nothing above 2^-39 (G = 8: 2^-37) of the largest weight is lost.
+// kSlack): nothing above 2^-38 (G = 8: 2^-36) of the largest p_j step_j is lost.
 //
 // Work: a team of up to 8 neighbouring warps takes as many neighbouring KV
 // heads, a warp each, through the same blocks, so that what it reads of a block
@@ -45,8 +45,11 @@
 // timing.
 //
 // Measured (8 kv heads, d = 128, fp16; event times): 64 contexts of 128 .. 8192
-// tokens 34.7 us = 4.0 TB/s of the codes and pairs, 59 % of the measured copy
-// rate; a batch-256 mix at 32 q heads 63.3 us = 61 %; 4 short contexts 9.2 us.
+// tokens 34.8 us = 4.0 TB/s of the codes and pairs, 59 % of the measured copy
+// rate; a batch-256 mix at 32 q heads 63.9 us = 60 %; 4 short contexts 9.3 us.
+// At 64 q heads (G = 8) contexts that take 32.8 us at 16 take 41.6: twice the P V
+// products, and at d = 128 a few spilled registers.  Few long contexts: 4 of
+// 65536 tokens 58 us = 4.9 TB/s, 8 of 131072 at 64 q heads 205 us = 5.6 TB/s.
 // What bounds it: the first data comes 4 us after the call's start and the merge
 // takes 3.5 us; between them 5.5 TB/s, the rate of the copies themselves: with
 // no arithmetic at all the first version of this split took 34.5 us where it
@@ -66,8 +69,10 @@ namespace {
 constexpr int kI4Warps = kInt4CtaWarps;   // warps per CTA
 constexpr int kI4Threads = 32 * kI4Warps;
 // What beginning and ending a pair (its q rows, the sums over the warp, the
-// output or a partial) costs a warp, in blocks of keys.  Batch-256 mix with 2,
-// 3, 5, 8: 83, 78, 70, 69 us; 64 long contexts 40.1, 37.7, 37.7, 38.6 us.
+// output or a partial) costs a warp, in blocks of keys.  With 3, 4, 5, 6, 7, 8: a
+// batch-256 mix 87.2, 83.8, 80.6, 79.4, 80.5, 80.1 us, 64 long contexts 33.7,
+// 32.9, 32.8, 32.7, 33.2, 32.8, 256 of 128 .. 4096 tokens 66.7, 66.1, 65.2, 65.1,
+// 66.8, 66.9.
 constexpr int kI4PairCost = 6;
 // Shortest run of a team on the line (4 contexts of up to 2048 tokens: 6 and
 // 8: 9.0 and 9.6 us).
@@ -735,8 +740,10 @@ cudaError_t launch_int4(const DecodeInt4Args& a, cudaStream_t stream) {
   if (a.ev_start) cudaEventRecord(a.ev_start, stream);
   e = launch_pdl(kern, dim3(grid), dim3(kI4Threads), C::kSmem, stream, a);
   if (e != cudaSuccess) return e;
-  // from two items a resident warp on, a warp an item (batch-256 mix 62.9 against
-  // 67.8 us); 1024 items of 64 long contexts 36.8 against 34.4 us
+  // from 16 items an SM (2432) on, a warp an item.  A warp against four: 1024 items of
+  // 64 long contexts 35.4, 32.7 us; 2048 of a mix 31.4, 28.9, of long contexts 54.5,
+  // 55.3; 2560 of a mix 34.2, 33.3; 4096 of a mix 47.8, 49.3, of long contexts 65.2,
+  // 69.9; 8192 of a mix 79.4, 85.2, of short contexts 18.4, 24.4
   const int items = a.B * a.Hq;
   e = items >= 16 * a.num_sms
           ? launch_pdl(paged_decode_int4_merge_kernel<T, D, 1>,

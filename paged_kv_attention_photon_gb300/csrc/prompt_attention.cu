@@ -23,7 +23,7 @@
 // over its S as 16-bit pairs and is read from there as the A operand, so the
 // softmax of one half runs while S or P V of the other does.  (With S of all 128
 // keys at once the tensor cores reach their rate on it, but a chunk is one long
-// chain: 1 x 16384 tokens 0.73 ms against 0.64 ms by halves.  At d = 64 TMEM has
+// chain: 1 x 16384 tokens 0.73 ms against 0.64 ms by halves (a few calls in a row).  At d = 64 TMEM has
 // room for a P apart from S; by halves that is slower, 4 x 4096 tokens 0.356 ms
 // against 0.30 to 0.33 ms.)  An issuing warp is held up for hundreds of clocks by
 // each of its commits, hence four of them; issued from inside one elected
@@ -31,9 +31,11 @@
 // 95.  Copies run ahead across items, and the next item's first S products
 // overlap this one's epilogue.
 //
-// Measured (16 q, 8 kv heads, d = 128, back to back): 1 x 16384 tokens, bf16, 0.635
-// ms = 1732 TFLOP/s, 92 % of the measured dense rate; 16 x 1024, fp16, 63.7 us =
-// 1080 TFLOP/s.  At d = 64 (32 q, 8 kv heads, fp16) 4 x 4096 tokens take 0.30 to
+// Measured (16 q, 8 kv heads, d = 128): 1 x 16384 tokens, bf16, 0.64 ms = 1718
+// TFLOP/s over 20 calls, 91 % of the measured dense burst rate; over 1000 calls
+// the power limit lowers the clock (2070 to about 1800 MHz) and it is 0.69 ms =
+// 1594 TFLOP/s, 94 % of the sustained rate; whether the inputs change makes no
+// difference.  16 x 1024, fp16, 64 us = 1080 TFLOP/s.  At d = 64 (32 q, 8 kv heads, fp16) 4 x 4096 tokens take 0.30 to
 // 0.33 ms = 840 to 920 TFLOP/s: the products are half as long for the same
 // softmax, which bounds it.  In short prompts the items do: ending one and
 // starting the next costs a tile about 3000 clocks (the last P V 120, the

@@ -64,8 +64,8 @@ __device__ __forceinline__ float row_max(float x) {
   return x;
 }
 
-// 32, 64, 96, 128, 256: 16 x 1024 tokens in 37.2, 34.6, 35.6, 35.4, 38.5 us, 6190 f32
-// tokens on three axes in 24.2, 24.8, 25.1, 25.3, 26.8
+// In one run with 32, 64, 96, 128, 256: 16 x 1024 tokens in 37.2, 34.6, 35.6, 35.4,
+// 38.5 us, 6190 f32 tokens on three axes in 24.2, 24.8, 25.1, 25.3, 26.8
 constexpr int kQkThreads = 64;
 constexpr int kQkHeads = 3;   // head rows a lane takes, all loaded before the first is used
 
