@@ -639,3 +639,29 @@ def test_write_several_rounds(dtype, d, hkv):
     assert P.photon_get_last_device_error() == (6, 2)
     for a, b in zip(got, packed_pools(fused[:, :hkv], fused[:, hkv:], slots, nb, dtype)):
         assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 4, 64), (16, 2, 128)])
+def test_decode_two_streams_at_once_and_repeated(hq, hkv, d):
+    """Two calls in flight with workspaces of their own, again and again: the same bits."""
+    rng = np.random.default_rng(6)
+    cases = [Decode(103, [int(x) for x in rng.integers(0, 900, 40)], hq, hkv, d, W.DTYPE_F16),
+             Decode(107, [2000, 3, 700], 8, 4, 64, W.DTYPE_BF16)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    first = []
+    for c in cases:
+        c.run()
+        ok_status()
+        c.check()
+        first.append(c.out.clone())
+    for _ in range(5):
+        for c in cases:
+            c.out.fill_(-1)
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for c, s in zip(cases, streams):
+                c.run(s)
+        torch.cuda.synchronize()
+        for c, f in zip(cases, first):
+            assert torch.equal(c.out, f)
+    ok_status()

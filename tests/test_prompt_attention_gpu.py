@@ -331,3 +331,15 @@ def test_many_keys_of_little_weight(dtype, hq, hkv, d, nats):
     bound += eps * (np.abs(want) + bound) + 2.0 ** -25
     want, bound = (np.repeat(y, hq // hkv, 1) for y in (want, bound))
     assert (np.abs(got - want) <= bound).all(), (np.abs(got - want) / bound).max()
+
+
+def test_repeated_calls_give_the_same_bits():
+    for c in (Case([700, 1, 90, 400, 33] * 9, 8, 4, 128, W.DTYPE_F16),
+              Case([513, 64, 2, 1000], 16, 4, 64, W.DTYPE_BF16)):
+        c.run()
+        c.check()
+        first = c.out.clone()
+        for _ in range(10):
+            c.out.fill_(-1)
+            c.run()
+            assert torch.equal(c.out, first)
