@@ -46,7 +46,7 @@
 //
 // Measured (8 kv heads, d = 128, fp16; event times): 64 contexts of 128 .. 8192
 // tokens 34.8 us = 4.0 TB/s of the codes and pairs, 59 % of the measured copy
-// rate; a batch-256 mix at 32 q heads 63.9 us = 60 %; 4 short contexts 9.3 us.
+// rate; a batch-256 mix at 32 q heads 65.0 us = 59 %; 4 short contexts 9.3 us.
 // At 64 q heads (G = 8) contexts that take 32.8 us at 16 take 41.6: twice the P V
 // products, and at d = 128 a few spilled registers.  Few long contexts: 4 of
 // 65536 tokens 58 us = 4.9 TB/s, 8 of 131072 at 64 q heads 205 us = 5.6 TB/s.
@@ -318,7 +318,14 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
   // ---- a pair's state.  Columns (slots) 2t and 2t + 1 of the score fragment
   // are this lane's; with G <= 4 column 4 + s repeats slot s.
   uint32_t bq[NW][2][2];   // Q^T fragments: column g, products 2j and 2j + 1 of word j
-  float c1[2], c2[2];      // score = (step acc + lo c2) c1, c1 > 0
+  // score = (step f acc + lo c2) c1: c1 a power of two, f the rest of the scale, in
+  // [1, 2).  So the maximum, scaled, is exact, and so is what the weights next to it
+  // are taken from.  With c1 the whole factor the maximum would be rounded, from
+  // 2^24 on by whole units, and a weight of 1 could be any power of two.  (Batch-256
+  // mix 79.5 -> 81.2 us, others the same; differences of scores instead 81.2 too, a
+  // branch for large scores only 80.5, but 64 long contexts 33.0 -> 33.4.)
+  const float f = __uint_as_float((__float_as_uint(a.qscale) & 0x7fffffu) | 0x3f800000u);
+  float c1[2], c2[2];
   float m[2], l[2], z[2];  // running max, sum of weights, sum of weights x lo of V
   float limit[2];          // (m + kSlack) / c1: what a score / c1 may reach before m moves
   float o[NW][2][4];       // O^T: dims (D / 8) g + 4j + 2h (rows g) and + 1 (rows g + 8)
@@ -367,8 +374,9 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
     // zero scale or a zero row every weight is 1, but the -inf of a key that
     // is not there has to remain one (-inf x 0 is NaN), and so has a score of 0
     // (0 x inf).
-    const float k1 = fminf(fmaxf((fabsf(a.qscale) * 16777216.f) * (1.f / up), 1e-37f), 1.7014118e38f);
-    const float k2 = sum * (sc * 6.1035156e-5f);
+    const float whole = __uint_as_float(__float_as_uint(a.qscale) & 0x7f800000u);   // |qscale| / f
+    const float k1 = fminf(fmaxf((whole * 16777216.f) * (1.f / up), 1.8807910e-37f), 1.7014118e38f);
+    const float k2 = sum * (sc * 6.1035156e-5f) * f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int col = 2 * t + i;
@@ -427,8 +435,8 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
           Mma<__half>::run(acc, f0, bq[j][0][0], bq[j][0][1]);
         Mma<__half>::run(acc, f1, bq[j][1][0], bq[j][1][1]);
       }
-      const float ks0 = Bits16<T>::to_f32(kp0 & 0xffffu), kl0 = Bits16<T>::to_f32(kp0 >> 16);
-      const float ks8 = Bits16<T>::to_f32(kp8 & 0xffffu), kl8 = Bits16<T>::to_f32(kp8 >> 16);
+      const float ks0 = Bits16<T>::to_f32(kp0 & 0xffffu) * f, kl0 = Bits16<T>::to_f32(kp0 >> 16);
+      const float ks8 = Bits16<T>::to_f32(kp8 & 0xffffu) * f, kl8 = Bits16<T>::to_f32(kp8 >> 16);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         y[u][i] = fmaf(i < 2 ? ks0 : ks8, acc[i], (i < 2 ? kl0 : kl8) * c2[i & 1]);
@@ -477,8 +485,8 @@ __global__ void __launch_bounds__(kI4Threads, I4Cfg<D>::kCtas)
       }
       m[0] = n0;
       m[1] = n1;
-      limit[0] = (n0 + kSlack) / c1[0];
-      limit[1] = (n1 + kSlack) / c1[1];
+      limit[0] = __fadd_rd(n0, kSlack) / c1[0];   // not above m + kSlack, however large m is
+      limit[1] = __fadd_rd(n1, kSlack) / c1[1];
       l[0] *= r0, z[0] *= r0;
       l[1] *= r1, z[1] *= r1;
 #pragma unroll

@@ -665,3 +665,44 @@ def test_decode_two_streams_at_once_and_repeated(hq, hkv, d):
         for c, f in zip(cases, first):
             assert torch.equal(c.out, f)
     ok_status()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (4, 1, 128), (8, 1, 64), (8, 1, 128)])
+@pytest.mark.parametrize("size", [1e3, 2e5, 7e6, 3e7, 1e8, 1e9, 1e10])
+def test_decode_scores_far_from_zero(dtype, hq, hkv, d, size):
+    """Scores of that size (log2 domain), so far apart that only the keys of the largest one weigh
+    anything; those are equal, and the output is the mean of their V.  Constant K rows, so equal
+    rows have equal scores whatever the products lose."""
+    rng = np.random.default_rng(int(size) % 1000 + d)
+    contexts = [300, 77, 1, 520]
+    kp, vp, bt, cl = I.build_pools(113, contexts=contexts, hkv=1, d=d, dtype=dtype)
+    ladder = np.array([0.25, 0.5, 0.625, 0.75, 0.875, 1.0]) * 1.37
+    picks = []
+    for b, n in enumerate(contexts):
+        # rising in steps, so that the maximum moves several times, the largest a few times over
+        pick = np.sort(rng.integers(0, len(ladder), n))
+        pick[rng.integers(0, n, n // 3)] = 0
+        picks.append(pick)
+        codes, step, lo = I.quantise(I.narrow(np.broadcast_to(ladder[pick][:, None], (n, d)), dtype), dtype)
+        for j in range(n):
+            I.store_row(kp, True, d, bt[b, j // 16], 0, j % 16, codes[j], step[j], lo[j])
+    q = I.narrow(np.full((len(contexts), hq, d), 3.0) + np.arange(hq)[None, :, None] / 4, dtype)
+    scale = size / (1.4427 * 1.37 * 3.0 * d)
+    shape = shape_for(seqs=len(contexts), hq=hq, hkv=1, d=d, nb=kp.shape[0], mbs=bt.shape[1], dtype=dtype)
+    n = P.photon_paged_decode_int4_workspace_size(shape)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for sign in (1, -1):     # a negative scale turns the ladder round
+        out = torch.full(q.shape, -1, dtype=torch.int16, device="cuda")
+        P.photon_paged_decode_int4(dev(q), dev(kp), dev(vp), dev(bt), dev(cl), sign * scale, out, ws, n,
+                                   shape)
+        ok_status()
+        got = I.to_f64(host(out, q), dtype)
+        for b, ctx in enumerate(contexts):
+            v = I.load_rows(vp, False, d, bt[b], ctx, dtype)[0]
+            top = picks[b] == (picks[b].max() if sign > 0 else picks[b].min())
+            want = v[top].mean(0)
+            # sums of up to ctx weights of 1: 2^-22 each; the other keys weigh 2^-100 and less
+            tol = ctx * 2.0 ** -22 * np.abs(v).max()
+            tol = tol + I.EPS[dtype] / 2 * (np.abs(want) + tol) + 2.0 ** -25
+            assert (np.abs(got[b] - want) <= tol).all(), (sign, b, np.abs(got[b] - want).max())
