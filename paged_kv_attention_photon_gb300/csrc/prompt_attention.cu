@@ -92,6 +92,12 @@ constexpr float kPaRescaleLog2 = 8.f;
 template <typename T>
 constexpr float kPaLift = std::is_same<T, __half>::value ? 7.f : 0.f;
 constexpr float kPaNoMax = -3e38f;      // before the first key; finite, so that no exponent is inf - inf
+// The weights' exponents are one operation on the scores, qm s + base.  base holds
+// the scaled maximum, rounded, which is the same for all of a row's weights; but
+// from this on (2^23) it is rounded by half a unit and more, and weights would leave
+// fp16.  There fp32 scores are whole units of the exponent apart, so qm is the scale's
+// power of two alone, with which the scaled maximum and the differences are exact.
+constexpr float kPaFar = 8388608.f;
 constexpr int kPaItems = 4;             // items found ahead
 constexpr int kPaRoles = 14;            // warps that work on an item
 
@@ -397,7 +403,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const int warp_row = (warp & 3) * 32;
       const int pos_min = (first_row + min(warp_row, mine.rows - 1)) >> g2;
       const int pos_max = (first_row + min(warp_row + 31, mine.rows - 1)) >> g2;
-      float m_run = kPaNoMax, l_run = 0.f;   // the running maximum less the lift
+      float m_run = kPaNoMax, l_run = 0.f;   // running maximum, unscaled; sum of weights
+      float qm = qmul, base = 0.f;
       for (int c = 0; c < mine.chunks; ++c, ++done) {
         const int key0 = c * kPaKeys;
         const bool second = key0 + kPaHalf <= pos_max;   // a row of the warp sees the second half
@@ -426,17 +433,20 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             for (int j = 16; j < 64; j += 16)
 #pragma unroll
               for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], s[j + k], s[j + 8 + k]);
-            const float mx = qmul * fmaxf(fmax3(m8[0], m8[1], m8[2]),
-                                          fmax3(fmaxf(m8[3], m8[4]), fmaxf(m8[5], m8[6]), m8[7]));
+            const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]),
+                                   fmax3(fmaxf(m8[3], m8[4]), fmaxf(m8[5], m8[6]), m8[7]));
             // The running maximum only moves when a score passes it by more
             // than 2^8, and only then is O rescaled: weights stay below 2^8
             // times the lift, and the stale maximum cancels in O / l.
-            const bool moved = mx > m_run + (kPaRescaleLog2 + kPaLift<T>);
+            const bool moved = (mx - m_run) * qmul > kPaRescaleLog2;
             if (__any_sync(0xffffffffu, moved)) {
-              const float m_new = mx - kPaLift<T>;
-              const float corr = moved ? softmax_exp2(m_run - m_new) : 1.f;   // 0 at first
+              const float corr = moved ? softmax_exp2((m_run - mx) * qmul) : 1.f;   // of nothing, at first
               l_run *= corr;
-              if (moved) m_run = m_new;
+              if (moved) {
+                m_run = mx;
+                qm = fabsf(qmul * mx) < kPaFar ? qmul : __uint_as_float(__float_as_uint(qmul) & 0x7f800000u);
+                base = __fmaf_rd(-qm, mx, kPaLift<T>);   // lifted no further, however large
+              }
               if (c > 0 || half > 0) {
                 // the product of the half before still adds to O
                 ok = pa_wait(&o_done[t][1 - half], (half ? done : done - 1) & 1, gave_up);
@@ -457,7 +467,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               float x0, x1;
-              fma_f32x2(x0, x1, s[2 * j], s[2 * j + 1], qmul, -m_run);
+              fma_f32x2(x0, x1, s[2 * j], s[2 * j + 1], qm, base);
               const float p0 = softmax_exp2(x0), p1 = softmax_exp2(x1);
               add_f32x2(sum[(j & 1) * 2], sum[(j & 1) * 2 + 1], p0, p1);
               w[j] = __uint_as_float(Mma<T>::pack(p0, p1));

@@ -343,3 +343,36 @@ def test_repeated_calls_give_the_same_bits():
             c.out.fill_(-1)
             c.run()
             assert torch.equal(c.out, first)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("hq,hkv,d", [(2, 2, 64), (8, 1, 128)])
+@pytest.mark.parametrize("size", [1e3, 2e5, 7e6, 3e7, 1e8, 1e9, 1e10])
+def test_scores_far_from_zero(dtype, hq, hkv, d, size):
+    """Scores of that size (log2 domain), so far apart that only the keys of the largest one so far
+    weigh anything; those are equal, and a row is the mean of their v.  Constant k rows, so equal
+    rows have equal scores whatever the products lose."""
+    n = 400
+    c = Case([n], hq, hkv, d, dtype)
+    rng = np.random.default_rng(int(size) % 1000 + d)
+    ladder = np.array([0.25, 0.5, 0.625, 0.75, 0.875, 1.0]) * 1.37
+    pick = np.sort(rng.integers(0, len(ladder), n))
+    pick[rng.integers(0, n, n // 3)] = 0
+    x = I.to_f64(c.all, dtype)
+    x[:, :hq] = 3.0 + np.arange(hq)[:, None] / 4
+    x[:, hq:hq + hkv] = ladder[pick][:, None, None]
+    c.all = I.narrow(x, dtype)
+    v = np.repeat(I.to_f64(c.all, dtype)[:, hq + hkv:], hq // hkv, 1)
+    for sign in (1, -1):     # a negative scale turns the ladder round
+        c.scale = sign * size / (1.4427 * 1.37 * 3.0 * d)
+        c.up()
+        c.run()
+        assert P.photon_get_last_device_error()[0] == 0
+        got = I.to_f64(host(c.out, c.parts()[0]), dtype)
+        for i in range(n):
+            seen = pick[:i + 1]
+            want = v[:i + 1][seen == (seen.max() if sign > 0 else seen.min())].mean(0)
+            # equal weights, each rounded (eps / 2); sums of up to n of them, 2^-22 each
+            tol = (I.EPS[dtype] / 2 + n * 2.0 ** -22) * np.abs(v).max()
+            tol = tol + I.EPS[dtype] / 2 * (np.abs(want) + tol) + 2.0 ** -25
+            assert (np.abs(got[i] - want) <= tol).all(), (sign, i, np.abs(got[i] - want).max())
