@@ -429,6 +429,149 @@ photon_status_t photon_prompt_attention(const void* q, int64_t q_stride, const v
                                         int64_t out_stride, const photon_paged_shape_t* shape,
                                         photon_stream_t stream);
 
+/* ---- A speculative step from drafted trees (README "Roadmap": speculative
+ * decoding).  Every sequence has a tree of 1 to 256 nodes, each a token that may
+ * follow.  Nodes are numbered 0 .. n-1 in the sequence, a node after its parent;
+ * sequence b's are rows query_start[b] .. query_start[b+1]-1 of all that is given
+ * per token, and their K and V rows are the last n of its context in the cache, in
+ * that order.  parents[row] is the parent's number in the sequence, or -1 for a
+ * node that follows the context directly.  A parent outside [-1, i) of node i sets
+ * device error bit 64 and counts as -1.  max_query_len is a host upper bound of
+ * every n, at most 256 (PHOTON_ERR_UNSUPPORTED); a sequence whose rows lie outside
+ * [0, num_tokens) or number more sets bit 32.
+ * A step: photon_rope_cache_append (positions: context before the tree + depth of
+ * the node) and photon_paged_tree_attention in every layer, photon_verify_tree on
+ * the last one's probabilities, photon_cache_compact on all layers' pools; the
+ * context is then path_len longer than before the tree, and next_token is the next
+ * tree's node 0. */
+
+/* Rotation of q and k by position and the cache write of k and v, in one pass over
+ * all three: for every token t, head row x of q and of k, and pair i of rotary_dim
+ * / 2, with (cos, sin) = rope_cos_sin[positions[t]][i],
+ *     z[a] = x[a] cos - x[b] sin,   z[b] = x[b] cos + x[a] sin,   z = x elsewhere,
+ * in fp32, rounded once to the storage type (f32, f16 or bf16); (a, b) = (i, i +
+ * rotary_dim / 2), or with interleaved == 1 (2i, 2i + 1).  z of q goes to q_out, z
+ * of k and v bit for bit to slot_mapping[t] of the caches.
+ *   q, q_out      [num_tokens] rows of num_q_heads x head_dim; both NULL: keys and
+ *                 values alone
+ *   k, v          [num_tokens] rows of num_kv_heads x head_dim
+ *   *_stride      elements from a token's row to the next one's (0: packed), at
+ *                 least the row's elements and a multiple of 16 bytes
+ *   positions     int32 [num_tokens]; negative: padding, nothing is stored and
+ *                 q_out's row is left as it was
+ *   slot_mapping  int64 [num_tokens]; negative: k and v are not stored, q is
+ *                 turned all the same; past the pool: device error bit 2, not stored
+ *   rope_cos_sin  from photon_rope_cos_sin(base, max_positions, rotary_dim), or a
+ *                 table of that form with scaled angles
+ * In place (q_out == q, same stride) is allowed; any other overlap is not.  A
+ * position >= max_positions sets device error bit 16 and that token's rows are
+ * stored unturned.  rotary_dim is a multiple of 16 (PHOTON_ERR_UNSUPPORTED), at
+ * least 16 and at most head_dim.  Two tokens with the same slot race.
+ * num_tokens == 0 is a no-op.  Uses shape: num_q_heads, num_kv_heads, head_dim,
+ * num_blocks, dtype. */
+photon_status_t photon_rope_cache_append(const void* q, int64_t q_stride, const void* k,
+                                         int64_t k_stride, const void* v, int64_t v_stride,
+                                         const int32_t* positions, const void* rope_cos_sin,
+                                         int32_t max_positions, int32_t rotary_dim,
+                                         int32_t interleaved, const int64_t* slot_mapping,
+                                         int32_t num_tokens, void* q_out, int64_t q_out_stride,
+                                         void* k_cache, void* v_cache,
+                                         const photon_paged_shape_t* shape,
+                                         photon_stream_t stream);
+
+/* Workspace bytes of photon_paged_tree_attention; 0 for arguments that it refuses,
+ * f32, num_seqs == 0, num_tokens == 0 or max_query_len == 0. */
+size_t photon_paged_tree_attention_workspace_size(const photon_paged_shape_t* shape,
+                                                  int32_t num_tokens, int32_t max_query_len);
+
+/* photon_paged_multi_query for trees: node i of a sequence of context ctx and n
+ * nodes attends to keys 0 .. ctx - n - 1, to the keys ctx - n + j of its ancestors j,
+ * and to its own, ctx - n + i:
+ *     out[row][h] = sum_j softmax_j(scale * q[row][h] . K_j[kvh]) V_j[kvh]
+ * over those, in fp32 arithmetic from fp16/bf16 operands on the tensor cores, out
+ * rounded to the stored dtype; the softmax weights enter the second product rounded
+ * to the storage type (fp16 keeps them down to 2^-32 of the largest).  A chain
+ * (parents[i] = i - 1) is photon_paged_multi_query.
+ *   q, out        [num_tokens][num_q_heads][head_dim]
+ *   context_lens  count the tree's nodes, whose K and V rows are in the cache
+ * Any NaN in a sequence's own V may reach any of its rows.  Rows of out that belong
+ * to no sequence are left as they were.  dtype must be PHOTON_F16 or PHOTON_BF16.
+ * A sequence with more nodes than max_query_len sets bit 32 and gets max_query_len
+ * zero rows (none if its rows lie outside [0, num_tokens)); n > ctx or a context
+ * outside [0, max_blocks_per_seq * block_size] sets bit 4 and gets zero rows; a block
+ * id outside the pool sets bit 1 and its keys are left out (a row that has no other
+ * is zero).  workspace as for photon_paged_multi_query.  num_seqs x num_kv_heads x
+ * (max_blocks_per_seq / 8 + 3) x ceil(max_query_len x G / 256) must stay below 2^30,
+ * num_blocks x num_kv_heads x 16 below 2^31 and num_tokens x num_q_heads below 2^30
+ * (PHOTON_ERR_UNSUPPORTED).  num_seqs == 0, num_tokens == 0 or max_query_len == 0 is
+ * a no-op.  partition_size is ignored. */
+photon_status_t photon_paged_tree_attention(const void* q, const void* k_cache,
+                                            const void* v_cache, const int32_t* block_tables,
+                                            const int32_t* context_lens,
+                                            const int32_t* query_start, const int32_t* parents,
+                                            int32_t num_tokens, int32_t max_query_len, float scale,
+                                            void* out, void* workspace, size_t workspace_bytes,
+                                            const photon_paged_shape_t* shape,
+                                            photon_stream_t stream);
+
+/* Rejection sampling of drafted trees: which nodes are accepted, and the token that
+ * follows, so that what comes out is distributed as the target's own sampling.
+ * Node 0 is accepted: it is certain (the last step's token).  From an accepted node
+ * c, with p and q the rows of c in target_probs and draft_probs (what follows c),
+ * r = p and Z = 1; its children in rising order, x a child's token and u its
+ * accept_uniforms:
+ *     r(x) > u Z q(x)    the child is accepted, and the walk goes on from it;
+ *     else               r <- max(0, r / Z - q), Z <- sum of r (r / 1 where Z is 0).
+ * draft_probs NULL: children are not drawn but chosen (the most likely ones, say); x
+ * is accepted if r(x) > u Z, else Z <- max(0, Z - r(x)) and r(x) <- 0.  Where no
+ * child is accepted, next_token is the first token whose cumulated r is above
+ * sample_uniforms[b] x the sum of r (of p, if r is 0 everywhere; the last token that
+ * r holds, if none is above), -1 if p is 0 everywhere.  Chains are trees with one
+ * child each; a target of ones and zeros verifies greedily.
+ *   target_probs, draft_probs  [num_tokens] rows of vocab entries of type dtype (f32,
+ *                 f16, bf16), *_stride elements apart (0: vocab), aligned to their
+ *                 elements (rows on 16-byte boundaries are read fastest); a NaN or
+ *                 negative entry counts as 0, one above 1 as 1
+ *   tokens        int32 [num_tokens]; a node with a negative token is never accepted
+ *                 and rejects nothing; so is one >= vocab, which sets bit 64.  Node
+ *                 0's is not used
+ *   accept_uniforms, sample_uniforms   float [num_tokens], [num_seqs], in [0, 1)
+ *   path          int32 [num_tokens]: a sequence's accepted nodes in order, node 0
+ *                 first, then -1 up to its last row
+ *   path_len      int32 [num_seqs]: how many (0 for a sequence without nodes or
+ *                 rejected with bit 32)
+ *   next_token    int32 [num_seqs]; -1 where path_len is 0
+ * Acceptances are decided in 64 bits, and sums of r held to 48 bits.  vocab <= 2^20,
+ * num_seqs <= 65535 (PHOTON_ERR_UNSUPPORTED).  num_seqs == 0 is a no-op. */
+photon_status_t photon_verify_tree(const void* target_probs, int64_t target_stride,
+                                   const void* draft_probs, int64_t draft_stride, int32_t vocab,
+                                   int32_t dtype, const int32_t* tokens, const int32_t* parents,
+                                   const int32_t* query_start, const float* accept_uniforms,
+                                   const float* sample_uniforms, int32_t num_seqs,
+                                   int32_t num_tokens, int32_t max_query_len, int32_t* path,
+                                   int32_t* path_len, int32_t* next_token,
+                                   photon_stream_t stream);
+
+/* Moves the accepted nodes' cached rows together: in every pool, the row at position
+ * first + path[j] of sequence b (first = context_lens[b] - n, n its nodes) is copied
+ * bit for bit to position first + j, for j < path_len[b], as if all were read before
+ * any is written; what lies behind is left as it was.  path, path_len as from
+ * photon_verify_tree.
+ *   pools         HOST array of num_pools <= 256 device pointers: K and V pools of any
+ *                 number of layers, no pool twice.  Read during the call
+ *   context_lens  as for the attention, with the tree's nodes
+ * A path that does not rise within [0, n), or a path_len outside [0, n], sets bit 64,
+ * a block id outside the pool bit 1, a bad context bit 4: that sequence is left as it
+ * was.  num_pools == 0, num_seqs == 0, num_tokens == 0 or max_query_len == 0 is a
+ * no-op.  Uses shape: num_seqs, num_kv_heads, head_dim, num_blocks,
+ * max_blocks_per_seq, dtype (16-bit or 32-bit rows). */
+photon_status_t photon_cache_compact(void* const* pools, int32_t num_pools,
+                                     const int32_t* block_tables, const int32_t* context_lens,
+                                     const int32_t* query_start, const int32_t* path,
+                                     const int32_t* path_len, int32_t num_tokens,
+                                     int32_t max_query_len, const photon_paged_shape_t* shape,
+                                     photon_stream_t stream);
+
 /* Test and tuning hook: which consumer the decode attention kernel runs
  * (photon_paged_decode, _step, _step_rope, _noalloc).  0 (default) = by the group size: the tensor-core consumer
  * (mma.sync over tensor-map copies of the blocks) for fp16/bf16 storage and
@@ -524,7 +667,8 @@ photon_status_t photon_paged_gather(const void* k_cache, const void* v_cache,
  * 4 = context length out of range, 8 = a bounded wait inside a kernel ran out
  * (the call's output is then incomplete), 16 = a RoPE position outside the
  * cos/sin table, 32 = inconsistent query_start / max_query_len of
- * photon_paged_multi_query or photon_prompt_attention. */
+ * photon_paged_multi_query, photon_prompt_attention or a drafted tree, 64 = a drafted
+ * tree's parent, token or path out of range. */
 photon_status_t photon_get_last_device_error(photon_stream_t stream, uint32_t* bits);
 
 /* Static text for a status code (never NULL). */

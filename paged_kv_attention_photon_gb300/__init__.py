@@ -34,6 +34,8 @@ __all__ = [
     "photon_cache_int4_bytes", "photon_cache_write_int4", "photon_paged_gather_int4",
     "photon_paged_decode_int4_workspace_size", "photon_paged_decode_int4",
     "RopeAxes", "photon_qk_norm_rope", "photon_prompt_attention",
+    "photon_rope_cache_append", "photon_paged_tree_attention_workspace_size",
+    "photon_paged_tree_attention", "photon_verify_tree", "CachePools", "photon_cache_compact",
     "photon_debug_wait_probe", "photon_debug_read_probe", "Scheduler",
     "F32", "F16", "BF16", "STATUS",
 ]
@@ -79,6 +81,23 @@ class RopeAxes(ctypes.Structure):
         sections = [int(x) for x in sections]
         held = (ctypes.c_int32 * 4)(*sections[:4])
         return cls(len(sections), held, int(interleaved))
+
+
+class CachePools:
+    """The K and V pools of a model's layers, as photon_cache_compact takes them: a
+    list of tensors (or device addresses), which are kept alive."""
+
+    def __init__(self, pools):
+        self.pools = list(pools)
+        self._held = (ctypes.c_void_p * len(self.pools))(*[_ptr(p) for p in self.pools])
+        self._at = ctypes.addressof(self._held)
+
+    def __len__(self) -> int:
+        return len(self.pools)
+
+    def data_ptr(self) -> int:
+        """Host address of the array of pool addresses."""
+        return self._at
 
 
 def library_path() -> str:
@@ -158,6 +177,18 @@ def _load() -> ctypes.CDLL:
     lib.photon_prompt_attention.argtypes = [P, I64, P, I64, P, I64, P, I32, I32, F32, P, I64, SP, P]
     lib.photon_prompt_attention.restype = ctypes.c_int
     lib.photon_paged_multi_query.restype = ctypes.c_int
+    lib.photon_rope_cache_append.argtypes = [P, I64, P, I64, P, I64, P, P, I32, I32, I32, P, I32, P,
+                                             I64, P, P, SP, P]
+    lib.photon_rope_cache_append.restype = ctypes.c_int
+    lib.photon_paged_tree_attention_workspace_size.argtypes = [SP, I32, I32]
+    lib.photon_paged_tree_attention_workspace_size.restype = SZ
+    lib.photon_paged_tree_attention.argtypes = [P, P, P, P, P, P, P, I32, I32, F32, P, P, SZ, SP, P]
+    lib.photon_paged_tree_attention.restype = ctypes.c_int
+    lib.photon_verify_tree.argtypes = [P, I64, P, I64, I32, I32, P, P, P, P, P, I32, I32, I32, P, P,
+                                       P, P]
+    lib.photon_verify_tree.restype = ctypes.c_int
+    lib.photon_cache_compact.argtypes = [P, I32, P, P, P, P, P, I32, I32, SP, P]
+    lib.photon_cache_compact.restype = ctypes.c_int
     # host scheduler (include/photon_scheduler.h)
     lib.photon_scheduler_create.argtypes = [P, ctypes.POINTER(P)]
     lib.photon_scheduler_destroy.argtypes = [P]
@@ -248,7 +279,9 @@ def _native():
         from . import _binding
         for name in ("photon_cache_write_int4", "photon_paged_gather_int4",
                      "photon_paged_decode_int4", "photon_qk_norm_rope",
-                     "photon_prompt_attention"):
+                     "photon_prompt_attention", "photon_rope_cache_append",
+                     "photon_paged_tree_attention", "photon_verify_tree",
+                     "photon_cache_compact"):
             _binding.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
         _calls = _binding
     return _calls
@@ -453,6 +486,64 @@ def photon_prompt_attention(q, q_stride: int, k, k_stride: int, v, v_stride: int
         out_stride, shape, _stream(stream))
     if status:
         raise PhotonError(status, "photon_prompt_attention")
+
+
+def photon_rope_cache_append(q, q_stride: int, k, k_stride: int, v, v_stride: int, positions,
+                             rope_cos_sin, max_positions: int, rotary_dim: int, interleaved: int,
+                             slot_mapping, num_tokens: int, q_out, q_out_stride: int, k_cache,
+                             v_cache, shape: PagedShape, stream=None) -> None:
+    """Rotation of q (None: keys alone) and k by position, k and v stored at their
+    slots; strides in elements from token to token, 0 = packed."""
+    status = (_calls or _native()).photon_rope_cache_append(
+        q, q_stride, k, k_stride, v, v_stride, positions, rope_cos_sin, max_positions, rotary_dim,
+        interleaved, slot_mapping, num_tokens, q_out, q_out_stride, k_cache, v_cache, shape,
+        _stream(stream))
+    if status:
+        raise PhotonError(status, "photon_rope_cache_append")
+
+
+def photon_paged_tree_attention_workspace_size(shape: PagedShape, num_tokens: int,
+                                               max_query_len: int) -> int:
+    return int(_load().photon_paged_tree_attention_workspace_size(
+        ctypes.byref(shape), int(num_tokens), int(max_query_len)))
+
+
+def photon_paged_tree_attention(q, k_cache, v_cache, block_tables, context_lens, query_start,
+                                parents, num_tokens: int, max_query_len: int, scale: float, out,
+                                workspace, workspace_bytes: int, shape: PagedShape,
+                                stream=None) -> None:
+    """Attention of each sequence's drafted tree over its cached context and, node by
+    node, its own ancestors."""
+    status = (_calls or _native()).photon_paged_tree_attention(
+        q, k_cache, v_cache, block_tables, context_lens, query_start, parents, num_tokens,
+        max_query_len, scale, out, workspace, workspace_bytes, shape, _stream(stream))
+    if status:
+        raise PhotonError(status, "photon_paged_tree_attention")
+
+
+def photon_verify_tree(target_probs, target_stride: int, draft_probs, draft_stride: int,
+                       vocab: int, dtype: int, tokens, parents, query_start, accept_uniforms,
+                       sample_uniforms, num_seqs: int, num_tokens: int, max_query_len: int, path,
+                       path_len, next_token, stream=None) -> None:
+    """Rejection sampling of drafted trees (draft_probs None: chosen, not drawn) from
+    given random numbers: the accepted nodes and the token that follows."""
+    status = (_calls or _native()).photon_verify_tree(
+        target_probs, target_stride, draft_probs, draft_stride, vocab, dtype, tokens, parents,
+        query_start, accept_uniforms, sample_uniforms, num_seqs, num_tokens, max_query_len, path,
+        path_len, next_token, _stream(stream))
+    if status:
+        raise PhotonError(status, "photon_verify_tree")
+
+
+def photon_cache_compact(pools: CachePools, block_tables, context_lens, query_start, path, path_len,
+                         num_tokens: int, max_query_len: int, shape: PagedShape,
+                         stream=None) -> None:
+    """The accepted nodes' rows moved together behind the context, in all pools."""
+    status = (_calls or _native()).photon_cache_compact(
+        pools, len(pools), block_tables, context_lens, query_start, path, path_len, num_tokens,
+        max_query_len, shape, _stream(stream))
+    if status:
+        raise PhotonError(status, "photon_cache_compact")
 
 
 def photon_paged_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, scale: float,

@@ -17,6 +17,7 @@
 #include "photon_common.cuh"
 #include "prompt_attention.cuh"
 #include "qk_norm_rope.cuh"
+#include "speculate.cuh"
 
 namespace photon {
 // selftest.cu
@@ -906,6 +907,270 @@ photon_status_t photon_prompt_attention(const void* q, int64_t q_stride, const v
   a.max_query_len = max_query_len;
   a.dtype = shape->dtype;
   return photon::launch_prompt_attention(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PHOTON_OK
+             : PHOTON_ERR_CUDA;
+}
+
+// ---- a speculative step from drafted trees
+
+photon_status_t photon_rope_cache_append(const void* q, int64_t q_stride, const void* k,
+                                         int64_t k_stride, const void* v, int64_t v_stride,
+                                         const int32_t* positions, const void* rope_cos_sin,
+                                         int32_t max_positions, int32_t rotary_dim,
+                                         int32_t interleaved, const int64_t* slot_mapping,
+                                         int32_t num_tokens, void* q_out, int64_t q_out_stride,
+                                         void* k_cache, void* v_cache,
+                                         const photon_paged_shape_t* shape,
+                                         photon_stream_t stream) {
+  photon_status_t st = check_shape(shape);
+  if (st != PHOTON_OK) return st;
+  if (num_tokens < 0 || max_positions <= 0 || interleaved < 0 || interleaved > 1 ||
+      rotary_dim <= 0 || rotary_dim > shape->head_dim || !q != !q_out)
+    return PHOTON_ERR_INVALID_ARG;
+  if (rotary_dim % 16 != 0) return PHOTON_ERR_UNSUPPORTED;
+  photon::RopeAppendArgs a{};
+  const size_t eb = elem_bytes(shape->dtype);
+  const int64_t qrow = (int64_t)shape->num_q_heads * shape->head_dim;
+  const int64_t krow = (int64_t)shape->num_kv_heads * shape->head_dim;
+  if ((st = token_stride(q_stride, qrow, eb, &a.q_stride)) != PHOTON_OK) return st;
+  if ((st = token_stride(k_stride, krow, eb, &a.k_stride)) != PHOTON_OK) return st;
+  if ((st = token_stride(v_stride, krow, eb, &a.v_stride)) != PHOTON_OK) return st;
+  if ((st = token_stride(q_out_stride, qrow, eb, &a.q_out_stride)) != PHOTON_OK) return st;
+  if (num_tokens == 0) return PHOTON_OK;
+  if (!k || !v || !positions || !rope_cos_sin || !slot_mapping || !k_cache || !v_cache)
+    return PHOTON_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(rope_cos_sin) ||
+      !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return PHOTON_ERR_MISALIGNED;
+  if ((st = error_word(&a.err)) != PHOTON_OK) return st;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.positions = positions;
+  a.cs = static_cast<const float2*>(rope_cos_sin);
+  a.slots = slot_mapping;
+  a.q_out = q_out;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.T = num_tokens;
+  a.Hq = q ? shape->num_q_heads : 0;
+  a.Hkv = shape->num_kv_heads;
+  a.D = shape->head_dim;
+  a.NB = shape->num_blocks;
+  a.max_pos = max_positions;
+  a.dtype = shape->dtype;
+  a.half = rotary_dim / 2;
+  a.interleaved = interleaved;
+  return photon::launch_rope_append(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PHOTON_OK
+             : PHOTON_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Workspace of photon_paged_tree_attention: [pairs][(m, l)][o], the last two for
+// every query row and for kTreeRows rows of every CTA.
+struct TreeLayout {
+  size_t off_ml, off_o, total;
+  int groups;
+};
+
+// Sizes that the kernels count in 32 bits.
+photon_status_t check_tree(const photon_paged_shape_t* s, int32_t num_tokens,
+                           int32_t max_query_len) {
+  const photon_status_t st = check_shape(s);
+  if (st != PHOTON_OK) return st;
+  if (s->dtype == PHOTON_F32) return PHOTON_ERR_UNSUPPORTED;
+  if (num_tokens < 0 || max_query_len < 0) return PHOTON_ERR_INVALID_ARG;
+  if (max_query_len > photon::kTreeNodes) return PHOTON_ERR_UNSUPPORTED;
+  const int64_t G = s->num_q_heads / s->num_kv_heads;
+  const int64_t groups = (max_query_len * G + photon::kTreeRows - 1) / photon::kTreeRows;
+  const int64_t span = (int64_t)s->max_blocks_per_seq * s->block_size;
+  const int64_t pairs = (int64_t)s->num_seqs * s->num_kv_heads * std::max<int64_t>(groups, 1);
+  if (pairs * (span / photon::kTreeChunk + 1 + photon::kTreePairCost) >= (1 << 30) ||
+      (int64_t)s->num_blocks * s->num_kv_heads * s->block_size > INT_MAX ||
+      (int64_t)num_tokens * s->num_q_heads > INT_MAX / 2)
+    return PHOTON_ERR_UNSUPPORTED;
+  return PHOTON_OK;
+}
+
+TreeLayout tree_layout(const photon_paged_shape_t* s, int32_t num_tokens, int32_t max_query_len) {
+  TreeLayout w{};
+  const int G = s->num_q_heads / s->num_kv_heads;
+  w.groups = (max_query_len * G + photon::kTreeRows - 1) / photon::kTreeRows;
+  const size_t rows = (size_t)num_tokens * s->num_q_heads +
+                      (size_t)photon::kTreeMaxCtas * photon::kTreeRows;
+  w.off_ml = round_up((size_t)s->num_seqs * s->num_kv_heads * w.groups * sizeof(int2), 256);
+  w.off_o = w.off_ml + round_up(rows * sizeof(float2), 256);
+  w.total = w.off_o + round_up(rows * s->head_dim * sizeof(float), 256);
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t photon_paged_tree_attention_workspace_size(const photon_paged_shape_t* shape,
+                                                  int32_t num_tokens, int32_t max_query_len) {
+  if (check_tree(shape, num_tokens, max_query_len) != PHOTON_OK || shape->num_seqs == 0 ||
+      num_tokens == 0 || max_query_len == 0)
+    return 0;
+  return tree_layout(shape, num_tokens, max_query_len).total;
+}
+
+photon_status_t photon_paged_tree_attention(const void* q, const void* k_cache,
+                                            const void* v_cache, const int32_t* block_tables,
+                                            const int32_t* context_lens,
+                                            const int32_t* query_start, const int32_t* parents,
+                                            int32_t num_tokens, int32_t max_query_len, float scale,
+                                            void* out, void* workspace, size_t workspace_bytes,
+                                            const photon_paged_shape_t* shape,
+                                            photon_stream_t stream) {
+  photon_status_t st = check_tree(shape, num_tokens, max_query_len);
+  if (st != PHOTON_OK) return st;
+  if (!std::isfinite(scale)) return PHOTON_ERR_INVALID_ARG;
+  if (shape->num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PHOTON_OK;
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start || !parents ||
+      !out)
+    return PHOTON_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
+      (reinterpret_cast<uintptr_t>(context_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(query_start) & 3u) ||
+      (reinterpret_cast<uintptr_t>(parents) & 3u))
+    return PHOTON_ERR_MISALIGNED;
+  const TreeLayout w = tree_layout(shape, num_tokens, max_query_len);
+  if (!workspace || workspace_bytes < w.total) return PHOTON_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return PHOTON_ERR_MISALIGNED;
+  photon::TreeArgs a{};
+  if ((st = error_word(&a.err)) != PHOTON_OK) return st;
+  if ((st = num_sms(&a.num_sms)) != PHOTON_OK) return st;
+  char* ws = static_cast<char*>(workspace);
+  a.ws_pair = reinterpret_cast<int2*>(ws);
+  a.ws_ml = reinterpret_cast<float2*>(ws + w.off_ml);
+  a.ws_o = reinterpret_cast<float*>(ws + w.off_o);
+  a.groups = w.groups;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.parents = parents;
+  a.out = out;
+  a.qscale = (float)((double)scale * 1.4426950408889634);
+  a.B = shape->num_seqs;
+  a.Hq = shape->num_q_heads;
+  a.Hkv = shape->num_kv_heads;
+  a.D = shape->head_dim;
+  a.NB = shape->num_blocks;
+  a.MBS = shape->max_blocks_per_seq;
+  a.num_tokens = num_tokens;
+  a.max_query_len = max_query_len;
+  a.dtype = shape->dtype;
+  return photon::launch_tree_attention(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PHOTON_OK
+             : PHOTON_ERR_CUDA;
+}
+
+photon_status_t photon_verify_tree(const void* target_probs, int64_t target_stride,
+                                   const void* draft_probs, int64_t draft_stride, int32_t vocab,
+                                   int32_t dtype, const int32_t* tokens, const int32_t* parents,
+                                   const int32_t* query_start, const float* accept_uniforms,
+                                   const float* sample_uniforms, int32_t num_seqs,
+                                   int32_t num_tokens, int32_t max_query_len, int32_t* path,
+                                   int32_t* path_len, int32_t* next_token,
+                                   photon_stream_t stream) {
+  if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0 || vocab <= 0 || target_stride < 0 ||
+      draft_stride < 0)
+    return PHOTON_ERR_INVALID_ARG;
+  if (dtype != PHOTON_F32 && dtype != PHOTON_F16 && dtype != PHOTON_BF16)
+    return PHOTON_ERR_UNSUPPORTED;
+  if (max_query_len > photon::kTreeNodes || vocab > photon::kVerifyVocab || num_seqs > 65535)
+    return PHOTON_ERR_UNSUPPORTED;
+  photon::VerifyArgs a{};
+  a.target_stride = target_stride ? target_stride : vocab;
+  a.draft_stride = draft_stride ? draft_stride : vocab;
+  if (a.target_stride < vocab || a.draft_stride < vocab) return PHOTON_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PHOTON_OK;
+  if (!target_probs || !tokens || !parents || !query_start || !accept_uniforms ||
+      !sample_uniforms || !path || !path_len || !next_token)
+    return PHOTON_ERR_INVALID_ARG;
+  const uintptr_t elem = elem_bytes(dtype) - 1;
+  if ((reinterpret_cast<uintptr_t>(target_probs) & elem) ||
+      (reinterpret_cast<uintptr_t>(draft_probs) & elem))
+    return PHOTON_ERR_MISALIGNED;
+  const void* words[] = {tokens, parents, query_start, accept_uniforms, sample_uniforms, path,
+                         path_len, next_token};
+  for (const void* p : words)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return PHOTON_ERR_MISALIGNED;
+  photon_status_t st;
+  if ((st = error_word(&a.err)) != PHOTON_OK) return st;
+  if ((st = num_sms(&a.num_sms)) != PHOTON_OK) return st;
+  a.target = target_probs;
+  a.draft = draft_probs;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.query_start = query_start;
+  a.accept = accept_uniforms;
+  a.sample = sample_uniforms;
+  a.path = path;
+  a.path_len = path_len;
+  a.next = next_token;
+  a.B = num_seqs;
+  a.num_tokens = num_tokens;
+  a.max_query_len = max_query_len;
+  a.vocab = vocab;
+  a.dtype = dtype;
+  return photon::launch_verify_tree(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PHOTON_OK
+             : PHOTON_ERR_CUDA;
+}
+
+photon_status_t photon_cache_compact(void* const* pools, int32_t num_pools,
+                                     const int32_t* block_tables, const int32_t* context_lens,
+                                     const int32_t* query_start, const int32_t* path,
+                                     const int32_t* path_len, int32_t num_tokens,
+                                     int32_t max_query_len, const photon_paged_shape_t* shape,
+                                     photon_stream_t stream) {
+  photon_status_t st = check_shape(shape);
+  if (st != PHOTON_OK) return st;
+  if (num_pools < 0 || num_tokens < 0 || max_query_len < 0) return PHOTON_ERR_INVALID_ARG;
+  if (num_pools > photon::kCompactPools || max_query_len > photon::kTreeNodes)
+    return PHOTON_ERR_UNSUPPORTED;
+  if (num_pools == 0 || shape->num_seqs == 0 || num_tokens == 0 || max_query_len == 0)
+    return PHOTON_OK;
+  if (!pools || !block_tables || !context_lens || !query_start || !path || !path_len)
+    return PHOTON_ERR_INVALID_ARG;
+  photon::CompactArgs a{};
+  for (int i = 0; i < num_pools; ++i) {
+    if (!pools[i]) return PHOTON_ERR_INVALID_ARG;
+    if (!aligned16(pools[i])) return PHOTON_ERR_MISALIGNED;
+    a.pools[i] = pools[i];
+  }
+  const void* words[] = {block_tables, context_lens, query_start, path, path_len};
+  for (const void* p : words)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return PHOTON_ERR_MISALIGNED;
+  if ((st = error_word(&a.err)) != PHOTON_OK) return st;
+  if ((st = num_sms(&a.num_sms)) != PHOTON_OK) return st;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.path = path;
+  a.path_len = path_len;
+  a.num_pools = num_pools;
+  a.B = shape->num_seqs;
+  a.Hkv = shape->num_kv_heads;
+  a.row_bytes = shape->head_dim * (int)elem_bytes(shape->dtype);
+  a.NB = shape->num_blocks;
+  a.MBS = shape->max_blocks_per_seq;
+  a.num_tokens = num_tokens;
+  a.max_query_len = max_query_len;
+  return photon::launch_cache_compact(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PHOTON_OK
              : PHOTON_ERR_CUDA;
 }

@@ -125,15 +125,6 @@ __device__ __forceinline__ uint64_t pa_v_desc(uint32_t saddr) {
   return d;
 }
 
-__device__ __forceinline__ void tma_load_box3(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                              int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-      "%3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-      : "memory");
-}
-
 // Tensor copy of a box from shared memory to global memory, in a bulk group of
 // its own.
 __device__ __forceinline__ void tma_store_box3(const CUtensorMap* map, int x, int y, int z,
@@ -148,23 +139,6 @@ __device__ __forceinline__ void tma_store_box3(const CUtensorMap* map, int x, in
 template <int N>
 __device__ __forceinline__ void bulk_store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
-// Bounded wait for a barrier phase, by a whole warp; false after kWaitLimitNs,
-// or once any other warp of the CTA has given up.
-__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!__all_sync(0xffffffffu, ok)) {
-    const unsigned long long t0 = global_timer_ns();
-    while (!ok) {
-#pragma unroll 1
-      for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(bar, parity);
-      if (ok || *gave_up) break;
-      if (global_timer_ns() - t0 > kWaitLimitNs) *gave_up = 1;
-    }
-    ok = __all_sync(0xffffffffu, ok);
-  }
-  return ok;
 }
 
 struct PaItem {
@@ -365,7 +339,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   // the CTA's m-th item, from the warp that finds them; false past the last one
   auto take = [&](uint32_t m, PaItem& to) -> bool {
     const int slot = m % kPaItems;
-    ok = pa_wait(&item_full[slot], (m / kPaItems) & 1, gave_up);
+    ok = cta_wait(&item_full[slot], (m / kPaItems) & 1, gave_up);
     if (!ok) return false;
     const int4 v = items[slot];
     __syncwarp();
@@ -413,7 +387,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         // cache, and the rarely taken masks then cost thousands of clocks).
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          ok = pa_wait(&s_full[t][half], done & 1, gave_up);
+          ok = cta_wait(&s_full[t][half], done & 1, gave_up);
           if (!ok) break;
           tc_fence_after();
           const uint32_t t_h = t_s + kPaHalf * half;
@@ -449,7 +423,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               }
               if (c > 0 || half > 0) {
                 // the product of the half before still adds to O
-                ok = pa_wait(&o_done[t][1 - half], (half ? done : done - 1) & 1, gave_up);
+                ok = cta_wait(&o_done[t][1 - half], (half ? done : done - 1) & 1, gave_up);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -490,7 +464,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       have = take(m, next);   // while the last product runs
       if (!ok) break;
       // ---- O / l
-      ok = pa_wait(&o_done[t][1], (done - 1) & 1, gave_up);
+      ok = cta_wait(&o_done[t][1], (done - 1) & 1, gave_up);
       if (!ok) break;
       tc_fence_after();
       // Through shared memory in the copies' swizzled layout.  A warp whose 32
@@ -557,7 +531,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const int chunks = max(t0.chunks, t1.chunks);
         for (int c = 0; c < chunks && ok; ++c, ++kc) {
           const int st = kc % SK;
-          if (kc >= SK) ok = pa_wait(&k_free[st], ((kc / SK) - 1) & 1, gave_up);
+          if (kc >= SK) ok = cta_wait(&k_free[st], ((kc / SK) - 1) & 1, gave_up);
           if (!ok) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(&k_full[st], C::kKvBytes);
@@ -570,7 +544,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           if (c > 0) continue;
           // the Q tiles, after the first chunk is on its way
           for (int t = 0; t < kPaTiles && ok; ++t) {
-            if (m > 0) ok = pa_wait(&q_free[t], (m - 1) & 1, gave_up);
+            if (m > 0) ok = cta_wait(&q_free[t], (m - 1) & 1, gave_up);
             if (!ok) break;
             ++q_count[t];
             if (lane != 0) continue;
@@ -602,7 +576,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const int chunks = max(t0.chunks, t1.chunks), kend = max(t0.kend, t1.kend);
         for (int c = 0; c < chunks && ok; ++c, ++vc) {
           const int st = vc % SV;
-          if (vc >= SV) ok = pa_wait(&v_free[st], ((vc / SV) - 1) & 1, gave_up);
+          if (vc >= SV) ok = cta_wait(&v_free[st], ((vc / SV) - 1) & 1, gave_up);
           if (!ok) break;
           // The products read whole groups of 16 keys.  Rows past the last key
           // meet zero weights, but 0 x NaN would not vanish: the last chunk
@@ -620,7 +594,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           }
           __syncwarp();
           if (fill) {
-            ok = pa_wait(&v_tail, tails & 1, gave_up);
+            ok = cta_wait(&v_tail, tails & 1, gave_up);
             if (!ok) {
               (void)mbar_wait_bounded(&v_tail, tails & 1);   // its copy, in flight
               break;
@@ -649,7 +623,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const uint32_t N = gridDim.x;
       for (uint32_t m = 0, run = 0;; ++m, run += N) {
         const int slot = m % kPaItems;
-        if (m >= kPaItems) ok = pa_wait(&item_free[slot], ((m / kPaItems) - 1) & 1, gave_up);
+        if (m >= kPaItems) ok = cta_wait(&item_free[slot], ((m / kPaItems) - 1) & 1, gave_up);
         if (!ok) break;
         // one item from each run of N, forwards and backwards in turn
         const bool found =
@@ -681,17 +655,17 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         for (uint32_t m = 0; ok && take(m, it); ++m) {
           const PaTile mine = pa_tile(it, g2, t), other = pa_tile(it, g2, 1 - t);
           const int chunks = max(mine.chunks, other.chunks);
-          ok = pa_wait(&q_full[t], m & 1, gave_up);
+          ok = cta_wait(&q_full[t], m & 1, gave_up);
           if (!ok) break;
           if (mine.chunks == 0 && lane == 0) mbar_arrive(&q_free[t]);
           for (int c = 0; c < chunks; ++c) {
             const uint32_t kc = chunk0 + c;
-            ok = pa_wait(&k_full[kc % SK], (kc / SK) & 1, gave_up);
+            ok = cta_wait(&k_full[kc % SK], (kc / SK) & 1, gave_up);
             if (ok && c < mine.chunks) {
               const uint64_t kb = k_desc + (uint64_t)(((kc % SK) * C::kKvBytes) >> 4);
               for (int h = 0; h < 2; ++h) {
                 // P of the last chunk's half, which lies over S, is used
-                if (done > 0) ok = pa_wait(&o_done[t][h], (done - 1) & 1, gave_up);
+                if (done > 0) ok = cta_wait(&o_done[t][h], (done - 1) & 1, gave_up);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
@@ -710,7 +684,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               }
               if (!ok) break;
               ++done;
-              ok = pa_wait(&s_full[t][1], (done - 1) & 1, gave_up);
+              ok = cta_wait(&s_full[t][1], (done - 1) & 1, gave_up);
             }
             if (!ok) break;
             if (lane == 0) mbar_arrive(&k_free[kc % SK]);
@@ -728,12 +702,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           for (int c = 0; c < chunks; ++c) {
             const uint32_t vc = chunk0 + c;
             if (held != kNothing) {
-              ok = pa_wait(&o_done[t][1], (done - 1) & 1, gave_up);
+              ok = cta_wait(&o_done[t][1], (done - 1) & 1, gave_up);
               if (!ok) break;
               if (lane == 0) mbar_arrive(&v_free[held % SV]);
               held = kNothing;
             }
-            ok = pa_wait(&v_full[vc % SV], (vc / SV) & 1, gave_up);
+            ok = cta_wait(&v_full[vc % SV], (vc / SV) & 1, gave_up);
             if (!ok) break;
             if (c >= mine.chunks) {   // a chunk of the other tile only
               if (lane == 0) mbar_arrive(&v_free[vc % SV]);
@@ -744,7 +718,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             // 64 keys at a time, as their weights become ready; a half without
             // keys has nothing to add, only its barrier to complete
             for (int h = 0; h < 2; ++h) {
-              ok = pa_wait(&p_full[t][h], done & 1, gave_up);
+              ok = cta_wait(&p_full[t][h], done & 1, gave_up);
               if (!ok) break;
               tc_fence_after();
               auto product = [&](int kk) {

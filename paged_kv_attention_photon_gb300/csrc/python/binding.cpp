@@ -127,7 +127,11 @@ PyObject* call(photon_status_t (*fn)(A...), const char* name, PyObject* const* a
   X(photon_paged_gather_int4)    \
   X(photon_paged_decode_int4)    \
   X(photon_qk_norm_rope)         \
-  X(photon_prompt_attention)
+  X(photon_prompt_attention)     \
+  X(photon_rope_cache_append)    \
+  X(photon_paged_tree_attention) \
+  X(photon_verify_tree)          \
+  X(photon_cache_compact)
 
 #define PHOTON_DEFINE(name)                                                         \
   decltype(&::name) g_##name;                                                       \

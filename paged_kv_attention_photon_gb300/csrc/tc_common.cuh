@@ -102,6 +102,34 @@ __device__ __forceinline__ void tc_fence_after() {
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+// 3-D tiled bulk tensor copy of one box into this CTA's shared memory, completing
+// on `bar`.
+__device__ __forceinline__ void tma_load_box3(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                              int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Bounded wait for a barrier phase, by a whole warp; false after kWaitLimitNs,
+// or once any other warp of the CTA has given up.
+__device__ __forceinline__ bool cta_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    const unsigned long long t0 = global_timer_ns();
+    while (!ok) {
+#pragma unroll 1
+      for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+      if (ok || *gave_up) break;
+      if (global_timer_ns() - t0 > kWaitLimitNs) *gave_up = 1;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  return ok;
+}
+
 // 32 consecutive fp32 columns of this thread's TMEM lane.  The wait sits in
 // the same asm statement as the load, so no use of the registers can be
 // scheduled before the data has arrived.

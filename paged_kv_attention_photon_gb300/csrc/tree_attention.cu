@@ -1,0 +1,910 @@
+// tree_attention.cu -- attention of each sequence's drafted tree over its paged
+// cache, on the fifth-generation tensor cores.
+//
+// PhotonInfer README, "Technical details / Paged attention" (block-wise KV cache,
+// per-sequence offsets); "Roadmap" (speculative decoding; FlashAttention-2 style
+// attention for long sequences).
+//
+// Node i of a tree of n nodes, whose rows are the last n of a context, attends to
+// the context before the tree, to its ancestors and to itself:
+// out = sum_j softmax_j(scale q . k_j) v_j over those keys.  A row of K and V is
+// read once for all n G query rows (node, head of the group) of its KV head: 2 n G
+// flops a byte at 16 bits, so memory bounds it up to about 280 rows and the tensor
+// cores above.  mma.sync would do for 8 rows or so (photon_paged_multi_query's
+// few-token mode); from 16 on only tcgen05 keeps up with memory, and as memory
+// bounds it the rows of a 128-row product that a small tree leaves empty cost nothing.
+//
+// A persistent CTA per SM takes runs of 128-key chunks of (sequence, KV head, group
+// of 256 rows).  Two tiles of 128 rows each have scores S and sums O in tensor
+// memory.  With more than 128 rows each tile has its own rows and sees every chunk;
+// with up to 128 both tiles have the same rows and take every other chunk, so that
+// one tile's softmax runs beside the other's products; their sums meet at the end
+// through shared memory.  S, softmax and P V go by halves of 64 keys; P of a half
+// lies over its S as 16-bit pairs.  15 warps in fixed roles:
+//   warps 0-3, 4-7  softmax of tile 0, 1: thread r owns TMEM lane r
+//   warp 8, 9       tensor-map copies of Q and K, of V: 16-row boxes through the table
+//   warp 10, 11     issue S of tile 0, 1
+//   warp 12, 13     issue P V of tile 0, 1
+//   warp 14         finds the items, and the ancestors of each node
+//
+// Which keys a node sees of its tree is a bit mask of its ancestors, found by
+// doubling (node i takes its ancestor's mask and the ancestor's ancestor, until all
+// have reached the root) when an item holds the tree's keys.  Only the chunks that
+// hold some are masked, 64 bits a row and half.
+//
+// The chunks of all (sequence, KV head, group) triples lie on one line, each triple
+// counting kTreePairCost more than it has for what beginning and ending it costs;
+// the line is cut into equal runs, one per CTA: no queue and no atomics, so results
+// do not depend on timing.  A triple within one run is written out at once, the
+// others leave partial sums, joined by a second kernel.
+//
+// Numerics: products of the stored values, sums and statistics in fp32; weights P
+// enter the second product rounded to the storage type, as in
+// photon_paged_multi_query and photon_prompt_attention: a product with their
+// rounding errors besides would be half again as many.  fp16 weights are lifted to
+// the upper end of fp16's range (kLift), so that what they lose lies below 2^-32 of
+// the largest.
+//
+// Barriers complete once per use; use i has parity i & 1:
+//   k_full, v_full[st]   a chunk landed      k_free, v_free[st]  both tiles are done with it
+//   q_full               the item's Q        q_free              both tiles' last S is done
+//   s_full[t][h]         S of 64 keys        p_full[t][h]        their P written
+//   o_done[t][h]         O += P V of 64 keys done; the next chunk's S may overwrite P
+//   item_full, item_free[i]  an item is known; every role has read it
+//   mask_full, mask_free     the ancestors of an item's tree; every softmax warp has used them
+//   meet_full, meet_free[w]  32 columns of one tile's O are in shared memory; the other has taken them
+// Where a wait runs out the CTA gives up, and what it has in flight still lands
+// first: the copying warps wait (bounded) for their last copies, the issuing ones on
+//   drained[i]           every product that the warp has issued is done
+#include <math.h>
+
+#include <algorithm>
+
+#include "speculate.cuh"
+#include "tc_common.cuh"
+
+namespace photon {
+namespace {
+
+constexpr int kRows = 128;              // query rows of a tile = TMEM lanes
+constexpr int kKeys = kTreeChunk;       // keys of a chunk
+constexpr int kHalf = 64;               // keys of an S product, of a softmax step and of a P V product
+constexpr int kChunkBlocks = kKeys / kBlockSize;
+constexpr int kTiles = 2;
+constexpr int kThreads = 512;           // four warpgroups; warp 15 has no role
+// Registers a thread: 512 x 128 at launch, dealt anew to the softmax warpgroups and
+// the other two (160 + 160 + 96 + 96 = 4 x 128).
+constexpr int kSoftmaxRegs = 160, kOtherRegs = 96;
+constexpr uint32_t kTmemO = 256;        // S of tile t: columns [128 t, 128 t + 128); then the O's
+constexpr float kRescale = 8.f;         // the running maximum moves by 2^8 or not at all
+// Weights are 2^(score - maximum + lift): see the top.
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
+constexpr float kNoMax = -3e38f;        // before the first key; finite, so that no exponent is inf - inf
+// From here on (2^23) fp32 scores are whole units of the exponent apart, and the
+// scaled maximum, rounded, would move all weights by half a unit and more: the
+// exponents then take the scale's power of two alone, which is exact.
+constexpr float kFar = 8388608.f;
+constexpr int kItems = 4;               // items found ahead
+constexpr int kRoles = 14;              // warps that work on an item
+constexpr int kMaskWords = kTreeNodes / 32, kMaskStride = kMaskWords + 1;
+constexpr int kGoneRing = 8;            // more than the chunks between a copy and its softmax
+
+template <int D>
+struct Cfg {
+  static constexpr int kKStages = D == 128 ? 2 : 4;
+  static constexpr int kVStages = D == 128 ? 2 : 4;
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kKvBytes = kKeys * D * 2;
+  static constexpr int kOffK = kTiles * kQBytes;
+  static constexpr int kOffV = kOffK + kKStages * kKvBytes;
+  static constexpr int kOffMeet = kOffV + kVStages * kKvBytes;   // 4 warps x 32 columns x 32 rows
+  static constexpr int kOffMask = kOffMeet + 4 * 4096;
+  static constexpr int kSmem = kOffMask + kTreeNodes * kMaskStride * 4 + 1024;   // + alignment to a swizzle atom
+  static_assert(kGoneRing >= kKStages + 2 && kGoneRing >= kVStages + 2, "the ring of missing blocks");
+};
+
+// MN-major V operand (sw128_desc walked along N): 64-element blocks of N are kKeys
+// rows of 128 bytes apart (leading offset), groups of 8 keys 1 KB.
+__device__ __forceinline__ uint64_t v_operand(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+  d |= (uint64_t)((kKeys * 128) >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// A sequence's tree and context; n == 0: empty or rejected.
+struct Seq {
+  int q0, n, ctx;
+};
+__device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b) {
+  Seq s{0, 0, 0};
+  if (b >= a.B) return s;
+  const int q0 = __ldg(a.query_start + b), q1 = __ldg(a.query_start + b + 1);
+  const int ctx = __ldg(a.context_lens + b);
+  if (q0 < 0 || q1 <= q0 || q1 > a.num_tokens || q1 - q0 > a.max_query_len || ctx < q1 - q0 ||
+      ctx > a.MBS * kBlockSize)
+    return s;
+  s.q0 = q0;
+  s.n = q1 - q0;
+  s.ctx = ctx;
+  return s;
+}
+__device__ __forceinline__ int chunks_of(int ctx) { return (ctx + kKeys - 1) / kKeys; }
+__device__ __forceinline__ int groups_of(int n, int G) { return (n * G + kTreeRows - 1) / kTreeRows; }
+// Units of a sequence on the line.
+__device__ __forceinline__ int units_of(const TreeArgs& a, const Seq& s, int G) {
+  return s.n == 0 ? 0 : a.Hkv * groups_of(s.n, G) * (chunks_of(s.ctx) + kTreePairCost);
+}
+
+// Chunks [c0, c1) of row group g of (sequence b, KV head kvh).
+struct Item {
+  int b, kvh, g, c0;
+  int c1, q0, n, ctx;
+  int place;   // where the sums go: 0 out, 1 the rows' own partials, 2 the CTA's
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
+  using C = Cfg<D>;
+  constexpr int SK = C::kKStages, SV = C::kVStages;
+  extern __shared__ unsigned char tree_smem_raw[];
+  __shared__ __align__(8) uint64_t k_full[SK], k_free[SK], v_full[SV], v_free[SV], q_full, q_free,
+      s_full[kTiles][2], p_full[kTiles][2], o_done[kTiles][2], item_full[kItems],
+      item_free[kItems], mask_full, mask_free, meet_full[4], meet_free[4], drained[2 * kTiles];
+  __shared__ int4 items[kItems][3];
+  __shared__ float2 meet_ml[4][32];
+  __shared__ uint8_t k_gone[kGoneRing], v_gone[kGoneRing];   // blocks of a chunk that are not there
+  __shared__ int up[kTreeNodes];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int gave_up_word;
+  volatile int* gave_up = &gave_up_word;
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(tree_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sQ = smem_addr(smem), sK = sQ + C::kOffK, sV = sQ + C::kOffV;
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::kOffMask);
+  auto uniform = [](uint32_t x) -> uint32_t { return __shfl_sync(0xffffffffu, x, 0); };
+  const int tid = threadIdx.x, warp = (int)uniform(tid >> 5), lane = tid & 31;
+  const int G = a.Hq / a.Hkv, g2 = __ffs(G) - 1;   // a power of two
+
+  if (tid == 0) {
+    gave_up_word = 0;
+    for (int i = 0; i < SK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_free[i], kTiles);
+    }
+    for (int i = 0; i < SV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_free[i], kTiles);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_free, kTiles);
+    for (int t = 0; t < kTiles; ++t)
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&s_full[t][h], 1);
+        mbar_init(&p_full[t][h], 4);   // one arrival per softmax warp
+        mbar_init(&o_done[t][h], 1);
+      }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_free[i], kRoles);
+    }
+    mbar_init(&mask_full, 1);
+    mbar_init(&mask_free, 8);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&meet_full[i], 1);
+      mbar_init(&meet_free[i], 1);
+    }
+    for (int i = 0; i < 2 * kTiles; ++i) mbar_init(&drained[i], 1);
+    mbar_init_fence();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 32 * 8) {
+    prefetch_tensor_map(&tm_q);
+    prefetch_tensor_map(&tm_k);
+  }
+  if (tid == 32 * 9) prefetch_tensor_map(&tm_v);
+  pdl_wait_primary();
+  pdl_launch_dependents();   // the merge reads lengths before its own wait: not sooner
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(tmem_slot);
+
+  bool ok = true;
+  Item it;
+  // the CTA's m-th item, from the warp that finds them; false past the last one
+  auto take = [&](uint32_t m, Item& to) -> bool {
+    const int slot = m % kItems;
+    ok = cta_wait(&item_full[slot], (m / kItems) & 1, gave_up);
+    if (!ok) return false;
+    const int4 x = items[slot][0], y = items[slot][1];
+    to.place = items[slot][2].x;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_free[slot]);
+    to.b = x.x, to.kvh = x.y, to.g = x.z, to.c0 = x.w;
+    to.c1 = y.x, to.q0 = y.y, to.n = y.z, to.ctx = y.w;
+    return to.n > 0;
+  };
+  // rows of the item's group; whether each tile has rows of its own
+  auto rows_of = [&](const Item& i) { return min(kTreeRows, (i.n << g2) - i.g * kTreeRows); };
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ================================================================ softmax rows
+    const int t = warp >> 2, w4 = warp & 3;
+    const int trow = w4 * 32 + lane;           // row inside the tile = TMEM lane
+    const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + t * kKeys;
+    const uint32_t t_o = tmem + lane_base + kTmemO + t * D;
+    const float qscale = a.qscale;
+    // a zero scale as a tiny one: every weight is 1 and -inf stays -inf
+    const float qmul = fmaxf(fabsf(qscale), 1e-37f);
+    uint32_t done = 0, chunk0 = 0, met = 0, masked = 0;   // this tile's chunks, the CTA's, exchanges, masks used
+    Item next;
+    bool have = take(0, next);
+    for (uint32_t m = 0; ok && have; ++m) {
+      it = next;
+      const int rows = rows_of(it), n_chunks = it.c1 - it.c0;
+      const bool apart = rows > kRows;                 // each tile has rows of its own
+      const int main = m & 1;                          // else the tile that ends the item
+      const int my_rows = apart && t == 1 ? rows - kRows : min(rows, kRows);
+      const bool active = w4 * 32 < my_rows;           // a row of the warp is there
+      const int group_row = apart ? t * kRows + trow : trow;
+      const int row = it.g * kTreeRows + min(group_row, rows - 1);   // (node, head) of the sequence
+      const int tree0 = it.ctx - it.n;
+      const bool has_tree = it.c1 * kKeys > tree0;     // the item holds keys of the tree
+      const uint32_t* mask = masks + (row >> g2) * kMaskStride;
+      bool mask_there = false;
+      float m_run = kNoMax, l_run = 0.f;   // running maximum, unscaled; sum of weights
+      float qm = qmul, base = 0.f;
+      bool begun = false;
+      for (int lc = 0; lc < n_chunks; ++lc) {
+        if (!apart && ((lc + main) & 1) != t) continue;
+        const int key0 = (it.c0 + lc) * kKeys;
+        const int valid = min(kKeys, it.ctx - key0);
+        uint32_t gone = 0;
+        // Half a chunk at a time: scores, maximum, weights.  One instance of the
+        // code, so that it stays in the instruction cache.
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          ok = cta_wait(&s_full[t][half], done & 1, gave_up);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t t_h = t_s + kHalf * half;
+          if (active && (half == 0 || valid > kHalf)) {
+            if (half == 0) gone = k_gone[(chunk0 + lc) % kGoneRing];
+            const int k0 = key0 + kHalf * half;
+            float s[64];
+            tmem_ld64(t_h, s);
+            const uint32_t gone4 = (gone >> (4 * half)) & 15u;
+            if (k0 + kHalf > tree0 || gone4) {
+              // which of the 64 keys the row sees
+              if (has_tree && !mask_there) {
+                ok = cta_wait(&mask_full, masked & 1, gave_up);
+                if (!ok) break;
+                mask_there = true;
+              }
+              const int rel = k0 - tree0;   // first key, counted from the tree's
+              uint64_t see = ~0ull;
+              if (rel > -kHalf) {
+                auto word = [&](int i) -> uint64_t { return i < kMaskWords ? mask[i] : 0u; };
+                if (rel < 0) {
+                  see = ((word(0) | word(1) << 32) << -rel) | ((1ull << -rel) - 1);
+                } else {
+                  const int i = rel >> 5, by = rel & 31;
+                  see = (word(i) | word(i + 1) << 32) >> by;
+                  if (by) see |= word(i + 2) << (64 - by);
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if ((gone4 >> i) & 1u) see &= ~(0xffffull << (16 * i));
+              const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                s[j] = (lo >> j) & 1u ? s[j] : -INFINITY;
+                s[32 + j] = (hi >> j) & 1u ? s[32 + j] : -INFINITY;
+              }
+            }
+            float m8[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m8[k] = fmaxf(s[k], s[8 + k]);
+#pragma unroll
+            for (int j = 16; j < 64; j += 16)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], s[j + k], s[j + 8 + k]);
+            const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]),
+                                   fmax3(fmaxf(m8[3], m8[4]), fmaxf(m8[5], m8[6]), m8[7]));
+            // The running maximum only moves when a score passes it by more than
+            // 2^8, and only then is O rescaled: weights stay below 2^8 times the
+            // lift, and the stale maximum cancels in O / l.
+            const bool moved = (mx - m_run) * qmul > kRescale;
+            if (__any_sync(0xffffffffu, moved)) {
+              const float corr = moved ? softmax_exp2((m_run - mx) * qmul) : 1.f;   // of nothing, at first
+              l_run *= corr;
+              if (moved) {
+                m_run = mx;
+                qm = fabsf(qmul * mx) < kFar ? qmul : __uint_as_float(__float_as_uint(qmul) & 0x7f800000u);
+                base = __fmaf_rd(-qm, mx, kLift<T>);   // lifted no further, however large
+              }
+              if (begun) {
+                // the product of the half before still adds to O
+                ok = cta_wait(&o_done[t][1 - half], (half ? done : done - 1) & 1, gave_up);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int col = 0; col < D; col += 32) {
+                  float o[32];
+                  tmem_ld32(t_o + col, o);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] *= corr;
+                  tmem_st32(t_o + col, o);
+                }
+              }
+            }
+            begun = true;
+            // weights as 16-bit pairs, over scores that are read
+            float w[32], sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float x0, x1;
+              fma_f32x2(x0, x1, s[2 * j], s[2 * j + 1], qm, base);
+              const float p0 = softmax_exp2(x0), p1 = softmax_exp2(x1);
+              add_f32x2(sum[(j & 1) * 2], sum[(j & 1) * 2 + 1], p0, p1);
+              w[j] = __uint_as_float(Mma<T>::pack(p0, p1));
+            }
+            tmem_st32(t_h, w);
+            l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[t][half]);
+        }
+        if (!ok) break;
+        ++done;
+      }
+      if (!ok) break;
+      chunk0 += n_chunks;
+      if (has_tree) {
+        // the masks go back, whether this warp has used them or not
+        if (!mask_there) ok = cta_wait(&mask_full, masked & 1, gave_up);
+        if (!ok) break;
+        ++masked;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mask_free);
+      }
+      have = take(m + 1, next);   // while the last product runs
+      if (!ok) break;
+      // ---- the item's end: O / l, or what a partial holds
+      const bool both = !apart && n_chunks > 1;   // both tiles have sums of the same rows
+      if (!active || (!apart && t != main && !both)) continue;
+      ok = cta_wait(&o_done[t][1], (done - 1) & 1, gave_up);
+      if (!ok) break;
+      tc_fence_after();
+      // what the weights' exponents exceed (score - maximum) by: the lift, and what
+      // the scaled maximum was rounded by
+      float factor = softmax_exp2(-fmaf(qm, m_run, base));
+      if (m_run == kNoMax) factor = 0.f;   // no key
+      float* meet = reinterpret_cast<float*>(smem + C::kOffMeet + w4 * 4096);
+      if (both && t != main) {
+        // to the other tile's warp of the same rows, 32 columns a turn
+        for (int col = 0; ok && col < D; col += 32, ++met) {
+          float o[32];
+          tmem_ld32(t_o + col, o);
+          if (met > 0) ok = cta_wait(&meet_free[w4], (met - 1) & 1, gave_up);
+          if (!ok) break;
+          if (col == 0) meet_ml[w4][lane] = make_float2(m_run, l_run * factor);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) meet[i * 32 + lane] = o[i] * factor;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&meet_full[w4]);
+        }
+        if (!ok) break;
+        tc_fence_before();
+        continue;
+      }
+      float other = 0.f;
+      const bool store = group_row < rows;
+      const int64_t head = (int64_t)(it.q0 + (row >> g2)) * a.Hq + it.kvh * G + (row & (G - 1));
+      const int64_t part = it.place == 2
+                               ? (int64_t)a.num_tokens * a.Hq + (int64_t)blockIdx.x * kTreeRows + group_row
+                               : head;
+      for (int col = 0; ok && col < D; col += 32) {
+        float o[32];
+        tmem_ld32(t_o + col, o);
+        if (both) {
+          ok = cta_wait(&meet_full[w4], met & 1, gave_up);
+          if (!ok) break;
+          if (col == 0) {
+            const float2 ml = meet_ml[w4][lane];
+            const float top = fmaxf(m_run, ml.x);
+            other = softmax_exp2((ml.x - top) * qmul);
+            factor *= softmax_exp2((m_run - top) * qmul);
+            l_run = fmaf(ml.y, other, l_run * factor);
+            m_run = top;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = fmaf(meet[i * 32 + lane], other, o[i] * factor);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&meet_free[w4]);
+          ++met;
+        } else {
+          if (col == 0) l_run *= factor;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= factor;
+        }
+        if (!store) continue;
+        if (it.place == 0) {
+          const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+          T* dst = static_cast<T*>(a.out) + head * D + col;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch)
+            *reinterpret_cast<uint4*>(dst + ch * 8) =
+                make_uint4(Mma<T>::pack(o[ch * 8] * inv, o[ch * 8 + 1] * inv),
+                           Mma<T>::pack(o[ch * 8 + 2] * inv, o[ch * 8 + 3] * inv),
+                           Mma<T>::pack(o[ch * 8 + 4] * inv, o[ch * 8 + 5] * inv),
+                           Mma<T>::pack(o[ch * 8 + 6] * inv, o[ch * 8 + 7] * inv));
+        } else {
+          if (col == 0) a.ws_ml[part] = make_float2(m_run, l_run);
+          float* dst = a.ws_o + part * D + col;
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch)
+            *reinterpret_cast<float4*>(dst + ch * 4) =
+                make_float4(o[ch * 4], o[ch * 4 + 1], o[ch * 4 + 2], o[ch * 4 + 3]);
+        }
+      }
+      if (!ok) break;
+      tc_fence_before();   // O is read before the next item's products (p_full orders them)
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8 || warp == 9) {
+      // ================================================================ copies
+      // warp 8: Q and K, warp 9: V.  Lane i < 8 copies block i of a chunk.
+      const bool is_v = warp == 9;
+      const int S = is_v ? SV : SK;
+      uint64_t* full = is_v ? v_full : k_full;
+      uint64_t* freed = is_v ? v_free : k_free;
+      uint8_t* missing = is_v ? v_gone : k_gone;
+      const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+      const uint32_t ring = is_v ? sV : sK;
+      uint32_t kc = 0, q_count = 0;   // chunks, Q's asked for so far
+      for (uint32_t m = 0; ok && take(m, it); ++m) {
+        const int32_t* table = a.block_tables + (int64_t)it.b * a.MBS;
+        auto block_of = [&](int c) -> int {   // -1: past the context; -2: outside the pool
+          const int i = c * kChunkBlocks + lane;
+          if (c >= it.c1 || lane >= kChunkBlocks || i * kBlockSize >= it.ctx) return -1;
+          const int id = __ldg(table + i);
+          return id >= 0 && id < a.NB ? id : -2;
+        };
+        int ahead = block_of(it.c0);
+        for (int c = it.c0; c < it.c1 && ok; ++c, ++kc) {
+          const int st = kc % S;
+          const int id = ahead;
+          ahead = block_of(c + 1);
+          if (kc >= (uint32_t)S) ok = cta_wait(&freed[st], ((kc / S) - 1) & 1, gave_up);
+          if (!ok) break;
+          const unsigned present = __ballot_sync(0xffffffffu, id >= 0);
+          const unsigned bad = __ballot_sync(0xffffffffu, id == -2);
+          if (lane == 0) {
+            missing[kc % kGoneRing] = (uint8_t)bad;   // published by the arrival below
+            if (bad && !is_v) raise_error(a.err, kErrBlock);
+            mbar_arrive_expect_tx(&full[st], __popc(present) * (kBlockSize * D * 2));
+          }
+          __syncwarp();
+          if (id >= 0) {
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_box(ring + st * C::kKvBytes + h * (kKeys * 128) + lane * (kBlockSize * 128),
+                           map, h * 64, (id * a.Hkv + it.kvh) * kBlockSize, &full[st]);
+          }
+          __syncwarp();
+          if (is_v || c > it.c0) continue;
+          // the Q tiles, after the first chunk is on its way
+          if (m > 0) ok = cta_wait(&q_free, (m - 1) & 1, gave_up);
+          if (!ok) break;
+          ++q_count;
+          if (lane == 0) {
+            const int tiles = rows_of(it) > kRows ? 2 : 1;
+            mbar_arrive_expect_tx(&q_full, tiles * C::kQBytes);
+            for (int i = 0; i < tiles; ++i)
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_box3(sQ + i * C::kQBytes + h * (kRows * 128), &tm_q, h * 64, it.kvh * G,
+                              it.q0 + ((it.g * kTreeRows + i * kRows) >> g2), &q_full);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) {
+        // what is in flight lands before the CTA ends
+        for (uint32_t c = kc > (uint32_t)S ? kc - S : 0; c < kc; ++c)
+          (void)mbar_wait_bounded(&full[c % S], (c / S) & 1);
+        if (q_count > 0) (void)mbar_wait_bounded(&q_full, (q_count - 1) & 1);
+      }
+    } else if (warp == 14) {
+      // ================================================================ items
+      // where the CTA's run lies on the line
+      int64_t total = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32)
+        total += __reduce_add_sync(0xffffffffu, (unsigned)units_of(a, seq_of(a, b0 + lane), G));
+      const int per = (int)((total + gridDim.x - 1) / gridDim.x);
+      const int u0 = (int)min(total, (int64_t)blockIdx.x * per), u1 = (int)min(total, (int64_t)u0 + per);
+      uint32_t m = 0, masked = 0;
+      auto publish = [&](const Item& i) {
+        const int slot = m % kItems;
+        if (m >= kItems) ok = cta_wait(&item_free[slot], ((m / kItems) - 1) & 1, gave_up);
+        if (!ok) return;
+        if (lane == 0) {
+          items[slot][0] = make_int4(i.b, i.kvh, i.g, i.c0);
+          items[slot][1] = make_int4(i.c1, i.q0, i.n, i.ctx);
+          items[slot][2].x = i.place;
+          mbar_arrive(&item_full[slot]);
+        }
+        __syncwarp();
+        ++m;
+      };
+      int u = 0;   // units before sequence b0 + ..
+      for (int b0 = 0; ok && b0 < a.B && u < u1; b0 += 32) {
+        const int mine = units_of(a, seq_of(a, b0 + lane), G);
+        int sum = mine;   // inclusive prefix
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += y;
+        }
+        unsigned in = __ballot_sync(0xffffffffu, mine > 0 && u + sum > u0 && u + sum - mine < u1);
+        while (ok && in) {
+          const int k = __ffs(in) - 1;
+          in &= in - 1;
+          const int start = u + __shfl_sync(0xffffffffu, sum - mine, k);
+          it.b = b0 + k;
+          const Seq s = seq_of(a, it.b);
+          it.q0 = s.q0, it.n = s.n, it.ctx = s.ctx;
+          const int chunks = chunks_of(s.ctx), groups = groups_of(s.n, G), each = chunks + kTreePairCost;
+          for (int p = max(0, u0 - start) / each; ok && p < a.Hkv * groups; ++p) {
+            const int at = start + p * each + kTreePairCost;   // the pair's first chunk on the line
+            if (at - kTreePairCost >= u1) break;
+            it.kvh = p / groups;
+            it.g = p - it.kvh * groups;
+            it.c0 = max(0, u0 - at);
+            it.c1 = min(chunks, u1 - at);
+            if (it.c1 <= it.c0) continue;
+            const int t_first = at / per, t_last = (at + chunks - 1) / per;
+            it.place = t_first == t_last ? 0 : (int)blockIdx.x == t_first ? 1 : 2;
+            if ((int)blockIdx.x == t_first && lane == 0)
+              a.ws_pair[((int64_t)it.b * a.Hkv + it.kvh) * a.groups + it.g] = make_int2(t_first, t_last);
+            publish(it);
+            if (!ok || it.c1 * kKeys <= it.ctx - it.n) continue;
+            // ---- the nodes' ancestors, each node its own
+            if (masked > 0) ok = cta_wait(&mask_free, (masked - 1) & 1, gave_up);
+            if (!ok) break;
+            ++masked;
+            const int words = (it.n + 31) >> 5;
+            bool wrong = false;
+            for (int i = lane; i < it.n; i += 32) {
+              int x = __ldg(a.parents + it.q0 + i);
+              if (x < -1 || x >= i) {
+                wrong = true;
+                x = -1;
+              }
+              up[i] = x;
+#pragma unroll
+              for (int w = 0; w < kMaskWords; ++w)
+                masks[i * kMaskStride + w] = w == i >> 5 ? 1u << (i & 31) : 0u;
+            }
+            if (wrong) raise_error(a.err, kErrTree);
+            __syncwarp();
+            // node i's mask holds it and its ancestors down to, not with, up[i]
+            bool more = true;
+            while (more) {
+              more = false;
+              for (int i0 = 0; i0 < it.n; i0 += 32) {
+                const int i = i0 + lane;
+                const int x = i < it.n ? up[i] : -1;
+                int y = -1;
+                uint32_t add[kMaskWords];
+                if (x >= 0) {
+                  y = up[x];
+#pragma unroll
+                  for (int w = 0; w < kMaskWords; ++w) add[w] = w < words ? masks[x * kMaskStride + w] : 0u;
+                }
+                __syncwarp();   // a node's mask and its up change together
+                if (x >= 0) {
+                  up[i] = y;
+#pragma unroll
+                  for (int w = 0; w < kMaskWords; ++w)
+                    if (w < words) masks[i * kMaskStride + w] |= add[w];
+                }
+                __syncwarp();
+                more |= __any_sync(0xffffffffu, y >= 0);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&mask_full);
+          }
+        }
+        u += __shfl_sync(0xffffffffu, sum, 31);
+      }
+      it.n = 0;
+      if (ok) publish(it);
+    } else if (warp >= 10 && warp < 14) {
+      // ================================================================ products
+      const int t = (warp - 10) & 1;
+      const uint32_t t_s = tmem + t * kKeys, t_o = tmem + kTmemO + t * D;
+      // a descriptor's start address is address >> 4 in its low 14 bits; every
+      // operand lies below 256 KB, so offsets are added to the base's descriptor
+      uint32_t chunk0 = 0, done = 0;   // the item's first chunk; chunks of this tile so far
+      const bool leader = elect_one();
+      if (warp < 12) {
+        // with a negative scale the product is negated (A's sign bit of the
+        // descriptor), so that the maximum is always the largest score
+        const uint32_t id_s = f16_idesc<T>(kRows, kHalf) | (a.qscale < 0.f ? 1u << 13 : 0u);
+        const uint64_t q_desc0 = sw128_desc(sQ), k_desc = sw128_desc(sK);
+        for (uint32_t m = 0; ok && take(m, it); ++m) {
+          const bool apart = rows_of(it) > kRows;
+          const int n_chunks = it.c1 - it.c0, main = m & 1;
+          const uint64_t q_desc = q_desc0 + (uint64_t)((apart ? t * C::kQBytes : 0) >> 4);
+          ok = cta_wait(&q_full, m & 1, gave_up);
+          if (!ok) break;
+          for (int lc = 0; lc < n_chunks; ++lc) {
+            const uint32_t kc = chunk0 + lc;
+            ok = cta_wait(&k_full[kc % SK], (kc / SK) & 1, gave_up);
+            if (ok && (apart || ((lc + main) & 1) == t)) {
+              const uint64_t kb = k_desc + (uint64_t)(((kc % SK) * C::kKvBytes) >> 4);
+              for (int h = 0; h < 2; ++h) {
+                // P of the last chunk's half, which lies over S, is used
+                if (done > 0) ok = cta_wait(&o_done[t][h], (done - 1) & 1, gave_up);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                  for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t at = (kk & 3) * 32;
+                    tc_mma(t_s + h * kHalf, q_desc + (uint64_t)(((kk >> 2) * (kRows * 128) + at) >> 4),
+                           kb + (uint64_t)(((kk >> 2) * (kKeys * 128) + h * (kHalf * 128) + at) >> 4),
+                           id_s, kk > 0);
+                  }
+                  tc_commit(&s_full[t][h]);
+                }
+                __syncwarp();
+              }
+              if (!ok) break;
+              ++done;
+              ok = cta_wait(&s_full[t][1], (done - 1) & 1, gave_up);
+            }
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&k_free[kc % SK]);
+          }
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(&q_free);   // the item's S are done
+          chunk0 = uniform(chunk0 + n_chunks);
+        }
+      } else {
+        const uint32_t id_o = f16_idesc<T>(kRows, D) | (1u << 16);   // B (V) MN-major
+        const uint64_t v_desc = v_operand(sV);
+        constexpr uint32_t kNothing = ~0u;
+        uint32_t held = kNothing;   // the chunk whose V stage is to be handed back
+        for (uint32_t m = 0; ok && take(m, it); ++m) {
+          const bool apart = rows_of(it) > kRows;
+          const int n_chunks = it.c1 - it.c0, main = m & 1;
+          bool begun = false;
+          for (int lc = 0; lc < n_chunks; ++lc) {
+            const uint32_t vc = chunk0 + lc;
+            if (held != kNothing) {
+              ok = cta_wait(&o_done[t][1], (done - 1) & 1, gave_up);
+              if (!ok) break;
+              if (lane == 0) mbar_arrive(&v_free[held % SV]);
+              held = kNothing;
+            }
+            ok = cta_wait(&v_full[vc % SV], (vc / SV) & 1, gave_up);
+            if (!ok) break;
+            if (!apart && ((lc + main) & 1) != t) {   // a chunk of the other tile
+              if (lane == 0) mbar_arrive(&v_free[vc % SV]);
+              continue;
+            }
+            const int valid = min(kKeys, it.ctx - (it.c0 + lc) * kKeys);
+            const int steps = (valid + 15) / 16;
+            // The products read whole groups of 16 keys.  Rows past the last key,
+            // and of blocks that are not there, meet zero weights, but 0 x NaN would
+            // not vanish: they are filled up with zeros.  (Where both tiles see the
+            // chunk both do it: the same zeros, before their own products.)
+            const uint32_t gone = v_gone[vc % kGoneRing];
+            if (gone || (valid & 15)) {
+              unsigned char* rows = smem + C::kOffV + (vc % SV) * C::kKvBytes;
+              for (int i = lane; i < steps * 16 * (D / 8); i += 32) {
+                const int r = i / (D / 8), ch = i % (D / 8);
+                if (r >= valid || (gone >> (r >> 4)) & 1u)
+                  *reinterpret_cast<uint4*>(rows + (ch >> 3) * (kKeys * 128) + r * 128 + ((ch & 7) << 4)) =
+                      make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_async_smem();
+              __syncwarp();
+            }
+            const uint64_t vb = v_desc + (uint64_t)(((vc % SV) * C::kKvBytes) >> 4);
+            // 64 keys at a time, as their weights become ready; a half without keys
+            // has nothing to add, only its barrier to complete
+            for (int h = 0; h < 2; ++h) {
+              ok = cta_wait(&p_full[t][h], done & 1, gave_up);
+              if (!ok) break;
+              tc_fence_after();
+              auto product = [&](int kk) {
+                tc_mma_ts(t_o, t_s + h * kHalf + kk * 8,
+                          vb + (uint64_t)((h * (kHalf * 128) + kk * 2048) >> 4), id_o,
+                          begun || h > 0 || kk > 0 ? 1u : 0u);
+              };
+              if (leader) {
+                if (steps >= 4 * h + 4) {
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk) product(kk);
+                } else {
+#pragma unroll 1
+                  for (int kk = 0; kk < steps - 4 * h; ++kk) product(kk);
+                }
+                tc_commit(&o_done[t][h]);
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            begun = true;
+            held = vc;
+            ++done;
+          }
+          chunk0 = uniform(chunk0 + n_chunks);
+        }
+      }
+      if (!ok) {
+        if (leader) tc_commit(&drained[warp - 10]);
+        __syncwarp();
+        (void)mbar_wait_bounded(&drained[warp - 10], 0);
+      }
+    }
+  }
+  if (!ok && lane == 0) raise_error(a.err, kErrTimeout);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+}
+
+// out = sum_p w_p o_p / sum_p w_p l_p with w_p = 2^(scale (m_p - max m)) over the
+// partials of a row, and the zero rows of rejected sequences.  A CTA takes rows
+// [slice kMergeRows, ..) of the trees of (sequence, KV head), a warp a row at a time.
+constexpr int kMergeThreads = 256, kMergeRows = 64;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a) {
+  constexpr int EPL = D / 32, kWarps = kMergeThreads / 32, kAhead = 4;
+  pdl_launch_dependents();
+  const int kvh = blockIdx.x, b = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = a.Hq / a.Hkv, g2 = __ffs(G) - 1;
+  // every CTA of the attention kernel has passed its own wait: these are there
+  const Seq s = seq_of(a, b);
+  const int row0 = blockIdx.z * kMergeRows;
+  T* out = static_cast<T*>(a.out);
+  if (s.n == 0) {
+    const int q0 = __ldg(a.query_start + b), n = __ldg(a.query_start + b + 1) - q0;
+    if (n == 0 && q0 >= 0 && q0 <= a.num_tokens) return;
+    const bool outside = q0 < 0 || n < 0 || q0 + n > a.num_tokens;
+    const bool query = outside || n > a.max_query_len;
+    if (threadIdx.x == 0 && kvh == 0 && row0 == 0) raise_error(a.err, query ? kErrQuery : kErrContext);
+    if (outside) return;
+    pdl_wait_primary();
+    const int rows = min(row0 + kMergeRows, min(n, a.max_query_len) << g2);
+    for (int i = row0 * (D / 8) + threadIdx.x; i < rows * (D / 8); i += kMergeThreads) {
+      const int r = i / (D / 8);
+      reinterpret_cast<uint4*>(out + ((int64_t)(q0 + (r >> g2)) * a.Hq + kvh * G + (r & (G - 1))) * D)[i % (D / 8)] =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
+    return;
+  }
+  const int rows = s.n << g2;
+  if (row0 >= rows) return;
+  pdl_wait_primary();
+  const float qmul = fmaxf(fabsf(a.qscale), 1e-37f);
+  const int g = row0 / kTreeRows;
+  const int2 pr = a.ws_pair[((int64_t)b * a.Hkv + kvh) * a.groups + g];
+  if (pr.x == pr.y) return;   // the attention kernel wrote out
+  for (int r = row0 + warp; r < min(rows, row0 + kMergeRows); r += kWarps) {
+    const int64_t head = (int64_t)(s.q0 + (r >> g2)) * a.Hq + kvh * G + (r & (G - 1));
+    // the first partial lies with the row, the others with their CTAs
+    const int64_t later = (int64_t)a.num_tokens * a.Hq + (int64_t)pr.x * kTreeRows + (r - g * kTreeRows);
+    const int parts = pr.y - pr.x + 1;
+    float M = kNoMax, L = 0.f, O[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) O[e] = 0.f;
+    for (int p0 = 0; p0 < parts; p0 += kAhead) {
+      float v[kAhead][EPL];
+      float2 ml[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int p = min(p0 + i, parts - 1);
+        const int64_t at = p == 0 ? head : later + (int64_t)p * kTreeRows;
+        ml[i] = a.ws_ml[at];
+        if (p0 + i >= parts) ml[i].y = 0.f;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) v[i][e] = a.ws_o[at * D + lane * EPL + e];
+      }
+      float top = M;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);
+      const float r0 = softmax_exp2((M - top) * qmul);
+      M = top;
+      L *= r0;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) O[e] *= r0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (ml[i].y == 0.f) continue;   // no key of that part, or not a part
+        const float w = softmax_exp2((ml[i].x - M) * qmul);
+        L = fmaf(w, ml[i].y, L);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) O[e] = fmaf(w, v[i][e], O[e]);
+      }
+    }
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+#pragma unroll
+    for (int e = 0; e < EPL; e += 2)
+      *reinterpret_cast<uint32_t*>(out + head * D + lane * EPL + e) =
+          Mma<T>::pack(O[e] * inv, O[e + 1] * inv);
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const TreeArgs& a, cudaStream_t stream) {
+  using C = Cfg<D>;
+  auto kern = tree_attention_kernel<T, D>;
+  static std::atomic<bool> configured[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    configured[dev].store(true, std::memory_order_relaxed);
+  }
+  CUtensorMap tq, tk, tv;
+  // q as [token][head][element], a box of 128 / G tokens x G heads x 64 elements
+  const cuuint32_t G = (cuuint32_t)(a.Hq / a.Hkv);
+  const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.num_tokens};
+  const cuuint64_t qs[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.Hq * D * 2};
+  const cuuint32_t qb[3] = {64, G, (cuuint32_t)kRows / G};
+  e = encode_tensor_map(&tq, a.dtype == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        3, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  if ((e = make_pool_map(&tk, a.k_cache, a.dtype, a.NB, a.Hkv, a.D)) != cudaSuccess) return e;
+  if ((e = make_pool_map(&tv, a.v_cache, a.dtype, a.NB, a.Hkv, a.D)) != cudaSuccess) return e;
+  const int64_t most = (int64_t)a.B * a.Hkv * a.groups * ((a.MBS * kBlockSize + kKeys - 1) / kKeys + kTreePairCost);
+  const int grid = (int)std::min<int64_t>(std::min(a.num_sms, kTreeMaxCtas), most);
+  e = launch_pdl(kern, dim3(grid), dim3(kThreads), C::kSmem, stream, tq, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  const int slices = (a.max_query_len * (int)G + kMergeRows - 1) / kMergeRows;
+  return launch_pdl(tree_merge_kernel<T, D>, dim3(a.Hkv, a.B, slices), dim3(kMergeThreads), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t stream) {
+  if (a.dtype == 1)
+    return a.D == 64 ? launch_t<__half, 64>(a, stream) : launch_t<__half, 128>(a, stream);
+  return a.D == 64 ? launch_t<__nv_bfloat16, 64>(a, stream) : launch_t<__nv_bfloat16, 128>(a, stream);
+}
+
+}  // namespace photon
