@@ -5,16 +5,18 @@
 // sampling); "Roadmap" (speculative decoding).
 //
 // At node c with the target's p and the draft's q, r = p and Z = 1; a child x is
-// accepted if r(x) > u Z q(x), else r <- max(0, r / Z - q), Z <- sum r.  With
-// r / Z = (A p - B q)+ this is A <- A / Z, B <- B / Z + 1: one pair of numbers
-// stands for the whole row, and a rejection costs one pass over two rows for Z,
-// none if no sibling follows (the sampling pass finds the sum by itself).  Without
-// q a child is a point mass: Z loses r(x), and the row needs no pass at all.
+// accepted if r(x) > u Z q(x), else r <- max(0, r / Z - q), Z <- sum r.  Up to a
+// factor, which neither the test nor the sampling needs, r is (p - L q)+ with L = 0,
+// and with F = 1, then F = sum (p - L q)+, in the place of Z a rejection is L <- L +
+// F: one number stands for the whole row, and a rejection costs one pass over two
+// rows for F, none if no sibling follows (the sampling pass finds the sum itself).
+// Without q a child is a point mass: Z loses r(x), and the row needs no pass at all.
 //
 // What it answers are whole numbers, so what they hang on is held to about 48 bits:
-// tests in double (one product and one comparison a child), row sums as pairs of
-// floats whose rounding errors are carried along (two-sum), joined in double; the
-// rate of doubles is too low for the rows themselves.
+// tests in double (a product and a comparison a child), L in two floats, row sums as
+// pairs of floats whose rounding errors are carried along (two-sum), two elements an
+// instruction, joined in double; the rate of doubles is too low for the rows, and for
+// more than one warp at a time.
 //
 // A cluster of CTAs takes a sequence.  All of them walk the tree, each for itself,
 // from the nodes' probabilities in shared memory; a pass over a row is cut into one
@@ -30,10 +32,42 @@
 namespace photon {
 namespace {
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyCtas = 4;      // per SM
 constexpr int kVerifyCluster = 8;   // most CTAs of a cluster
 constexpr int kVerifyRun = kVerifyVocab / kVerifyCluster;   // most tokens of a CTA's run
+
+// Two floats in one register pair, and the paired instructions.
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ float2 parts(Pair p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+  return f;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ Pair sub2(Pair a, Pair b) {   // a - b, rounded once
+  return fma2(b, pair(-1.f, -1.f), a);
+}
 
 // A sum held in two floats.
 struct Sum2 {
@@ -52,6 +86,24 @@ struct Sum2 {
     }
   }
 };
+// Two such sums side by side.
+struct Sums2 {
+  Pair hi = 0, lo = 0;
+  __device__ __forceinline__ void add(Pair x, Pair rest) {
+    const Pair s = add2(hi, x), b = sub2(s, hi);
+    const Pair off = add2(sub2(hi, sub2(s, b)), sub2(x, b));
+    lo = add2(lo, add2(off, rest));
+    hi = s;
+  }
+  __device__ __forceinline__ Sum2 both() const {
+    const float2 h = parts(hi), l = parts(lo);
+    Sum2 s;
+    s.hi = h.x;
+    s.lo = l.x;
+    s.add(h.y, l.y);
+    return s;
+  }
+};
 // Inclusive prefix sums over a warp.
 __device__ __forceinline__ double prefix(double x, int lane) {
 #pragma unroll
@@ -63,45 +115,35 @@ __device__ __forceinline__ double prefix(double x, int lane) {
 }
 
 // An entry as a probability: NaN and negative ones are 0, ones above 1 are 1.
-__device__ __forceinline__ float as_prob(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+__device__ __forceinline__ float as_prob(float x) { return __saturatef(x); }
 
-// r = (A p - B q)+ of a row: mode 0 is p, 1 is p - q, 2 has A and B in two floats
-// each; `out` marks the tokens of the CTA's run that count as 0 (mode 0 alone).
-struct Rest {
-  int mode;
-  float ah, al, bh, bl;
-  __device__ __forceinline__ void of(float p, float q, float& r, float& rest) const {
-    rest = 0.f;
-    if (mode == 0) {
-      r = p;
-    } else if (mode == 1) {
-      r = p - q;
-      rest = (p - r) - q;   // exact where p >= q
-      if (!(r > 0.f)) r = rest = 0.f;
-    } else {
-      const float x = ah * p, y = bh * q;
-      const float xl = fmaf(ah, p, -x) + al * p, yl = fmaf(bh, q, -y) + bl * q;
-      r = x - y;
-      const float b = r - x;
-      rest = ((x - (r - b)) + (-y - b)) + (xl - yl);
-      if (!(r + rest > 0.f)) r = rest = 0.f;
-    }
-  }
-};
+// r = (p - L q)+ of two elements as r + rest, L = hi + lo.
+__device__ __forceinline__ void left_of(float2 p, float2 q, float hi, float lo, Pair& r, Pair& rest) {
+  const Pair h = pair(hi, hi), qq = pair(q.x, q.y);
+  const Pair y = mul2(h, qq);
+  const float2 yf = parts(y);
+  // what rounding y has cost, and L's second part
+  const Pair yl = fma2(pair(lo, lo), qq, fma2(h, qq, sub2(0, y)));
+  const Pair m = pair(fmaxf(p.x, yf.x), fmaxf(p.y, yf.y));
+  r = sub2(m, y);   // 0 where p <= y; (m - r) - y is exact, as m >= y >= 0
+  const float2 e = parts(sub2(sub2(sub2(m, r), y), yl));
+  rest = pair(p.x > yf.x ? e.x : 0.f, p.y > yf.y ? e.y : 0.f);
+}
 
+// 16 bytes of a row from element e on; what lies behind its end is 0.
 template <typename T, bool kVec>
-__device__ __forceinline__ void load_probs(const T* row, int e, int vocab, float* f) {
+__device__ __forceinline__ uint4 load_chunk(const T* row, int e, int vocab) {
   constexpr int N = 16 / sizeof(T);
-  if (kVec && e + N <= vocab) {
-    const uint4 c = __ldg(reinterpret_cast<const uint4*>(row + e));
-    Elem<T>::widen(c, f);
+  if (kVec && e + N <= vocab) return __ldg(reinterpret_cast<const uint4*>(row + e));
+  union {
+    uint4 all;
+    T one[N];
+  } c;
+  c.all = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = as_prob(f[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      f[i] = e + i < vocab ? as_prob(Elem<T>::to_f32(row[e + i])) : 0.f;
-  }
+  for (int i = 0; i < N; ++i)
+    if (e + i < vocab) c.one[i] = row[e + i];
+  return c.all;
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -119,16 +161,16 @@ __device__ __forceinline__ void store_peer(double* p, int rank, double v) {
 
 // kVec: rows begin on 16-byte boundaries.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kVerifyThreads)
+__global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
     verify_tree_kernel(const VerifyArgs a, int ranks) {
-  constexpr int N = 16 / sizeof(T), kTile = 32 * N, kDepth = 2;   // elements of a lane, of a warp; loads ahead
+  constexpr int N = 16 / sizeof(T), kTile = 32 * N, kDepth = 8 / N;   // elements of a lane, of a warp; loads ahead
   __shared__ int parent[kTreeNodes], token[kTreeNodes], path[kTreeNodes];
   __shared__ float prob[kTreeNodes], draft[kTreeNodes], number[kTreeNodes];
   __shared__ float2 warp_sum[kVerifyWarps];
   __shared__ double cta_sum[2][kVerifyCluster], row_sum;
-  __shared__ double state_a, state_b, state_z, owner_before;
-  __shared__ int owner_warp;
-  __shared__ int state_node, state_last, state_len, state_sweep;
+  __shared__ double owner_before;
+  __shared__ float2 state_less;   // L
+  __shared__ int state_node, state_len, state_sweep, state_out, row_left, owner_warp;
   extern __shared__ uint32_t out[];   // a bit for each token of the CTA's run
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / ranks, rank = blockIdx.x % ranks;
@@ -173,62 +215,70 @@ __global__ void __launch_bounds__(kVerifyThreads)
     prob[i] = p;
     draft[i] = q;
   }
-  if (tid == 0) {
-    state_node = state_last = 0;
-    state_len = 1;
-    path[0] = 0;
-    state_a = state_z = 1.0;
-    state_b = 0.0;
-  }
+  if (tid == 0) path[0] = 0;
   __syncthreads();
+  if (!drafts) {
+    // a sibling before it has the same token: nothing is left for it
+    for (int i = tid; i < n; i += kVerifyThreads) {
+      bool same = false;
+      for (int j = 0; j < i; ++j) same |= parent[j] == parent[i] && token[j] == token[i];
+      if (same) prob[i] = 0.f;
+    }
+    __syncthreads();
+  }
 
-  Rest rest{};
+  float2 less = make_float2(0.f, 0.f);   // L
   const T* prow = target;
   const T* qrow = drafts;
   bool marked = false;   // some tokens of the run are out
 
-  // r of the N elements from e on, whose sum is wanted
-  auto left = [&](int e, const float* p, const float* q, float* r, float* l) {
-    uint32_t gone = 0;
+  // adds r of the N elements from e on, of chunks p and q
+  auto add_left = [&](int e, uint4 pc, uint4 qc, Sums2& sum) {
+    float p[N], q[N];
+    Elem<T>::widen(pc, p);
+    Elem<T>::widen(qc, q);
     if (marked && e < run1) {
       const uint32_t at = (uint32_t)(e - cta_begin);
-      gone = out[at >> 5] >> (at & 31);
+      const uint32_t gone = out[at >> 5] >> (at & 31);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((gone >> i) & 1u) p[i] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      rest.of((gone >> i) & 1u ? 0.f : p[i], q[i], r[i], l[i]);
+    for (int i = 0; i < N; i += 2) {
+      const float2 pp = make_float2(as_prob(p[i]), as_prob(p[i + 1]));
+      Pair r = pair(pp.x, pp.y), l = 0;
+      if (less.x != 0.f) left_of(pp, make_float2(as_prob(q[i]), as_prob(q[i + 1])), less.x, less.y, r, l);
+      sum.add(r, l);
     }
   };
-  auto load = [&](int e, float* p, float* q) {
+  auto load = [&](int e, uint4& p, uint4& q) {
+    p = q = make_uint4(0u, 0u, 0u, 0u);
     if (e < run1) {
-      load_probs<T, kVec>(prow, e, V, p);
-      if (rest.mode > 0) load_probs<T, kVec>(qrow, e, V, q);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) p[i] = q[i] = 0.f;
-    }
-    if (rest.mode == 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) q[i] = 0.f;
+      p = load_chunk<T, kVec>(prow, e, V);
+      if (less.x != 0.f) q = load_chunk<T, kVec>(qrow, e, V);
     }
   };
   int round = 0;
   // The sum of r over the row; the CTAs' sums are in cta_sum[parity], the warps' in
   // warp_sum.
-  auto sweep = [&]() -> double {
-    Sum2 sum;
-    for (int e0 = run0 + lane * N; e0 < run1; e0 += kDepth * kTile) {
-      float p[kDepth][N], q[kDepth][N];
+  auto sweep = [&]() {
+    Sums2 sums;
+    uint4 p[kDepth], q[kDepth], p2[kDepth], q2[kDepth];
+    int e0 = run0 + lane * N;
 #pragma unroll
-      for (int k = 0; k < kDepth; ++k) load(e0 + k * kTile, p[k], q[k]);
+    for (int k = 0; k < kDepth; ++k) load(e0 + k * kTile, p[k], q[k]);
+    while (e0 < run1) {
+      const int e1 = e0 + kDepth * kTile;
 #pragma unroll
-      for (int k = 0; k < kDepth; ++k) {
-        float r[N], l[N];
-        left(e0 + k * kTile, p[k], q[k], r, l);
+      for (int k = 0; k < kDepth; ++k) load(e1 + k * kTile, p2[k], q2[k]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum.add(r[i], l[i]);
-      }
+      for (int k = 0; k < kDepth; ++k) add_left(e0 + k * kTile, p[k], q[k], sums);
+#pragma unroll
+      for (int k = 0; k < kDepth; ++k) p[k] = p2[k], q[k] = q2[k];
+      e0 = e1;
     }
+    Sum2 sum = sums.both();
     sum.over(32);
     const int parity = round++ & 1;
     if (lane == 0) warp_sum[warp] = make_float2(sum.hi, sum.lo);
@@ -247,128 +297,120 @@ __global__ void __launch_bounds__(kVerifyThreads)
       double total = lane < ranks ? cta_sum[parity][lane] : 0.0;
 #pragma unroll
       for (int o = 1; o < kVerifyCluster; o <<= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-      if (lane == 0) row_sum = total;
+      if (lane == 0) {
+        row_sum = total;
+        row_left = total > 0.0;
+      }
     }
     __syncthreads();
-    return row_sum;
   };
-  auto take_rest = [&](double A, double B) {
-    rest.mode = B == 0.0 ? 0 : (A == 1.0 && B == 1.0 ? 1 : 2);
-    rest.ah = (float)A;
-    rest.al = (float)(A - (double)rest.ah);
-    rest.bh = (float)B;
-    rest.bl = (float)(B - (double)rest.bh);
-  };
-
-  // ---- the walk: warp 0, up to the next pass that it needs
+  // ---- the walk: warp 0, up to the next pass that it needs.  Doubles are for one
+  // warp at a time: at their rate the whole CTA's would take longer than a pass.
+  int node = 0, last = 0, len = 1;
+  double L = 0.0, F = 1.0;   // F < 0: not known yet
   while (true) {
     if (warp == 0) {
-      int node = state_node, last = state_last, len = state_len;
-      double A = state_a, B = state_b, Z = state_z;
-      int want = 0;
+      bool want = false, some = false;
       while (true) {
-        // the node's next child
-        int j = n;
-        for (int i0 = (last + 1) & ~31; i0 < n && j == n; i0 += 32) {
-          const int i = i0 + lane;
-          const unsigned hit = __ballot_sync(0xffffffffu, i > last && i < n && parent[i] == node);
-          if (hit) j = i0 + __ffs(hit) - 1;
-        }
-        if (j == n) break;
-        if (token[j] < 0) {   // no token
-          last = j;
-          continue;
-        }
-        if (Z < 0.0) {   // not known yet: the sum of what a rejection left
-          want = 1;
-          break;
-        }
-        last = j;
-        double r = (double)prob[j], q = 1.0;
+        int taken = -1;
+        some = false;   // a child of the node was rejected
         if (drafts) {
-          q = (double)draft[j];
-          r = fmax(A * r - B * q, 0.0);
-        } else if (B != 0.0) {   // a sibling before it had the same token
-          bool same = false;
-          for (int i = lane; i < j; i += 32) same |= parent[i] == node && token[i] == token[j];
-          if (__any_sync(0xffffffffu, same)) r = 0.0;
-        }
-        if (r > (double)number[j] * Z * q) {
-          if (lane == 0) path[len] = j;
-          ++len;
-          node = j;
-          A = Z = 1.0;
-          B = 0.0;
-        } else if (drafts) {
-          const double safe = Z > 0.0 ? Z : 1.0;
-          A = A / safe;
-          B = B / safe + 1.0;
-          Z = -1.0;
+          // one child after another
+          int j = n;
+          for (int i0 = (last + 1) & ~31; i0 < n && j == n; i0 += 32) {
+            const int i = i0 + lane;
+            const unsigned hit = __ballot_sync(
+                0xffffffffu, i > last && i < n && parent[i] == node && token[i] >= 0);
+            if (hit) j = i0 + __ffs(hit) - 1;
+          }
+          if (j == n) break;
+          if (F < 0.0) {
+            want = true;
+            break;
+          }
+          last = j;
+          const double q = (double)draft[j];
+          if (fmax((double)prob[j] - L * q, 0.0) > (double)number[j] * F * q) {
+            taken = j;
+          } else {
+            L += F > 0.0 ? F : 1.0;
+            F = -1.0;
+            continue;
+          }
         } else {
-          Z = fmax(Z - r, 0.0);
-          B = 1.0;   // tokens are out
+          // all children at once: before each, Z has lost what those before it had
+          double lost = 0.0;
+          for (int i0 = (node + 1) & ~31; i0 < n && taken < 0; i0 += 32) {
+            const int i = i0 + lane;
+            const bool child = i > node && i < n && parent[i] == node && token[i] >= 0;
+            if (!__any_sync(0xffffffffu, child)) continue;
+            const double r = child ? (double)prob[i] : 0.0;
+            const double up_to = lost + prefix(r, lane);
+            const unsigned yes = __ballot_sync(
+                0xffffffffu, child && r > (double)number[i] * fmax(1.0 - (up_to - r), 0.0));
+            if (yes) taken = i0 + __ffs(yes) - 1;
+            some = true;
+            lost = __shfl_sync(0xffffffffu, up_to, 31);
+          }
+          if (taken < 0) break;
         }
+        if (lane == 0) path[len] = taken;
+        ++len;
+        node = last = taken;
+        L = 0.0;
+        F = 1.0;
       }
       if (lane == 0) {
         state_node = node;
-        state_last = last;
         state_len = len;
-        state_a = A;
-        state_b = B;
-        state_z = Z;
         state_sweep = want;
+        state_out = some;
+        const float hi = (float)L;
+        state_less = make_float2(hi, (float)(L - (double)hi));
       }
     }
     __syncthreads();
-    if (!state_sweep) break;
     prow = target + (int64_t)state_node * a.target_stride;
     qrow = drafts + (int64_t)state_node * a.draft_stride;
-    take_rest(state_a, state_b);
-    const double z = sweep();
-    if (tid == 0) state_z = z;
-    __syncthreads();
+    less = state_less;
+    if (!state_sweep) break;
+    sweep();
+    if (warp == 0) F = row_sum;
   }
 
   // ---- the token that follows
-  const int node = state_node, len = state_len;
-  prow = target + (int64_t)node * a.target_stride;
-  if (drafts) {
-    qrow = drafts + (int64_t)node * a.draft_stride;
-    take_rest(state_a, state_b);
-  } else {
-    rest.mode = 0;
-    if (state_b != 0.0) {
-      // all of the node's children are out: mark them in the CTA's run
-      const int words = (kVerifyWarps * per_warp + 31) / 32;
-      for (int i = tid; i < words; i += kVerifyThreads) out[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < n; i += kVerifyThreads) {
-        const int64_t at = (int64_t)token[i] - cta_begin;
-        if (parent[i] == node && token[i] >= 0 && at >= 0 && at < (int64_t)kVerifyWarps * per_warp)
-          atomicOr(&out[at >> 5], 1u << (at & 31));
-      }
-      __syncthreads();
-      marked = true;
+  if (state_out) {
+    // all of the node's children are out: mark them in the CTA's run
+    const int words = (kVerifyWarps * per_warp + 31) / 32;
+    for (int i = tid; i < words; i += kVerifyThreads) out[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kVerifyThreads) {
+      const int64_t at = (int64_t)token[i] - cta_begin;
+      if (parent[i] == state_node && token[i] >= 0 && at >= 0 &&
+          at < (int64_t)kVerifyWarps * per_warp)
+        atomicOr(&out[at >> 5], 1u << (at & 31));
     }
+    __syncthreads();
+    marked = true;
   }
-  double total = sweep();
-  if (!(total > 0.0) && (marked || rest.mode != 0)) {   // nothing is left: the target's own row
+  sweep();
+  if (!row_left && (marked || less.x != 0.f)) {   // nothing is left: the target's own row
     marked = false;
-    rest.mode = 0;
-    total = sweep();
+    less = make_float2(0.f, 0.f);
+    sweep();
   }
   const int parity = (round - 1) & 1;
-  const float chance = __ldg(a.sample + b);
-  const double t = (double)chance * total;
   if (rank == 0) {
-    for (int i = tid; i < n; i += kVerifyThreads) a.path[q0 + i] = i < len ? path[i] : -1;
-    if (tid == 0) a.path_len[b] = len;
-    if (tid == 0 && !(total > 0.0)) a.next[b] = -1;
+    for (int i = tid; i < n; i += kVerifyThreads) a.path[q0 + i] = i < state_len ? path[i] : -1;
+    if (tid == 0) a.path_len[b] = state_len;
+    if (tid == 0 && !row_left) a.next[b] = -1;
   }
-  if (!(total > 0.0)) return;
+  if (!row_left) return;
   // The CTA in whose run t is passed, and there the warp; rounding aside there is
   // one, else the last that holds anything.
+  double t = 0.0;
   if (warp == 0) {
+    t = (double)__ldg(a.sample + b) * row_sum;
     auto passed = [&](double mine, double before, double& at) -> int {
       const double up_to = before + prefix(mine, lane);
       unsigned hit = __ballot_sync(0xffffffffu, up_to > t && mine > 0.0);
@@ -396,43 +438,45 @@ __global__ void __launch_bounds__(kVerifyThreads)
   }
   __syncthreads();
   if (warp != owner_warp) return;
-  double sum = owner_before;
-  int answer = -1, positive = -1;   // where t is passed; the last one that holds anything
-  for (int e0 = run0; e0 < run1 && answer < 0; e0 += kTile) {
-    const int e = e0 + lane * N;
-    float p[N], q[N], r[N], l[N];
+  t = (double)__ldg(a.sample + b) * row_sum;
+  // Each lane sums its share of the run, in order; then the warp goes through the
+  // share in which t is passed.
+  auto chosen = [&](double up_to, bool any) -> int {   // the lane, or -1 if none holds anything
+    const unsigned held = __ballot_sync(0xffffffffu, any);
+    const unsigned hit = __ballot_sync(0xffffffffu, any && up_to > t);
+    return hit ? __ffs(hit) - 1 : held ? 31 - __clz(held) : -1;
+  };
+  const int share = per_warp / 32;   // a multiple of N
+  const int begin = run0 + lane * share, end = min(begin + share, run1);
+  Sums2 own;
+  for (int e = begin; e < end; e += N) {
+    uint4 p, q;
     load(e, p, q);
-    left(e, p, q, r, l);
-    Sum2 own;
-#pragma unroll
-    for (int i = 0; i < N; ++i) own.add(r[i], l[i]);
-    const double held = own.value(), scan = prefix(held, lane);
-    int highest = -1;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (r[i] + l[i] > 0.f) highest = e + i;
-    const unsigned hit = __ballot_sync(0xffffffffu, sum + scan > t && highest >= 0);
-    if (hit) {
-      const int from = __ffs(hit) - 1;
-      int found = highest;
-      if (lane == from) {
-        double c = sum + (scan - held);
-        bool yet = false;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          c += (double)r[i] + (double)l[i];
-          if (!yet && r[i] + l[i] > 0.f && c > t) {
-            found = e + i;
-            yet = true;
-          }
-        }
-      }
-      answer = __shfl_sync(0xffffffffu, found, from);
-    }
-    positive = max(positive, __reduce_max_sync(0xffffffffu, highest));
-    sum += __shfl_sync(0xffffffffu, scan, 31);
+    add_left(e, p, q, own);
   }
-  if (lane == 0) a.next[b] = answer >= 0 ? answer : positive;
+  const double held = own.both().value();
+  double up_to = owner_before + prefix(held, lane);
+  const int lucky = max(0, chosen(up_to, held > 0.0));
+  double sum = __shfl_sync(0xffffffffu, up_to - held, lucky);
+  const int from = run0 + lucky * share, to = min(from + share, run1);
+  int answer = -1;
+  for (int e0 = from; e0 < to; e0 += 32) {
+    const int e = e0 + lane;
+    double x = 0.0;
+    if (e < to) {
+      float p = as_prob(Elem<T>::to_f32(prow[e])), q = 0.f;
+      if (less.x != 0.f) q = as_prob(Elem<T>::to_f32(qrow[e]));
+      const uint32_t at = (uint32_t)(e - cta_begin);
+      if (marked && (out[at >> 5] >> (at & 31)) & 1u) p = 0.f;
+      x = fmax((double)p - ((double)less.x + (double)less.y) * (double)q, 0.0);
+    }
+    up_to = sum + prefix(x, lane);
+    const int k = chosen(up_to, x > 0.0);
+    if (k >= 0) answer = e0 + k;   // or the last one that holds anything, so far
+    if (__any_sync(0xffffffffu, x > 0.0 && up_to > t)) break;
+    sum = __shfl_sync(0xffffffffu, up_to, 31);
+  }
+  if (lane == 0) a.next[b] = answer;
 }
 
 template <typename T, bool kVec>
