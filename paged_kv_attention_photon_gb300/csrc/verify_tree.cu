@@ -13,10 +13,10 @@
 // Without q a child is a point mass: Z loses r(x), and the row needs no pass at all.
 //
 // What it answers are whole numbers, so what they hang on is held to about 48 bits:
-// tests in double (a product and a comparison a child), L in two floats, row sums as
-// pairs of floats whose rounding errors are carried along (two-sum), two elements an
-// instruction, joined in double; the rate of doubles is too low for the rows, and for
-// more than one warp at a time.
+// L, F and the row sums are pairs of floats whose rounding errors are carried along
+// (two-sum), two elements an instruction; a test is made in single precision, and
+// where that leaves it open in double.  Doubles throughout are too slow here, the rows
+// by their rate, the walk by their latency.
 //
 // A cluster of CTAs takes a sequence.  All of them walk the tree, each for itself,
 // from the nodes' probabilities in shared memory; a pass over a row is cut into one
@@ -78,6 +78,8 @@ struct Sum2 {
     hi = s;
   }
   __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+  __device__ __forceinline__ bool positive() const { return hi + lo > 0.f; }
+  __device__ __forceinline__ bool above(const Sum2& t) const { return (hi - t.hi) + (lo - t.lo) > 0.f; }
   // the sum over `lanes` neighbouring lanes, in all of them
   __device__ __forceinline__ void over(int lanes) {
     for (int o = 1; o < lanes; o <<= 1) {
@@ -104,14 +106,28 @@ struct Sums2 {
     return s;
   }
 };
-// Inclusive prefix sums over a warp.
-__device__ __forceinline__ double prefix(double x, int lane) {
+// before, and x of the lanes up to each one's: prefix sums over a warp.
+__device__ __forceinline__ Sum2 prefix(const Sum2& before, Sum2 x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const float h = __shfl_up_sync(0xffffffffu, x.hi, o), l = __shfl_up_sync(0xffffffffu, x.lo, o);
+    if (lane >= o) x.add(h, l);
   }
+  x.add(before.hi, before.lo);
   return x;
+}
+__device__ __forceinline__ Sum2 of_lane(const Sum2& x, int lane) {
+  Sum2 s;
+  s.hi = __shfl_sync(0xffffffffu, x.hi, lane);
+  s.lo = __shfl_sync(0xffffffffu, x.lo, lane);
+  return s;
+}
+// x > y for x = max(0, p - L q), y = u F q: in single precision where that is clear
+// (each side is off by a few 2^-24 of what goes into it), else in double.
+__device__ __forceinline__ bool passes(float p, float q, const Sum2& L, float u, const Sum2& F) {
+  const float lq = L.hi * q, x = fmaxf(p - lq, 0.f), y = u * F.hi * q;
+  if (fabsf(x - y) > 1e-5f * (p + lq + y)) return x > y;
+  return fmax((double)p - L.value() * (double)q, 0.0) > (double)u * F.value() * (double)q;
 }
 
 // An entry as a probability: NaN and negative ones are 0, ones above 1 are 1.
@@ -150,12 +166,12 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-// Stores a double into the same place of another CTA's shared memory.
-__device__ __forceinline__ void store_peer(double* p, int rank, double v) {
+// Stores into the same place of another CTA's shared memory.
+__device__ __forceinline__ void store_peer(float2* p, int rank, float2 v) {
   asm volatile(
-      "{\n.reg .b32 at;\nmapa.shared::cluster.u32 at, %0, %1;\nst.shared::cluster.f64 [at], %2;\n}" ::
-          "r"(smem_addr(p)),
-      "r"(rank), "d"(v)
+      "{\n.reg .b32 at;\nmapa.shared::cluster.u32 at, %0, %1;\n"
+      "st.shared::cluster.v2.f32 [at], {%2, %3};\n}" ::"r"(smem_addr(p)),
+      "r"(rank), "f"(v.x), "f"(v.y)
       : "memory");
 }
 
@@ -163,12 +179,11 @@ __device__ __forceinline__ void store_peer(double* p, int rank, double v) {
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
     verify_tree_kernel(const VerifyArgs a, int ranks) {
-  constexpr int N = 16 / sizeof(T), kTile = 32 * N, kDepth = 8 / N;   // elements of a lane, of a warp; loads ahead
+  constexpr int N = 16 / sizeof(T), kTile = 32 * N, kDepth = 16 / N;   // elements of a lane, of a warp; loads ahead
   __shared__ int parent[kTreeNodes], token[kTreeNodes], path[kTreeNodes];
   __shared__ float prob[kTreeNodes], draft[kTreeNodes], number[kTreeNodes];
-  __shared__ float2 warp_sum[kVerifyWarps];
-  __shared__ double cta_sum[2][kVerifyCluster], row_sum;
-  __shared__ double owner_before;
+  __shared__ float2 sums_of[2][kVerifyCluster * kVerifyWarps];
+  __shared__ float2 threshold, owner_before;
   __shared__ float2 state_less;   // L
   __shared__ int state_node, state_len, state_sweep, state_out, row_left, owner_warp;
   extern __shared__ uint32_t out[];   // a bit for each token of the CTA's run
@@ -260,54 +275,39 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
     }
   };
   int round = 0;
-  // The sum of r over the row; the CTAs' sums are in cta_sum[parity], the warps' in
-  // warp_sum.
+  Sum2 row;   // warp 0's
+  // The sum of r over the row, into warp 0's `row`; the warps' sums are in sums_of[parity].
   auto sweep = [&]() {
     Sums2 sums;
-    uint4 p[kDepth], q[kDepth], p2[kDepth], q2[kDepth];
-    int e0 = run0 + lane * N;
+    for (int e0 = run0 + lane * N; e0 < run1; e0 += kDepth * kTile) {
+      uint4 p[kDepth], q[kDepth];
 #pragma unroll
-    for (int k = 0; k < kDepth; ++k) load(e0 + k * kTile, p[k], q[k]);
-    while (e0 < run1) {
-      const int e1 = e0 + kDepth * kTile;
-#pragma unroll
-      for (int k = 0; k < kDepth; ++k) load(e1 + k * kTile, p2[k], q2[k]);
+      for (int k = 0; k < kDepth; ++k) load(e0 + k * kTile, p[k], q[k]);
 #pragma unroll
       for (int k = 0; k < kDepth; ++k) add_left(e0 + k * kTile, p[k], q[k], sums);
-#pragma unroll
-      for (int k = 0; k < kDepth; ++k) p[k] = p2[k], q[k] = q2[k];
-      e0 = e1;
     }
     Sum2 sum = sums.both();
     sum.over(32);
     const int parity = round++ & 1;
-    if (lane == 0) warp_sum[warp] = make_float2(sum.hi, sum.lo);
-    __syncthreads();
-    if (warp == 0) {
-      Sum2 all;
-      if (lane < kVerifyWarps) {
-        all.hi = warp_sum[lane].x;
-        all.lo = warp_sum[lane].y;
-      }
-      all.over(kVerifyWarps);
-      if (lane < ranks) store_peer(&cta_sum[parity][rank], lane, all.value());
-    }
+    // every warp's sum to every CTA of the cluster
+    if (lane < ranks) store_peer(&sums_of[parity][rank * kVerifyWarps + warp], lane, make_float2(sum.hi, sum.lo));
     cluster_sync();
     if (warp == 0) {
-      double total = lane < ranks ? cta_sum[parity][lane] : 0.0;
-#pragma unroll
-      for (int o = 1; o < kVerifyCluster; o <<= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-      if (lane == 0) {
-        row_sum = total;
-        row_left = total > 0.0;
+      Sum2 all;
+      for (int k = lane; k < ranks * kVerifyWarps; k += 32) {
+        const float2 s = sums_of[parity][k];
+        all.add(s.x, s.y);
       }
+      all.over(32);
+      row = all;
+      if (lane == 0) row_left = all.positive();
     }
-    __syncthreads();
   };
   // ---- the walk: warp 0, up to the next pass that it needs.  Doubles are for one
   // warp at a time: at their rate the whole CTA's would take longer than a pass.
   int node = 0, last = 0, len = 1;
-  double L = 0.0, F = 1.0;   // F < 0: not known yet
+  Sum2 L, F;
+  F.hi = 1.f;   // < 0: not known yet
   while (true) {
     if (warp == 0) {
       bool want = false, some = false;
@@ -324,49 +324,57 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
             if (hit) j = i0 + __ffs(hit) - 1;
           }
           if (j == n) break;
-          if (F < 0.0) {
+          if (F.hi < 0.f) {
             want = true;
             break;
           }
           last = j;
-          const double q = (double)draft[j];
-          if (fmax((double)prob[j] - L * q, 0.0) > (double)number[j] * F * q) {
+          if (passes(prob[j], draft[j], L, number[j], F)) {
             taken = j;
           } else {
-            L += F > 0.0 ? F : 1.0;
-            F = -1.0;
+            if (F.positive())
+              L.add(F.hi, F.lo);
+            else
+              L.add(1.f, 0.f);
+            F.hi = -1.f;
+            F.lo = 0.f;
             continue;
           }
         } else {
           // all children at once: before each, Z has lost what those before it had
-          double lost = 0.0;
+          Sum2 lost, one;
+          one.hi = 1.f;
           for (int i0 = (node + 1) & ~31; i0 < n && taken < 0; i0 += 32) {
             const int i = i0 + lane;
             const bool child = i > node && i < n && parent[i] == node && token[i] >= 0;
             if (!__any_sync(0xffffffffu, child)) continue;
-            const double r = child ? (double)prob[i] : 0.0;
-            const double up_to = lost + prefix(r, lane);
-            const unsigned yes = __ballot_sync(
-                0xffffffffu, child && r > (double)number[i] * fmax(1.0 - (up_to - r), 0.0));
+            Sum2 mine;
+            if (child) mine.hi = prob[i];
+            const Sum2 up_to = prefix(lost, mine, lane);
+            Sum2 z = one;   // 1 - what those before it had
+            z.add(-up_to.hi, -up_to.lo);
+            z.add(mine.hi, 0.f);
+            if (!z.positive()) z = Sum2{};
+            const unsigned yes =
+                __ballot_sync(0xffffffffu, child && passes(mine.hi, 1.f, Sum2{}, number[i], z));
             if (yes) taken = i0 + __ffs(yes) - 1;
             some = true;
-            lost = __shfl_sync(0xffffffffu, up_to, 31);
+            lost = of_lane(up_to, 31);
           }
           if (taken < 0) break;
         }
         if (lane == 0) path[len] = taken;
         ++len;
         node = last = taken;
-        L = 0.0;
-        F = 1.0;
+        L = F = Sum2{};
+        F.hi = 1.f;
       }
       if (lane == 0) {
         state_node = node;
         state_len = len;
         state_sweep = want;
         state_out = some;
-        const float hi = (float)L;
-        state_less = make_float2(hi, (float)(L - (double)hi));
+        state_less = make_float2(L.hi, L.lo);
       }
     }
     __syncthreads();
@@ -375,7 +383,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
     less = state_less;
     if (!state_sweep) break;
     sweep();
-    if (warp == 0) F = row_sum;
+    if (warp == 0) F = row;
   }
 
   // ---- the token that follows
@@ -394,10 +402,13 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
     marked = true;
   }
   sweep();
+  __syncthreads();
   if (!row_left && (marked || less.x != 0.f)) {   // nothing is left: the target's own row
     marked = false;
     less = make_float2(0.f, 0.f);
+    __syncthreads();   // all have read row_left
     sweep();
+    __syncthreads();
   }
   const int parity = (round - 1) & 1;
   if (rank == 0) {
@@ -406,75 +417,84 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
     if (tid == 0 && !row_left) a.next[b] = -1;
   }
   if (!row_left) return;
-  // The CTA in whose run t is passed, and there the warp; rounding aside there is
-  // one, else the last that holds anything.
-  double t = 0.0;
+  // The warp in whose run t is passed; rounding aside there is one, else the last
+  // that holds anything.
+  Sum2 t;
+  auto chosen = [&](const Sum2& up_to, bool any) -> int {   // the lane, or -1 if none holds anything
+    const unsigned held = __ballot_sync(0xffffffffu, any);
+    const unsigned hit = __ballot_sync(0xffffffffu, any && up_to.above(t));
+    return hit ? __ffs(hit) - 1 : held ? 31 - __clz(held) : -1;
+  };
   if (warp == 0) {
-    t = (double)__ldg(a.sample + b) * row_sum;
-    auto passed = [&](double mine, double before, double& at) -> int {
-      const double up_to = before + prefix(mine, lane);
-      unsigned hit = __ballot_sync(0xffffffffu, up_to > t && mine > 0.0);
-      if (!hit) hit = 0x80000000u >> __clz(__ballot_sync(0xffffffffu, mine > 0.0));
-      const int k = __ffs(hit) - 1;
-      at = __shfl_sync(0xffffffffu, up_to - mine, k);
-      return k;
-    };
-    double at = 0.0;
-    int who = passed(lane < ranks ? cta_sum[parity][lane] : 0.0, 0.0, at);
-    if (who == rank) {
+    const float chance = __ldg(a.sample + b);
+    t.hi = chance * row.hi;
+    t.lo = fmaf(chance, row.hi, -t.hi) + chance * row.lo;
+    Sum2 sum, at;
+    int who = -1;
+    for (int k0 = 0; k0 < ranks * kVerifyWarps; k0 += 32) {
       Sum2 mine;
-      if (lane < kVerifyWarps) {
-        mine.hi = warp_sum[lane].x;
-        mine.lo = warp_sum[lane].y;
+      if (k0 + lane < ranks * kVerifyWarps) {
+        mine.hi = sums_of[parity][k0 + lane].x;
+        mine.lo = sums_of[parity][k0 + lane].y;
       }
-      who = passed(mine.value(), at, at);
-    } else {
-      who = -1;
+      const Sum2 up_to = prefix(sum, mine, lane);
+      const int k = chosen(up_to, mine.positive());
+      if (k >= 0) {
+        who = k0 + k;
+        at = k > 0 ? of_lane(up_to, k - 1) : sum;
+      }
+      if (__any_sync(0xffffffffu, mine.positive() && up_to.above(t))) break;
+      sum = of_lane(up_to, 31);
     }
     if (lane == 0) {
-      owner_warp = who;
-      owner_before = at;
+      owner_warp = who - rank * kVerifyWarps;   // another CTA's: none of this one's
+      owner_before = make_float2(at.hi, at.lo);
+      threshold = make_float2(t.hi, t.lo);
     }
   }
   __syncthreads();
   if (warp != owner_warp) return;
-  t = (double)__ldg(a.sample + b) * row_sum;
+  t.hi = threshold.x;
+  t.lo = threshold.y;
+  Sum2 sum;
+  sum.hi = owner_before.x;
+  sum.lo = owner_before.y;
   // Each lane sums its share of the run, in order; then the warp goes through the
   // share in which t is passed.
-  auto chosen = [&](double up_to, bool any) -> int {   // the lane, or -1 if none holds anything
-    const unsigned held = __ballot_sync(0xffffffffu, any);
-    const unsigned hit = __ballot_sync(0xffffffffu, any && up_to > t);
-    return hit ? __ffs(hit) - 1 : held ? 31 - __clz(held) : -1;
-  };
   const int share = per_warp / 32;   // a multiple of N
   const int begin = run0 + lane * share, end = min(begin + share, run1);
-  Sums2 own;
-  for (int e = begin; e < end; e += N) {
-    uint4 p, q;
-    load(e, p, q);
-    add_left(e, p, q, own);
+  Sums2 sums;
+  for (int e = begin; e < end; e += kDepth * N) {
+    uint4 p[kDepth], q[kDepth];
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) load(e + k * N < end ? e + k * N : run1, p[k], q[k]);
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) add_left(e + k * N < end ? e + k * N : run1, p[k], q[k], sums);
   }
-  const double held = own.both().value();
-  double up_to = owner_before + prefix(held, lane);
-  const int lucky = max(0, chosen(up_to, held > 0.0));
-  double sum = __shfl_sync(0xffffffffu, up_to - held, lucky);
+  const Sum2 own = sums.both();
+  Sum2 up_to = prefix(sum, own, lane);
+  const int lucky = max(0, chosen(up_to, own.positive()));
+  if (lucky > 0) sum = of_lane(up_to, lucky - 1);
   const int from = run0 + lucky * share, to = min(from + share, run1);
   int answer = -1;
   for (int e0 = from; e0 < to; e0 += 32) {
     const int e = e0 + lane;
-    double x = 0.0;
+    Sum2 x;
     if (e < to) {
       float p = as_prob(Elem<T>::to_f32(prow[e])), q = 0.f;
       if (less.x != 0.f) q = as_prob(Elem<T>::to_f32(qrow[e]));
       const uint32_t at = (uint32_t)(e - cta_begin);
       if (marked && (out[at >> 5] >> (at & 31)) & 1u) p = 0.f;
-      x = fmax((double)p - ((double)less.x + (double)less.y) * (double)q, 0.0);
+      Pair r, l;
+      left_of(make_float2(p, 0.f), make_float2(q, 0.f), less.x, less.y, r, l);
+      x.hi = parts(r).x;
+      x.lo = parts(l).x;
     }
-    up_to = sum + prefix(x, lane);
-    const int k = chosen(up_to, x > 0.0);
+    up_to = prefix(sum, x, lane);
+    const int k = chosen(up_to, x.positive());
     if (k >= 0) answer = e0 + k;   // or the last one that holds anything, so far
-    if (__any_sync(0xffffffffu, x > 0.0 && up_to > t)) break;
-    sum = __shfl_sync(0xffffffffu, up_to, 31);
+    if (__any_sync(0xffffffffu, x.positive() && up_to.above(t))) break;
+    sum = of_lane(up_to, 31);
   }
   if (lane == 0) a.next[b] = answer;
 }
