@@ -972,11 +972,10 @@ photon_status_t photon_rope_cache_append(const void* q, int64_t q_stride, const 
 
 namespace {
 
-// Workspace of photon_paged_tree_attention: [pairs][(m, l)][o], the last two for
+// Workspace of photon_paged_tree_attention: [CTAs][(m, l)][o], the last two for
 // every query row and for kTreeRows rows of every CTA.
 struct TreeLayout {
   size_t off_ml, off_o, total;
-  int groups;
 };
 
 // Sizes that the kernels count in 32 bits.
@@ -998,13 +997,11 @@ photon_status_t check_tree(const photon_paged_shape_t* s, int32_t num_tokens,
   return PHOTON_OK;
 }
 
-TreeLayout tree_layout(const photon_paged_shape_t* s, int32_t num_tokens, int32_t max_query_len) {
+TreeLayout tree_layout(const photon_paged_shape_t* s, int32_t num_tokens) {
   TreeLayout w{};
-  const int G = s->num_q_heads / s->num_kv_heads;
-  w.groups = (max_query_len * G + photon::kTreeRows - 1) / photon::kTreeRows;
   const size_t rows = (size_t)num_tokens * s->num_q_heads +
                       (size_t)photon::kTreeMaxCtas * photon::kTreeRows;
-  w.off_ml = round_up((size_t)s->num_seqs * s->num_kv_heads * w.groups * sizeof(int2), 256);
+  w.off_ml = round_up((size_t)photon::kTreeMaxCtas * sizeof(int4), 256);
   w.off_o = w.off_ml + round_up(rows * sizeof(float2), 256);
   w.total = w.off_o + round_up(rows * s->head_dim * sizeof(float), 256);
   return w;
@@ -1019,7 +1016,7 @@ size_t photon_paged_tree_attention_workspace_size(const photon_paged_shape_t* sh
   if (check_tree(shape, num_tokens, max_query_len) != PHOTON_OK || shape->num_seqs == 0 ||
       num_tokens == 0 || max_query_len == 0)
     return 0;
-  return tree_layout(shape, num_tokens, max_query_len).total;
+  return tree_layout(shape, num_tokens).total;
 }
 
 photon_status_t photon_paged_tree_attention(const void* q, const void* k_cache,
@@ -1043,17 +1040,16 @@ photon_status_t photon_paged_tree_attention(const void* q, const void* k_cache,
       (reinterpret_cast<uintptr_t>(query_start) & 3u) ||
       (reinterpret_cast<uintptr_t>(parents) & 3u))
     return PHOTON_ERR_MISALIGNED;
-  const TreeLayout w = tree_layout(shape, num_tokens, max_query_len);
+  const TreeLayout w = tree_layout(shape, num_tokens);
   if (!workspace || workspace_bytes < w.total) return PHOTON_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PHOTON_ERR_MISALIGNED;
   photon::TreeArgs a{};
   if ((st = error_word(&a.err)) != PHOTON_OK) return st;
   if ((st = num_sms(&a.num_sms)) != PHOTON_OK) return st;
   char* ws = static_cast<char*>(workspace);
-  a.ws_pair = reinterpret_cast<int2*>(ws);
+  a.ws_split = reinterpret_cast<int4*>(ws);
   a.ws_ml = reinterpret_cast<float2*>(ws + w.off_ml);
   a.ws_o = reinterpret_cast<float*>(ws + w.off_o);
-  a.groups = w.groups;
   a.q = q;
   a.k_cache = k_cache;
   a.v_cache = v_cache;

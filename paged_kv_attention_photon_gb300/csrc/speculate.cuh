@@ -38,13 +38,13 @@ struct TreeArgs {
   const int32_t* query_start;   // [B + 1]
   const int32_t* parents;       // [num_tokens]
   void* out;
-  int2* ws_pair;   // [B][Hkv][groups] first and last CTA of the pair's keys
+  int4* ws_split;  // [CTA] the pair that its run begins in the midst of: sequence, KV head
+                   // and row group, first and last CTA (-1: none)
   float2* ws_ml;   // [row] maximum (unscaled) and sum of weights of a partial ..
   float* ws_o;     // [row][D] .. and its weighted V sum
   uint32_t* err;
   float qscale;    // scale * log2(e)
   int B, Hq, Hkv, D, NB, MBS, num_tokens, max_query_len, dtype, num_sms;
-  int groups;      // row groups of the longest tree
 };
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t stream);
 // Query rows of a group: what one CTA holds at a time.
@@ -52,7 +52,7 @@ constexpr int kTreeRows = 256;
 // Most CTAs of the attention grid: each has kTreeRows rows of partials in the
 // workspace, whose size so does not depend on the device.
 constexpr int kTreeMaxCtas = 160;
-// Most of (sequence, KV head, row group) x (chunks of keys + what one counts).
+// Keys of a chunk, and the chunks that beginning and ending a pair counts for.
 constexpr int kTreeChunk = 128;
 constexpr int kTreePairCost = 2;
 

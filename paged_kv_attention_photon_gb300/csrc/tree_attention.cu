@@ -18,14 +18,16 @@
 // of 256 rows).  Two tiles of 128 rows each have scores S and sums O in tensor
 // memory.  With more than 128 rows each tile has its own rows and sees every chunk;
 // with up to 128 both tiles have the same rows and take every other chunk, so that
-// one tile's softmax runs beside the other's products; their sums meet at the end
-// through shared memory.  S, softmax and P V go by halves of 64 keys; P of a half
-// lies over its S as 16-bit pairs.  15 warps in fixed roles:
+// one tile's softmax runs beside the other's products, and their sums meet at the end
+// through shared memory, or, up to kWhole chunks, one tile takes the item and the other
+// the next one.  S, softmax and P V go by halves of 64 keys; P of a half lies over its S
+// as 16-bit pairs.  16 warps in fixed roles:
 //   warps 0-3, 4-7  softmax of tile 0, 1: thread r owns TMEM lane r
 //   warp 8, 9       tensor-map copies of Q and K, of V: 16-row boxes through the table
 //   warp 10, 11     issue S of tile 0, 1
 //   warp 12, 13     issue P V of tile 0, 1
-//   warp 14         finds the items, and the ancestors of each node
+//   warp 14         finds the items
+//   warp 15         finds the ancestors of each node; rejected sequences
 //
 // Which keys a node sees of its tree is a bit mask of its ancestors, found by
 // doubling (node i takes its ancestor's mask and the ancestor's ancestor, until all
@@ -36,7 +38,8 @@
 // counting kTreePairCost more than it has for what beginning and ending it costs;
 // the line is cut into equal runs, one per CTA: no queue and no atomics, so results
 // do not depend on timing.  A triple within one run is written out at once, the
-// others leave partial sums, joined by a second kernel.
+// others (one at most at each end of a run) leave partial sums, joined by a second
+// kernel.
 //
 // Numerics: products of the stored values, sums and statistics in fp32; weights P
 // enter the second product rounded to the storage type, as in
@@ -47,11 +50,11 @@
 //
 // Barriers complete once per use; use i has parity i & 1:
 //   k_full, v_full[st]   a chunk landed      k_free, v_free[st]  both tiles are done with it
-//   q_full               the item's Q        q_free              both tiles' last S is done
+//   q_full[i]            a Q tile landed     q_free[i]           the item's last S is done
 //   s_full[t][h]         S of 64 keys        p_full[t][h]        their P written
 //   o_done[t][h]         O += P V of 64 keys done; the next chunk's S may overwrite P
 //   item_full, item_free[i]  an item is known; every role has read it
-//   mask_full, mask_free     the ancestors of an item's tree; every softmax warp has used them
+//   mask_full, mask_free     the ancestors of a tree's nodes; no softmax warp uses them any more
 //   meet_full, meet_free[w]  32 columns of one tile's O are in shared memory; the other has taken them
 // Where a wait runs out the CTA gives up, and what it has in flight still lands
 // first: the copying warps wait (bounded) for their last copies, the issuing ones on
@@ -71,7 +74,7 @@ constexpr int kKeys = kTreeChunk;       // keys of a chunk
 constexpr int kHalf = 64;               // keys of an S product, of a softmax step and of a P V product
 constexpr int kChunkBlocks = kKeys / kBlockSize;
 constexpr int kTiles = 2;
-constexpr int kThreads = 512;           // four warpgroups; warp 15 has no role
+constexpr int kThreads = 512;           // four warpgroups
 // Registers a thread: 512 x 128 at launch, dealt anew to the softmax warpgroups and
 // the other two (160 + 160 + 96 + 96 = 4 x 128).
 constexpr int kSoftmaxRegs = 160, kOtherRegs = 96;
@@ -86,8 +89,10 @@ constexpr float kNoMax = -3e38f;        // before the first key; finite, so that
 // exponents then take the scale's power of two alone, which is exact.
 constexpr float kFar = 8388608.f;
 constexpr int kItems = 4;               // items found ahead
-constexpr int kRoles = 14;              // warps that work on an item
+constexpr int kRoles = 15;              // warps that an item is told
 constexpr int kMaskWords = kTreeNodes / 32, kMaskStride = kMaskWords + 1;
+// Items of up to so many chunks (and 128 rows) go to one tile, the next one to the other.
+constexpr int kWhole = 4;
 constexpr int kGoneRing = 8;            // more than the chunks between a copy and its softmax
 
 template <int D>
@@ -134,7 +139,7 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b) {
   return s;
 }
 __device__ __forceinline__ int chunks_of(int ctx) { return (ctx + kKeys - 1) / kKeys; }
-__device__ __forceinline__ int groups_of(int n, int G) { return (n * G + kTreeRows - 1) / kTreeRows; }
+__host__ __device__ __forceinline__ int groups_of(int n, int G) { return (n * G + kTreeRows - 1) / kTreeRows; }
 // Units of a sequence on the line.
 __device__ __forceinline__ int units_of(const TreeArgs& a, const Seq& s, int G) {
   return s.n == 0 ? 0 : a.Hkv * groups_of(s.n, G) * (chunks_of(s.ctx) + kTreePairCost);
@@ -145,6 +150,17 @@ struct Item {
   int b, kvh, g, c0;
   int c1, q0, n, ctx;
   int place;   // where the sums go: 0 out, 1 the rows' own partials, 2 the CTA's
+  int tree;    // which of the trees' masks it needs, counted up; -1: holds no key of a tree
+  __device__ __forceinline__ int rows(int g2) const { return min(kTreeRows, (n << g2) - g * kTreeRows); }
+  __device__ __forceinline__ int chunks() const { return c1 - c0; }
+  // both tiles have rows of their own
+  __device__ __forceinline__ bool apart(int g2) const { return rows(g2) > kRows; }
+  // both tiles have the same rows, and every other chunk each
+  __device__ __forceinline__ bool shared(int g2) const { return !apart(g2) && chunks() > kWhole; }
+  // whether tile t takes the lc-th chunk of the CTA's m-th item
+  __device__ __forceinline__ bool takes(int g2, uint32_t m, int lc, int t) const {
+    return apart(g2) || (((int)m + (chunks() > kWhole ? lc : 0)) & 1) == t;
+  }
 };
 
 template <typename T, int D>
@@ -155,8 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   constexpr int SK = C::kKStages, SV = C::kVStages;
   extern __shared__ unsigned char tree_smem_raw[];
-  __shared__ __align__(8) uint64_t k_full[SK], k_free[SK], v_full[SV], v_free[SV], q_full, q_free,
-      s_full[kTiles][2], p_full[kTiles][2], o_done[kTiles][2], item_full[kItems],
+  __shared__ __align__(8) uint64_t k_full[SK], k_free[SK], v_full[SV], v_free[SV],
+      q_full[kTiles], q_free[kTiles], s_full[kTiles][2], p_full[kTiles][2], o_done[kTiles][2], item_full[kItems],
       item_free[kItems], mask_full, mask_free, meet_full[4], meet_free[4], drained[2 * kTiles];
   __shared__ int4 items[kItems][3];
   __shared__ float2 meet_ml[4][32];
@@ -183,14 +199,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_full[i], 1);
       mbar_init(&v_free[i], kTiles);
     }
-    mbar_init(&q_full, 1);
-    mbar_init(&q_free, kTiles);
-    for (int t = 0; t < kTiles; ++t)
+    for (int t = 0; t < kTiles; ++t) {
+      mbar_init(&q_full[t], 1);
+      mbar_init(&q_free[t], kTiles);
       for (int h = 0; h < 2; ++h) {
         mbar_init(&s_full[t][h], 1);
         mbar_init(&p_full[t][h], 4);   // one arrival per softmax warp
         mbar_init(&o_done[t][h], 1);
       }
+    }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&item_full[i], 1);
       mbar_init(&item_free[i], kRoles);
@@ -217,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 32 * 9) prefetch_tensor_map(&tm_v);
   pdl_wait_primary();
-  pdl_launch_dependents();   // the merge reads lengths before its own wait: not sooner
+  pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -232,14 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) return false;
     const int4 x = items[slot][0], y = items[slot][1];
     to.place = items[slot][2].x;
+    to.tree = items[slot][2].y;
     __syncwarp();
     if (lane == 0) mbar_arrive(&item_free[slot]);
     to.b = x.x, to.kvh = x.y, to.g = x.z, to.c0 = x.w;
     to.c1 = y.x, to.q0 = y.y, to.n = y.z, to.ctx = y.w;
     return to.n > 0;
   };
-  // rows of the item's group; whether each tile has rows of its own
-  auto rows_of = [&](const Item& i) { return min(kTreeRows, (i.n << g2) - i.g * kTreeRows); };
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -252,27 +268,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float qscale = a.qscale;
     // a zero scale as a tiny one: every weight is 1 and -inf stays -inf
     const float qmul = fmaxf(fabsf(qscale), 1e-37f);
-    uint32_t done = 0, chunk0 = 0, met = 0, masked = 0;   // this tile's chunks, the CTA's, exchanges, masks used
+    uint32_t done = 0, chunk0 = 0, met = 0;   // this tile's chunks, the CTA's, exchanges
+    int held = -1;                            // the masks that this warp may still use ..
+    bool mask_there = false;                  // .. and whether it has waited for them
     Item next;
     bool have = take(0, next);
     for (uint32_t m = 0; ok && have; ++m) {
       it = next;
-      const int rows = rows_of(it), n_chunks = it.c1 - it.c0;
-      const bool apart = rows > kRows;                 // each tile has rows of its own
-      const int main = m & 1;                          // else the tile that ends the item
+      const int rows = it.rows(g2), n_chunks = it.chunks();
+      const bool apart = it.apart(g2), both = it.shared(g2);
+      const int main = m & 1;                          // the tile that ends an item of one tile's rows
       const int my_rows = apart && t == 1 ? rows - kRows : min(rows, kRows);
       const bool active = w4 * 32 < my_rows;           // a row of the warp is there
       const int group_row = apart ? t * kRows + trow : trow;
       const int row = it.g * kTreeRows + min(group_row, rows - 1);   // (node, head) of the sequence
       const int tree0 = it.ctx - it.n;
-      const bool has_tree = it.c1 * kKeys > tree0;     // the item holds keys of the tree
       const uint32_t* mask = masks + (row >> g2) * kMaskStride;
-      bool mask_there = false;
+      if (it.tree >= 0 && it.tree != held) {
+        // the last ones go back; no phase of the barrier is passed over
+        if (held >= 0 && !mask_there) ok = cta_wait(&mask_full, held & 1, gave_up);
+        if (!ok) break;
+        __syncwarp();
+        if (held >= 0 && lane == 0) mbar_arrive(&mask_free);
+        held = it.tree;
+        mask_there = false;
+      }
       float m_run = kNoMax, l_run = 0.f;   // running maximum, unscaled; sum of weights
       float qm = qmul, base = 0.f;
       bool begun = false;
       for (int lc = 0; lc < n_chunks; ++lc) {
-        if (!apart && ((lc + main) & 1) != t) continue;
+        if (!it.takes(g2, m, lc, t)) continue;
         const int key0 = (it.c0 + lc) * kKeys;
         const int valid = min(kKeys, it.ctx - key0);
         uint32_t gone = 0;
@@ -292,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t gone4 = (gone >> (4 * half)) & 15u;
             if (k0 + kHalf > tree0 || gone4) {
               // which of the 64 keys the row sees
-              if (has_tree && !mask_there) {
-                ok = cta_wait(&mask_full, masked & 1, gave_up);
+              if (it.tree >= 0 && !mask_there) {
+                ok = cta_wait(&mask_full, it.tree & 1, gave_up);
                 if (!ok) break;
                 mask_there = true;
               }
@@ -378,18 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       chunk0 += n_chunks;
-      if (has_tree) {
-        // the masks go back, whether this warp has used them or not
-        if (!mask_there) ok = cta_wait(&mask_full, masked & 1, gave_up);
-        if (!ok) break;
-        ++masked;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&mask_free);
-      }
       have = take(m + 1, next);   // while the last product runs
       if (!ok) break;
       // ---- the item's end: O / l, or what a partial holds
-      const bool both = !apart && n_chunks > 1;   // both tiles have sums of the same rows
       if (!active || (!apart && t != main && !both)) continue;
       ok = cta_wait(&o_done[t][1], (done - 1) & 1, gave_up);
       if (!ok) break;
@@ -481,20 +497,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* missing = is_v ? v_gone : k_gone;
       const CUtensorMap* map = is_v ? &tm_v : &tm_k;
       const uint32_t ring = is_v ? sV : sK;
-      uint32_t kc = 0, q_count = 0;   // chunks, Q's asked for so far
-      for (uint32_t m = 0; ok && take(m, it); ++m) {
-        const int32_t* table = a.block_tables + (int64_t)it.b * a.MBS;
-        auto block_of = [&](int c) -> int {   // -1: past the context; -2: outside the pool
-          const int i = c * kChunkBlocks + lane;
-          if (c >= it.c1 || lane >= kChunkBlocks || i * kBlockSize >= it.ctx) return -1;
-          const int id = __ldg(table + i);
-          return id >= 0 && id < a.NB ? id : -2;
-        };
-        int ahead = block_of(it.c0);
-        for (int c = it.c0; c < it.c1 && ok; ++c, ++kc) {
-          const int st = kc % S;
-          const int id = ahead;
-          ahead = block_of(c + 1);
+      uint32_t kc = 0, q_uses[kTiles] = {0, 0};   // chunks, Q tiles of each place asked for so far
+      // Block ids come for four chunks at a time (a lane each), asked for a group ahead,
+      // across items too.  -1: past the context; -2: outside the pool.
+      constexpr int kGroup = 32 / kChunkBlocks;
+      auto blocks_of = [&](const Item& i, int c) -> int {
+        const int k = c * kChunkBlocks + lane;
+        if (k >= i.c1 * kChunkBlocks || k * kBlockSize >= i.ctx) return -1;
+        const int id = __ldg(a.block_tables + (int64_t)i.b * a.MBS + k);
+        return id >= 0 && id < a.NB ? id : -2;
+      };
+      Item next;
+      bool have = take(0, next);
+      int ids = 0, ahead = have ? blocks_of(next, next.c0) : -1;
+      for (uint32_t m = 0; ok && have; ++m) {
+        it = next;
+        for (int c = it.c0; c < it.c1 && ok; ++c) {
+          const int st = kc % S, in_group = (c - it.c0) % kGroup;
+          if (in_group == 0) ids = ahead;
+          const int mine = __shfl_sync(0xffffffffu, ids, in_group * kChunkBlocks + lane % kChunkBlocks);
+          const int id = lane < kChunkBlocks ? mine : -1;
           if (kc >= (uint32_t)S) ok = cta_wait(&freed[st], ((kc / S) - 1) & 1, gave_up);
           if (!ok) break;
           const unsigned present = __ballot_sync(0xffffffffu, id >= 0);
@@ -512,28 +534,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                            map, h * 64, (id * a.Hkv + it.kvh) * kBlockSize, &full[st]);
           }
           __syncwarp();
-          if (is_v || c > it.c0) continue;
-          // the Q tiles, after the first chunk is on its way
-          if (m > 0) ok = cta_wait(&q_free, (m - 1) & 1, gave_up);
-          if (!ok) break;
-          ++q_count;
-          if (lane == 0) {
-            const int tiles = rows_of(it) > kRows ? 2 : 1;
-            mbar_arrive_expect_tx(&q_full, tiles * C::kQBytes);
-            for (int i = 0; i < tiles; ++i)
+          ++kc;
+          if (!is_v && c == it.c0) {
+            // the Q tiles, after the first chunk is on its way; items of one tile's rows
+            // take the two places in turn
+            const bool apart = it.apart(g2);
+            for (int i = 0; ok && i < kTiles; ++i) {
+              if (!apart && i != (int)(m & 1)) continue;
+              if (q_uses[i] > 0) ok = cta_wait(&q_free[i], (q_uses[i] - 1) & 1, gave_up);
+              if (!ok) break;
+              ++q_uses[i];
+              if (lane != 0) continue;
+              mbar_arrive_expect_tx(&q_full[i], C::kQBytes);
 #pragma unroll
               for (int h = 0; h < D / 64; ++h)
                 tma_load_box3(sQ + i * C::kQBytes + h * (kRows * 128), &tm_q, h * 64, it.kvh * G,
-                              it.q0 + ((it.g * kTreeRows + i * kRows) >> g2), &q_full);
+                              it.q0 + ((it.g * kTreeRows + (apart ? i * kRows : 0)) >> g2), &q_full[i]);
+            }
+            __syncwarp();
+            if (!ok) break;
           }
-          __syncwarp();
+          if (in_group == 0) {
+            if (c + kGroup < it.c1) {
+              ahead = blocks_of(it, c + kGroup);
+            } else {
+              have = take(m + 1, next);
+              if (ok && have) ahead = blocks_of(next, next.c0);
+            }
+          }
         }
       }
       if (!ok) {
         // what is in flight lands before the CTA ends
         for (uint32_t c = kc > (uint32_t)S ? kc - S : 0; c < kc; ++c)
           (void)mbar_wait_bounded(&full[c % S], (c / S) & 1);
-        if (q_count > 0) (void)mbar_wait_bounded(&q_full, (q_count - 1) & 1);
+        for (int i = 0; i < kTiles; ++i)
+          if (q_uses[i] > 0) (void)mbar_wait_bounded(&q_full[i], (q_uses[i] - 1) & 1);
       }
     } else if (warp == 14) {
       // ================================================================ items
@@ -543,7 +579,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         total += __reduce_add_sync(0xffffffffu, (unsigned)units_of(a, seq_of(a, b0 + lane), G));
       const int per = (int)((total + gridDim.x - 1) / gridDim.x);
       const int u0 = (int)min(total, (int64_t)blockIdx.x * per), u1 = (int)min(total, (int64_t)u0 + per);
-      uint32_t m = 0, masked = 0;
+      uint32_t m = 0;
+      int trees = 0, masked_b = -1;   // masks asked for so far, and the last one's sequence
+      bool told = false;
+      // whose partials lie with this CTA: the pair that its run begins in the midst of
+      auto tell = [&](int4 v) {
+        if (!told && lane == 0) a.ws_split[blockIdx.x] = v;
+        told = true;
+      };
       auto publish = [&](const Item& i) {
         const int slot = m % kItems;
         if (m >= kItems) ok = cta_wait(&item_free[slot], ((m / kItems) - 1) & 1, gave_up);
@@ -552,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           items[slot][0] = make_int4(i.b, i.kvh, i.g, i.c0);
           items[slot][1] = make_int4(i.c1, i.q0, i.n, i.ctx);
           items[slot][2].x = i.place;
+          items[slot][2].y = i.tree;
           mbar_arrive(&item_full[slot]);
         }
         __syncwarp();
@@ -585,62 +629,85 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.c1 <= it.c0) continue;
             const int t_first = at / per, t_last = (at + chunks - 1) / per;
             it.place = t_first == t_last ? 0 : (int)blockIdx.x == t_first ? 1 : 2;
-            if ((int)blockIdx.x == t_first && lane == 0)
-              a.ws_pair[((int64_t)it.b * a.Hkv + it.kvh) * a.groups + it.g] = make_int2(t_first, t_last);
+            tell(it.place == 2 ? make_int4(it.b, it.kvh * groups + it.g, t_first, t_last)
+                               : make_int4(0, 0, 0, -1));
+            const bool tree = it.c1 * kKeys > it.ctx - it.n, fresh = tree && it.b != masked_b;
+            trees += fresh;
+            it.tree = tree ? trees - 1 : -1;
+            if (tree) masked_b = it.b;
             publish(it);
-            if (!ok || it.c1 * kKeys <= it.ctx - it.n) continue;
-            // ---- the nodes' ancestors, each node its own
-            if (masked > 0) ok = cta_wait(&mask_free, (masked - 1) & 1, gave_up);
-            if (!ok) break;
-            ++masked;
-            const int words = (it.n + 31) >> 5;
-            bool wrong = false;
-            for (int i = lane; i < it.n; i += 32) {
-              int x = __ldg(a.parents + it.q0 + i);
-              if (x < -1 || x >= i) {
-                wrong = true;
-                x = -1;
-              }
-              up[i] = x;
-#pragma unroll
-              for (int w = 0; w < kMaskWords; ++w)
-                masks[i * kMaskStride + w] = w == i >> 5 ? 1u << (i & 31) : 0u;
-            }
-            if (wrong) raise_error(a.err, kErrTree);
-            __syncwarp();
-            // node i's mask holds it and its ancestors down to, not with, up[i]
-            bool more = true;
-            while (more) {
-              more = false;
-              for (int i0 = 0; i0 < it.n; i0 += 32) {
-                const int i = i0 + lane;
-                const int x = i < it.n ? up[i] : -1;
-                int y = -1;
-                uint32_t add[kMaskWords];
-                if (x >= 0) {
-                  y = up[x];
-#pragma unroll
-                  for (int w = 0; w < kMaskWords; ++w) add[w] = w < words ? masks[x * kMaskStride + w] : 0u;
-                }
-                __syncwarp();   // a node's mask and its up change together
-                if (x >= 0) {
-                  up[i] = y;
-#pragma unroll
-                  for (int w = 0; w < kMaskWords; ++w)
-                    if (w < words) masks[i * kMaskStride + w] |= add[w];
-                }
-                __syncwarp();
-                more |= __any_sync(0xffffffffu, y >= 0);
-              }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&mask_full);
           }
         }
         u += __shfl_sync(0xffffffffu, sum, 31);
       }
+      tell(make_int4(0, 0, 0, -1));
       it.n = 0;
       if (ok) publish(it);
+    } else if (warp == 15) {
+      // ================================================================ the nodes' ancestors
+      // One set of masks at a time, for all items of a sequence in a row; a softmax warp
+      // gives them back on the first item with others.
+      int made = -1;
+      for (uint32_t m = 0; ok && take(m, it); ++m) {
+        if (it.tree <= made) continue;
+        made = it.tree;
+        if (made > 0) ok = cta_wait(&mask_free, (made - 1) & 1, gave_up);
+        if (!ok) break;
+        const int words = (it.n + 31) >> 5;
+        bool wrong = false;
+        for (int i = lane; i < it.n; i += 32) {
+          int x = __ldg(a.parents + it.q0 + i);
+          if (x < -1 || x >= i) {
+            wrong = true;
+            x = -1;
+          }
+          up[i] = x;
+#pragma unroll
+          for (int w = 0; w < kMaskWords; ++w)
+            masks[i * kMaskStride + w] = w == i >> 5 ? 1u << (i & 31) : 0u;
+        }
+        if (wrong) raise_error(a.err, kErrTree);
+        __syncwarp();
+        // node i's mask holds it and its ancestors down to, not with, up[i]
+        bool more = true;
+        while (more) {
+          more = false;
+          for (int i0 = 0; i0 < it.n; i0 += 32) {
+            const int i = i0 + lane;
+            const int x = i < it.n ? up[i] : -1;
+            int y = -1;
+            uint32_t add[kMaskWords];
+            if (x >= 0) {
+              y = up[x];
+#pragma unroll
+              for (int w = 0; w < kMaskWords; ++w) add[w] = w < words ? masks[x * kMaskStride + w] : 0u;
+            }
+            __syncwarp();   // a node's mask and its up change together
+            if (x >= 0) {
+              up[i] = y;
+#pragma unroll
+              for (int w = 0; w < kMaskWords; ++w)
+                if (w < words) masks[i * kMaskStride + w] |= add[w];
+            }
+            __syncwarp();
+            more |= __any_sync(0xffffffffu, y >= 0);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mask_full);
+      }
+      // ---- rejected sequences: their error, and zero rows where they have rows
+      for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        if (seq_of(a, b).n > 0) continue;
+        const int q0 = __ldg(a.query_start + b), n = __ldg(a.query_start + b + 1) - q0;
+        const bool outside = q0 < 0 || n < 0 || q0 + n > a.num_tokens;
+        if (n == 0 && !outside) continue;
+        if (lane == 0) raise_error(a.err, outside || n > a.max_query_len ? kErrQuery : kErrContext);
+        if (outside) continue;
+        const int64_t chunks = (int64_t)min(n, a.max_query_len) * a.Hq * (D / 8);
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)q0 * a.Hq * D);
+        for (int64_t i = lane; i < chunks; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
     } else if (warp >= 10 && warp < 14) {
       // ================================================================ products
       const int t = (warp - 10) & 1;
@@ -654,16 +721,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // descriptor), so that the maximum is always the largest score
         const uint32_t id_s = f16_idesc<T>(kRows, kHalf) | (a.qscale < 0.f ? 1u << 13 : 0u);
         const uint64_t q_desc0 = sw128_desc(sQ), k_desc = sw128_desc(sK);
+        uint32_t q_uses[kTiles] = {0, 0};
         for (uint32_t m = 0; ok && take(m, it); ++m) {
-          const bool apart = rows_of(it) > kRows;
-          const int n_chunks = it.c1 - it.c0, main = m & 1;
-          const uint64_t q_desc = q_desc0 + (uint64_t)((apart ? t * C::kQBytes : 0) >> 4);
-          ok = cta_wait(&q_full, m & 1, gave_up);
+          const bool apart = it.apart(g2);
+          const int n_chunks = it.chunks(), place = apart ? t : (int)(m & 1);
+          const uint64_t q_desc = q_desc0 + (uint64_t)((place * C::kQBytes) >> 4);
+          ok = cta_wait(&q_full[place], q_uses[place] & 1, gave_up);
           if (!ok) break;
           for (int lc = 0; lc < n_chunks; ++lc) {
             const uint32_t kc = chunk0 + lc;
             ok = cta_wait(&k_full[kc % SK], (kc / SK) & 1, gave_up);
-            if (ok && (apart || ((lc + main) & 1) == t)) {
+            if (ok && it.takes(g2, m, lc, t)) {
               const uint64_t kb = k_desc + (uint64_t)(((kc % SK) * C::kKvBytes) >> 4);
               for (int h = 0; h < 2; ++h) {
                 // P of the last chunk's half, which lies over S, is used
@@ -690,7 +758,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&k_free[kc % SK]);
           }
           if (!ok) break;
-          if (lane == 0) mbar_arrive(&q_free);   // the item's S are done
+          // the item's S are done
+          for (int i = 0; i < kTiles; ++i) {
+            if (!apart && i != place) continue;
+            ++q_uses[i];
+            if (lane == 0) mbar_arrive(&q_free[i]);
+          }
           chunk0 = uniform(chunk0 + n_chunks);
         }
       } else {
@@ -699,8 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kNothing = ~0u;
         uint32_t held = kNothing;   // the chunk whose V stage is to be handed back
         for (uint32_t m = 0; ok && take(m, it); ++m) {
-          const bool apart = rows_of(it) > kRows;
-          const int n_chunks = it.c1 - it.c0, main = m & 1;
+          const int n_chunks = it.chunks();
           bool begun = false;
           for (int lc = 0; lc < n_chunks; ++lc) {
             const uint32_t vc = chunk0 + lc;
@@ -712,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ok = cta_wait(&v_full[vc % SV], (vc / SV) & 1, gave_up);
             if (!ok) break;
-            if (!apart && ((lc + main) & 1) != t) {   // a chunk of the other tile
+            if (!it.takes(g2, m, lc, t)) {   // a chunk of the other tile
               if (lane == 0) mbar_arrive(&v_free[vc % SV]);
               continue;
             }
@@ -782,54 +854,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // out = sum_p w_p o_p / sum_p w_p l_p with w_p = 2^(scale (m_p - max m)) over the
-// partials of a row, and the zero rows of rejected sequences.  A CTA takes rows
-// [slice kMergeRows, ..) of the trees of (sequence, KV head), a warp a row at a time.
-constexpr int kMergeThreads = 256, kMergeRows = 64;
+// partials of a row.  A pair's partials lie with consecutive CTAs, and the second one's
+// index names the pair here; a CTA takes kMergeRows of its rows, D / 4 lanes a row.
+constexpr int kMergeThreads = 256, kMergeRows = 16;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a) {
-  constexpr int EPL = D / 32, kWarps = kMergeThreads / 32, kAhead = 4;
+  constexpr int kLanes = D / 4, kAtOnce = kMergeThreads / kLanes, kAhead = 4;
   pdl_launch_dependents();
-  const int kvh = blockIdx.x, b = blockIdx.y;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = a.Hq / a.Hkv, g2 = __ffs(G) - 1;
-  // every CTA of the attention kernel has passed its own wait: these are there
-  const Seq s = seq_of(a, b);
-  const int row0 = blockIdx.z * kMergeRows;
-  T* out = static_cast<T*>(a.out);
-  if (s.n == 0) {
-    const int q0 = __ldg(a.query_start + b), n = __ldg(a.query_start + b + 1) - q0;
-    if (n == 0 && q0 >= 0 && q0 <= a.num_tokens) return;
-    const bool outside = q0 < 0 || n < 0 || q0 + n > a.num_tokens;
-    const bool query = outside || n > a.max_query_len;
-    if (threadIdx.x == 0 && kvh == 0 && row0 == 0) raise_error(a.err, query ? kErrQuery : kErrContext);
-    if (outside) return;
-    pdl_wait_primary();
-    const int rows = min(row0 + kMergeRows, min(n, a.max_query_len) << g2);
-    for (int i = row0 * (D / 8) + threadIdx.x; i < rows * (D / 8); i += kMergeThreads) {
-      const int r = i / (D / 8);
-      reinterpret_cast<uint4*>(out + ((int64_t)(q0 + (r >> g2)) * a.Hq + kvh * G + (r & (G - 1))) * D)[i % (D / 8)] =
-          make_uint4(0u, 0u, 0u, 0u);
-    }
-    return;
-  }
-  const int rows = s.n << g2;
-  if (row0 >= rows) return;
   pdl_wait_primary();
+  const int4 split = a.ws_split[blockIdx.y + 1];
+  if (split.w < 0 || split.z != (int)blockIdx.y) return;   // nothing, or another one's pair
+  const int lane = threadIdx.x % kLanes;
+  const int G = a.Hq / a.Hkv, g2 = __ffs(G) - 1;
+  const int b = split.x;
+  const Seq s = seq_of(a, b);
+  const int groups = groups_of(s.n, G), kvh = split.y / groups, g = split.y - kvh * groups;
+  const int row0 = g * kTreeRows + blockIdx.x * kMergeRows, rows = min(s.n << g2, (g + 1) * kTreeRows);
+  const int2 pr = make_int2(split.z, split.w);
   const float qmul = fmaxf(fabsf(a.qscale), 1e-37f);
-  const int g = row0 / kTreeRows;
-  const int2 pr = a.ws_pair[((int64_t)b * a.Hkv + kvh) * a.groups + g];
-  if (pr.x == pr.y) return;   // the attention kernel wrote out
-  for (int r = row0 + warp; r < min(rows, row0 + kMergeRows); r += kWarps) {
+  T* out = static_cast<T*>(a.out);
+  for (int r = row0 + threadIdx.x / kLanes; r < min(rows, row0 + kMergeRows); r += kAtOnce) {
     const int64_t head = (int64_t)(s.q0 + (r >> g2)) * a.Hq + kvh * G + (r & (G - 1));
     // the first partial lies with the row, the others with their CTAs
     const int64_t later = (int64_t)a.num_tokens * a.Hq + (int64_t)pr.x * kTreeRows + (r - g * kTreeRows);
     const int parts = pr.y - pr.x + 1;
-    float M = kNoMax, L = 0.f, O[EPL];
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) O[e] = 0.f;
+    float M = kNoMax, L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p0 = 0; p0 < parts; p0 += kAhead) {
-      float v[kAhead][EPL];
+      float4 v[kAhead];
       float2 ml[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
@@ -837,8 +890,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
         const int64_t at = p == 0 ? head : later + (int64_t)p * kTreeRows;
         ml[i] = a.ws_ml[at];
         if (p0 + i >= parts) ml[i].y = 0.f;
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) v[i][e] = a.ws_o[at * D + lane * EPL + e];
+        v[i] = reinterpret_cast<const float4*>(a.ws_o + at * D)[lane];
       }
       float top = M;
 #pragma unroll
@@ -847,22 +899,19 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
       const float r0 = softmax_exp2((M - top) * qmul);
       M = top;
       L *= r0;
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) O[e] *= r0;
+      O.x *= r0, O.y *= r0, O.z *= r0, O.w *= r0;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (ml[i].y == 0.f) continue;   // no key of that part, or not a part
         const float w = softmax_exp2((ml[i].x - M) * qmul);
         L = fmaf(w, ml[i].y, L);
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) O[e] = fmaf(w, v[i][e], O[e]);
+        O.x = fmaf(w, v[i].x, O.x), O.y = fmaf(w, v[i].y, O.y);
+        O.z = fmaf(w, v[i].z, O.z), O.w = fmaf(w, v[i].w, O.w);
       }
     }
     const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-#pragma unroll
-    for (int e = 0; e < EPL; e += 2)
-      *reinterpret_cast<uint32_t*>(out + head * D + lane * EPL + e) =
-          Mma<T>::pack(O[e] * inv, O[e + 1] * inv);
+    reinterpret_cast<uint2*>(out + head * D)[lane] =
+        make_uint2(Mma<T>::pack(O.x * inv, O.y * inv), Mma<T>::pack(O.z * inv, O.w * inv));
   }
 }
 
@@ -891,12 +940,14 @@ cudaError_t launch_t(const TreeArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if ((e = make_pool_map(&tk, a.k_cache, a.dtype, a.NB, a.Hkv, a.D)) != cudaSuccess) return e;
   if ((e = make_pool_map(&tv, a.v_cache, a.dtype, a.NB, a.Hkv, a.D)) != cudaSuccess) return e;
-  const int64_t most = (int64_t)a.B * a.Hkv * a.groups * ((a.MBS * kBlockSize + kKeys - 1) / kKeys + kTreePairCost);
+  const int64_t most = (int64_t)a.B * a.Hkv * groups_of(a.max_query_len, (int)G) * ((a.MBS * kBlockSize + kKeys - 1) / kKeys + kTreePairCost);
   const int grid = (int)std::min<int64_t>(std::min(a.num_sms, kTreeMaxCtas), most);
   e = launch_pdl(kern, dim3(grid), dim3(kThreads), C::kSmem, stream, tq, tk, tv, a);
   if (e != cudaSuccess) return e;
-  const int slices = (a.max_query_len * (int)G + kMergeRows - 1) / kMergeRows;
-  return launch_pdl(tree_merge_kernel<T, D>, dim3(a.Hkv, a.B, slices), dim3(kMergeThreads), 0, stream, a);
+  if (grid == 1) return cudaSuccess;
+  const int rows = std::min(a.max_query_len * (int)G, kTreeRows);
+  return launch_pdl(tree_merge_kernel<T, D>, dim3((rows + kMergeRows - 1) / kMergeRows, grid - 1),
+                    dim3(kMergeThreads), 0, stream, a);
 }
 
 }  // namespace
