@@ -1093,8 +1093,9 @@ photon_status_t photon_verify_tree(const void* target_probs, int64_t target_stri
   a.draft_stride = draft_stride ? draft_stride : vocab;
   if (a.target_stride < vocab || a.draft_stride < vocab) return PHOTON_ERR_INVALID_ARG;
   if (num_seqs == 0) return PHOTON_OK;
-  if (!target_probs || !tokens || !parents || !query_start || !accept_uniforms ||
-      !sample_uniforms || !path || !path_len || !next_token)
+  if (!query_start || !sample_uniforms || !path_len || !next_token) return PHOTON_ERR_INVALID_ARG;
+  // (arrays of no rows may be null)
+  if (num_tokens > 0 && (!target_probs || !tokens || !parents || !accept_uniforms || !path))
     return PHOTON_ERR_INVALID_ARG;
   const uintptr_t elem = elem_bytes(dtype) - 1;
   if ((reinterpret_cast<uintptr_t>(target_probs) & elem) ||

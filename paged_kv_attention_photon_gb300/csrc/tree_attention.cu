@@ -157,6 +157,10 @@ struct Item {
   __device__ __forceinline__ bool apart(int g2) const { return rows(g2) > kRows; }
   // both tiles have the same rows, and every other chunk each
   __device__ __forceinline__ bool shared(int g2) const { return !apart(g2) && chunks() > kWhole; }
+  // the place of tile t's Q: items of one tile's rows take the two places in turn
+  __device__ __forceinline__ int place_of(int g2, uint32_t m, int t) const {
+    return apart(g2) ? t : (int)(m & 1);
+  }
   // whether tile t takes the lc-th chunk of the CTA's m-th item
   __device__ __forceinline__ bool takes(int g2, uint32_t m, int lc, int t) const {
     return apart(g2) || (((int)m + (chunks() > kWhole ? lc : 0)) & 1) == t;
@@ -536,20 +540,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           ++kc;
           if (!is_v && c == it.c0) {
-            // the Q tiles, after the first chunk is on its way; items of one tile's rows
-            // take the two places in turn
-            const bool apart = it.apart(g2);
+            // the Q tiles, after the first chunk is on its way
             for (int i = 0; ok && i < kTiles; ++i) {
-              if (!apart && i != (int)(m & 1)) continue;
+              if (it.place_of(g2, m, i) != i) continue;
               if (q_uses[i] > 0) ok = cta_wait(&q_free[i], (q_uses[i] - 1) & 1, gave_up);
               if (!ok) break;
               ++q_uses[i];
               if (lane != 0) continue;
+              const int first = it.g * kTreeRows + (it.apart(g2) ? i * kRows : 0);
               mbar_arrive_expect_tx(&q_full[i], C::kQBytes);
 #pragma unroll
               for (int h = 0; h < D / 64; ++h)
                 tma_load_box3(sQ + i * C::kQBytes + h * (kRows * 128), &tm_q, h * 64, it.kvh * G,
-                              it.q0 + ((it.g * kTreeRows + (apart ? i * kRows : 0)) >> g2), &q_full[i]);
+                              it.q0 + (first >> g2), &q_full[i]);
             }
             __syncwarp();
             if (!ok) break;
@@ -721,12 +724,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // descriptor), so that the maximum is always the largest score
         const uint32_t id_s = f16_idesc<T>(kRows, kHalf) | (a.qscale < 0.f ? 1u << 13 : 0u);
         const uint64_t q_desc0 = sw128_desc(sQ), k_desc = sw128_desc(sK);
-        uint32_t q_uses[kTiles] = {0, 0};
+        uint32_t q_uses0 = 0, q_uses1 = 0;   // of each place so far
         for (uint32_t m = 0; ok && take(m, it); ++m) {
-          const bool apart = it.apart(g2);
-          const int n_chunks = it.chunks(), place = apart ? t : (int)(m & 1);
+          const int n_chunks = it.chunks(), place = it.place_of(g2, m, t);
           const uint64_t q_desc = q_desc0 + (uint64_t)((place * C::kQBytes) >> 4);
-          ok = cta_wait(&q_full[place], q_uses[place] & 1, gave_up);
+          ok = cta_wait(&q_full[place], (place ? q_uses1 : q_uses0) & 1, gave_up);
           if (!ok) break;
           for (int lc = 0; lc < n_chunks; ++lc) {
             const uint32_t kc = chunk0 + lc;
@@ -759,10 +761,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           // the item's S are done
-          for (int i = 0; i < kTiles; ++i) {
-            if (!apart && i != place) continue;
-            ++q_uses[i];
-            if (lane == 0) mbar_arrive(&q_free[i]);
+          if (it.place_of(g2, m, 0) == 0) {
+            ++q_uses0;
+            if (lane == 0) mbar_arrive(&q_free[0]);
+          }
+          if (it.place_of(g2, m, 1) == 1) {
+            ++q_uses1;
+            if (lane == 0) mbar_arrive(&q_free[1]);
           }
           chunk0 = uniform(chunk0 + n_chunks);
         }
@@ -855,11 +860,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // out = sum_p w_p o_p / sum_p w_p l_p with w_p = 2^(scale (m_p - max m)) over the
 // partials of a row.  A pair's partials lie with consecutive CTAs, and the second one's
-// index names the pair here; a CTA takes kMergeRows of its rows, D / 4 lanes a row.
-constexpr int kMergeThreads = 256, kMergeRows = 16;
+// index names the pair here; a CTA takes `slice` of its rows, D / 4 lanes a row.
+constexpr int kMergeThreads = 256, kMergeSlices = 8;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a, int slice) {
   constexpr int kLanes = D / 4, kAtOnce = kMergeThreads / kLanes, kAhead = 4;
   pdl_launch_dependents();
   pdl_wait_primary();
@@ -870,11 +875,11 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
   const int b = split.x;
   const Seq s = seq_of(a, b);
   const int groups = groups_of(s.n, G), kvh = split.y / groups, g = split.y - kvh * groups;
-  const int row0 = g * kTreeRows + blockIdx.x * kMergeRows, rows = min(s.n << g2, (g + 1) * kTreeRows);
+  const int row0 = g * kTreeRows + blockIdx.x * slice, rows = min(s.n << g2, (g + 1) * kTreeRows);
   const int2 pr = make_int2(split.z, split.w);
   const float qmul = fmaxf(fabsf(a.qscale), 1e-37f);
   T* out = static_cast<T*>(a.out);
-  for (int r = row0 + threadIdx.x / kLanes; r < min(rows, row0 + kMergeRows); r += kAtOnce) {
+  for (int r = row0 + threadIdx.x / kLanes; r < min(rows, row0 + slice); r += kAtOnce) {
     const int64_t head = (int64_t)(s.q0 + (r >> g2)) * a.Hq + kvh * G + (r & (G - 1));
     // the first partial lies with the row, the others with their CTAs
     const int64_t later = (int64_t)a.num_tokens * a.Hq + (int64_t)pr.x * kTreeRows + (r - g * kTreeRows);
@@ -945,9 +950,11 @@ cudaError_t launch_t(const TreeArgs& a, cudaStream_t stream) {
   e = launch_pdl(kern, dim3(grid), dim3(kThreads), C::kSmem, stream, tq, tk, tv, a);
   if (e != cudaSuccess) return e;
   if (grid == 1) return cudaSuccess;
+  // the pairs' rows in up to kMergeSlices parts: as many CTAs as the device holds at once
   const int rows = std::min(a.max_query_len * (int)G, kTreeRows);
-  return launch_pdl(tree_merge_kernel<T, D>, dim3((rows + kMergeRows - 1) / kMergeRows, grid - 1),
-                    dim3(kMergeThreads), 0, stream, a);
+  const int slice = std::max(kMergeThreads / (D / 4), (rows + kMergeSlices - 1) / kMergeSlices);
+  return launch_pdl(tree_merge_kernel<T, D>, dim3((rows + slice - 1) / slice, grid - 1),
+                    dim3(kMergeThreads), 0, stream, a, slice);
 }
 
 }  // namespace

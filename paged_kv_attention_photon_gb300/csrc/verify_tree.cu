@@ -32,9 +32,7 @@
 namespace photon {
 namespace {
 
-constexpr int kVerifyThreads = 256;
-constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyCtas = 4;      // per SM
+constexpr int kVerifyResident = 1024;   // threads per SM: 64 registers each
 constexpr int kVerifyCluster = 8;   // most CTAs of a cluster
 constexpr int kVerifyRun = kVerifyVocab / kVerifyCluster;   // most tokens of a CTA's run
 
@@ -176,13 +174,13 @@ __device__ __forceinline__ void store_peer(float2* p, int rank, float2 v) {
 }
 
 // kVec: rows begin on 16-byte boundaries.
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
+template <typename T, bool kVec, int kThreads>
+__global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
     verify_tree_kernel(const VerifyArgs a, int ranks) {
-  constexpr int N = 16 / sizeof(T), kTile = 32 * N, kDepth = 16 / N;   // elements of a lane, of a warp; loads ahead
+  constexpr int kWarps = kThreads / 32, N = 16 / sizeof(T), kTile = 32 * N, kDepth = 8 / N;   // elements of a lane, of a warp; loads ahead
   __shared__ int parent[kTreeNodes], token[kTreeNodes], path[kTreeNodes];
   __shared__ float prob[kTreeNodes], draft[kTreeNodes], number[kTreeNodes];
-  __shared__ float2 sums_of[2][kVerifyCluster * kVerifyWarps];
+  __shared__ float2 sums_of[2][kVerifyCluster * kWarps];
   __shared__ float2 threshold, owner_before;
   __shared__ float2 state_less;   // L
   __shared__ int state_node, state_len, state_sweep, state_out, row_left, owner_warp;
@@ -206,12 +204,12 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
   const T* drafts = a.draft ? static_cast<const T*>(a.draft) + (int64_t)q0 * a.draft_stride : nullptr;
   const int V = a.vocab;
   // each warp's run, in whole tiles
-  const int per_warp = ((V + ranks * kVerifyWarps - 1) / (ranks * kVerifyWarps) + kTile - 1) / kTile * kTile;
-  const int64_t cta_begin = (int64_t)rank * kVerifyWarps * per_warp;
+  const int per_warp = ((V + ranks * kWarps - 1) / (ranks * kWarps) + kTile - 1) / kTile * kTile;
+  const int64_t cta_begin = (int64_t)rank * kWarps * per_warp;
   const int run0 = (int)min((int64_t)V, cta_begin + (int64_t)warp * per_warp);
   const int run1 = (int)min((int64_t)V, cta_begin + (int64_t)(warp + 1) * per_warp);
 
-  for (int i = tid; i < n; i += kVerifyThreads) {
+  for (int i = tid; i < n; i += kThreads) {
     int up = __ldg(a.parents + q0 + i);
     int x = __ldg(a.tokens + q0 + i);
     if (up < -1 || up >= i || x >= V) {
@@ -234,7 +232,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
   __syncthreads();
   if (!drafts) {
     // a sibling before it has the same token: nothing is left for it
-    for (int i = tid; i < n; i += kVerifyThreads) {
+    for (int i = tid; i < n; i += kThreads) {
       bool same = false;
       for (int j = 0; j < i; ++j) same |= parent[j] == parent[i] && token[j] == token[i];
       if (same) prob[i] = 0.f;
@@ -290,11 +288,11 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
     sum.over(32);
     const int parity = round++ & 1;
     // every warp's sum to every CTA of the cluster
-    if (lane < ranks) store_peer(&sums_of[parity][rank * kVerifyWarps + warp], lane, make_float2(sum.hi, sum.lo));
+    if (lane < ranks) store_peer(&sums_of[parity][rank * kWarps + warp], lane, make_float2(sum.hi, sum.lo));
     cluster_sync();
     if (warp == 0) {
       Sum2 all;
-      for (int k = lane; k < ranks * kVerifyWarps; k += 32) {
+      for (int k = lane; k < ranks * kWarps; k += 32) {
         const float2 s = sums_of[parity][k];
         all.add(s.x, s.y);
       }
@@ -389,13 +387,13 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
   // ---- the token that follows
   if (state_out) {
     // all of the node's children are out: mark them in the CTA's run
-    const int words = (kVerifyWarps * per_warp + 31) / 32;
-    for (int i = tid; i < words; i += kVerifyThreads) out[i] = 0;
+    const int words = (kWarps * per_warp + 31) / 32;
+    for (int i = tid; i < words; i += kThreads) out[i] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kVerifyThreads) {
+    for (int i = tid; i < n; i += kThreads) {
       const int64_t at = (int64_t)token[i] - cta_begin;
       if (parent[i] == state_node && token[i] >= 0 && at >= 0 &&
-          at < (int64_t)kVerifyWarps * per_warp)
+          at < (int64_t)kWarps * per_warp)
         atomicOr(&out[at >> 5], 1u << (at & 31));
     }
     __syncthreads();
@@ -412,7 +410,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
   }
   const int parity = (round - 1) & 1;
   if (rank == 0) {
-    for (int i = tid; i < n; i += kVerifyThreads) a.path[q0 + i] = i < state_len ? path[i] : -1;
+    for (int i = tid; i < n; i += kThreads) a.path[q0 + i] = i < state_len ? path[i] : -1;
     if (tid == 0) a.path_len[b] = state_len;
     if (tid == 0 && !row_left) a.next[b] = -1;
   }
@@ -431,9 +429,9 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
     t.lo = fmaf(chance, row.hi, -t.hi) + chance * row.lo;
     Sum2 sum, at;
     int who = -1;
-    for (int k0 = 0; k0 < ranks * kVerifyWarps; k0 += 32) {
+    for (int k0 = 0; k0 < ranks * kWarps; k0 += 32) {
       Sum2 mine;
-      if (k0 + lane < ranks * kVerifyWarps) {
+      if (k0 + lane < ranks * kWarps) {
         mine.hi = sums_of[parity][k0 + lane].x;
         mine.lo = sums_of[parity][k0 + lane].y;
       }
@@ -447,7 +445,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
       sum = of_lane(up_to, 31);
     }
     if (lane == 0) {
-      owner_warp = who - rank * kVerifyWarps;   // another CTA's: none of this one's
+      owner_warp = who - rank * kWarps;   // another CTA's: none of this one's
       owner_before = make_float2(at.hi, at.lo);
       threshold = make_float2(t.hi, t.lo);
     }
@@ -499,22 +497,23 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
   if (lane == 0) a.next[b] = answer;
 }
 
-template <typename T, bool kVec>
+template <typename T, bool kVec, int kThreads>
 cudaError_t launch_t(const VerifyArgs& a, cudaStream_t stream) {
-  auto kern = verify_tree_kernel<T, kVec>;
+  constexpr int kWarps = kThreads / 32;
+  auto kern = verify_tree_kernel<T, kVec, kThreads>;
   // as many CTAs a sequence as the device holds at once, but none with less than a
   // tile or two a warp
   constexpr int kTile = 512 / (int)sizeof(T);
   int ranks = 1;
   while (ranks < kVerifyCluster &&
          (a.vocab > ranks * kVerifyRun ||   // the tokens' bits fit shared memory
-          (a.B * ranks < 4 * a.num_sms && a.vocab > 2 * ranks * kVerifyWarps * kTile)))
+          (a.B * ranks * kThreads < kVerifyResident * a.num_sms && a.vocab > 2 * ranks * kWarps * kTile)))
     ranks *= 2;
-  const int run = kVerifyWarps * (((a.vocab + ranks * kVerifyWarps - 1) / (ranks * kVerifyWarps) + kTile - 1) / kTile * kTile);
+  const int run = kWarps * (((a.vocab + ranks * kWarps - 1) / (ranks * kWarps) + kTile - 1) / kTile * kTile);
   const size_t smem = a.draft ? 0 : (size_t)(run + 31) / 32 * 4;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.B * ranks));
-  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -534,7 +533,12 @@ cudaError_t launch_rows(const VerifyArgs& a, cudaStream_t stream) {
   const bool vec = (reinterpret_cast<uintptr_t>(a.target) & 15u) == 0 && a.target_stride % N == 0 &&
                    (!a.draft || ((reinterpret_cast<uintptr_t>(a.draft) & 15u) == 0 &&
                                  a.draft_stride % N == 0));
-  return vec ? launch_t<T, true>(a, stream) : launch_t<T, false>(a, stream);
+  // Larger CTAs while all of a full cluster's are on the device at once, else smaller
+  // ones, of which they are (64 x 1 node over 128256 tokens: 16.5, 12.6 us; 32 x 1..48
+  // chosen nodes over 99991: 11.7, 13.6; 64 x 16 drawn nodes over 128256: 52 to 61, 54 to 65).
+  if (a.B * kVerifyCluster * 512 <= kVerifyResident * a.num_sms)
+    return vec ? launch_t<T, true, 512>(a, stream) : launch_t<T, false, 512>(a, stream);
+  return vec ? launch_t<T, true, 256>(a, stream) : launch_t<T, false, 256>(a, stream);
 }
 
 }  // namespace

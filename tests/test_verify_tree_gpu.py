@@ -120,6 +120,14 @@ def test_shapes_of_trees(kind, drafted):
     c.go()
 
 
+def test_no_rows_at_all():
+    starts, sample = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(3, device="cuda")
+    count, following = torch.full((3,), -7, device="cuda").int(), torch.full((3,), -7, device="cuda").int()
+    P.photon_verify_tree(None, 0, None, 0, 100, W.DTYPE_F32, None, None, starts, None, sample, 3, 0, 5,
+                         None, count, following)
+    assert count.tolist() == [0] * 3 and following.tolist() == [-1] * 3
+
+
 def test_all_accepted_and_none():
     c = Case([6, 6], 500, kind="chain", apart=0.0)     # p == q: every child is accepted
     assert c.go() == 10
