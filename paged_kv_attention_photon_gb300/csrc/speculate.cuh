@@ -52,7 +52,9 @@ constexpr int kTreeRows = 256;
 // Most CTAs of the attention grid: each has kTreeRows rows of partials in the
 // workspace, whose size so does not depend on the device.
 constexpr int kTreeMaxCtas = 160;
-// Keys of a chunk, and the chunks that beginning and ending a pair counts for.
+// Keys of a chunk, and the chunks that beginning and ending a pair counts for.  With 1,
+// 2, 3, 4: a batch-256 mix 204, 193, 200, 205 us, 64 long contexts 93.9, 94.6, 95.6,
+// 97.7, 32 contexts x 256 rows 59.8, 57.9, 57.9, 60.4.
 constexpr int kTreeChunk = 128;
 constexpr int kTreePairCost = 2;
 
