@@ -1001,7 +1001,7 @@ TreeLayout tree_layout(const photon_paged_shape_t* s, int32_t num_tokens) {
   TreeLayout w{};
   const size_t rows = (size_t)num_tokens * s->num_q_heads +
                       (size_t)photon::kTreeMaxCtas * photon::kTreeRows;
-  w.off_ml = round_up((size_t)photon::kTreeMaxCtas * sizeof(int4), 256);
+  w.off_ml = round_up((size_t)photon::kTreeMaxCtas * 2 * sizeof(int4), 256);
   w.off_o = w.off_ml + round_up(rows * sizeof(float2), 256);
   w.total = w.off_o + round_up(rows * s->head_dim * sizeof(float), 256);
   return w;

@@ -38,8 +38,8 @@ struct TreeArgs {
   const int32_t* query_start;   // [B + 1]
   const int32_t* parents;       // [num_tokens]
   void* out;
-  int4* ws_split;  // [CTA] the pair that its run begins in the midst of: sequence, KV head
-                   // and row group, first and last CTA (-1: none)
+  int4* ws_split;  // [CTA][2] the pair that its run begins in the midst of: first row of q,
+                   // nodes, KV head, row group; first and last CTA (last -1: none)
   float2* ws_ml;   // [row] maximum (unscaled) and sum of weights of a partial ..
   float* ws_o;     // [row][D] .. and its weighted V sum
   uint32_t* err;

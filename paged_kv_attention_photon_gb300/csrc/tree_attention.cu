@@ -603,8 +603,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int trees = 0, masked_b = -1;   // masks asked for so far, and the last one's sequence
       bool told = false;
       // whose partials lie with this CTA: the pair that its run begins in the midst of
-      auto tell = [&](int4 v) {
-        if (!told && lane == 0) a.ws_split[blockIdx.x] = v;
+      auto tell = [&](const Item& i, int t_first, int t_last) {
+        if (!told && lane == 0) {
+          a.ws_split[2 * blockIdx.x] = make_int4(i.q0, i.n, i.kvh, i.g);
+          a.ws_split[2 * blockIdx.x + 1] = make_int4(t_first, t_last, 0, 0);
+        }
         told = true;
       };
       auto publish = [&](const Item& i) {
@@ -621,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++m;
       };
+      it = Item{};
       int u = 0;   // units before sequence b0 + ..
       for (int b0 = 0; ok && b0 < a.B && u < u1; b0 += 32) {
         const int mine = units_of(a, seq_of(a, b0 + lane), G);
@@ -649,8 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.c1 <= it.c0) continue;
             const int t_first = at / per, t_last = (at + chunks - 1) / per;
             it.place = t_first == t_last ? 0 : (int)blockIdx.x == t_first ? 1 : 2;
-            tell(it.place == 2 ? make_int4(it.b, it.kvh * groups + it.g, t_first, t_last)
-                               : make_int4(0, 0, 0, -1));
+            tell(it, t_first, it.place == 2 ? t_last : -1);
             const bool tree = it.c1 * kKeys > it.ctx - it.n, fresh = tree && it.b != masked_b;
             trees += fresh;
             it.tree = tree ? trees - 1 : -1;
@@ -660,8 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         u += __shfl_sync(0xffffffffu, sum, 31);
       }
-      tell(make_int4(0, 0, 0, -1));
       it.n = 0;
+      tell(it, 0, -1);
       if (ok) publish(it);
     } else if (warp == 15) {
       // ================================================================ the nodes' ancestors
@@ -875,65 +878,105 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
 }
 
-// out = sum_p w_p o_p / sum_p w_p l_p with w_p = 2^(scale (m_p - max m)) over the
-// partials of a row.  A pair's partials lie with consecutive CTAs, and the second one's
-// index names the pair here; a CTA takes `slice` of its rows, D / 4 lanes a row.
-constexpr int kMergeThreads = 256, kMergeSlices = 8;
+// The weighted sums of some partials of a row: l, and four elements of o, against the
+// largest of their maxima m; w_p = 2^(scale (m_p - m)).
+struct Joined {
+  float m = kNoMax, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void raise(float to, float qmul) {
+    const float r = softmax_exp2((m - to) * qmul);
+    m = to;
+    l *= r;
+    o.x *= r, o.y *= r, o.z *= r, o.w *= r;
+  }
+  __device__ __forceinline__ void add(float2 ml, float4 v, float qmul) {   // ml.x <= m
+    const float w = softmax_exp2((ml.x - m) * qmul);
+    l = fmaf(w, ml.y, l);
+    o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+  }
+};
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a, int slice) {
-  constexpr int kLanes = D / 4, kAtOnce = kMergeThreads / kLanes, kAhead = 4;
+// out = sum_p w_p o_p / sum_p w_p l_p over the partials of a row.  A pair's partials lie
+// with consecutive CTAs, and the second one's index names the pair here.  A CTA takes a
+// slice of its rows; D / 4 lanes a row and each of kSplit parts of its partials, all
+// asked for at once: one round trip for up to 16 partials (kSplit > 1), or for two rows'
+// 4 (kSplit == 1).
+constexpr int kMergeThreads = 256;
+template <int D, int kSplit>
+constexpr int kMergeRows = kMergeThreads / (D / 4 * kSplit) * (kSplit == 1 ? 2 : 1);
+
+template <typename T, int D, int kSplit>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a) {
+  constexpr int kLanes = D / 4, kAtOnce = kMergeThreads / (kLanes * kSplit);
+  constexpr int kAhead = kSplit == 1 ? 4 : 16 / kSplit;
+  constexpr int kInFlight = kSplit == 1 ? 2 : 1;
+  __shared__ Joined parts_of[kSplit > 1 ? kMergeThreads : 1];
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int4 split = a.ws_split[blockIdx.y + 1];
-  if (split.w < 0 || split.z != (int)blockIdx.y) return;   // nothing, or another one's pair
-  const int lane = threadIdx.x % kLanes;
+  const int4 at = a.ws_split[2 * (blockIdx.y + 1)], of = a.ws_split[2 * (blockIdx.y + 1) + 1];
+  if (of.y < 0 || of.x != (int)blockIdx.y) return;   // nothing, or another one's pair
+  const int lane = threadIdx.x % kLanes, part = threadIdx.x / kLanes % kSplit;
   const int G = a.Hq / a.Hkv, g2 = __ffs(G) - 1;
-  const int b = split.x;
-  const Seq s = seq_of(a, b);
-  const int groups = groups_of(s.n, G), kvh = split.y / groups, g = split.y - kvh * groups;
-  const int row0 = g * kTreeRows + blockIdx.x * slice, rows = min(s.n << g2, (g + 1) * kTreeRows);
-  const int2 pr = make_int2(split.z, split.w);
+  const int q0 = at.x, n = at.y, kvh = at.z, g = at.w, parts = of.y - of.x + 1;
+  const int rows = min(n << g2, (g + 1) * kTreeRows);
+  const int row0 = g * kTreeRows + (int)blockIdx.x * (kAtOnce * kInFlight) + threadIdx.x / (kLanes * kSplit);
+  if (g * kTreeRows + (int)blockIdx.x * (kAtOnce * kInFlight) >= rows) return;
   const float qmul = fmaxf(fabsf(a.qscale), 1e-37f);
-  T* out = static_cast<T*>(a.out);
-  for (int r = row0 + threadIdx.x / kLanes; r < min(rows, row0 + slice); r += kAtOnce) {
-    const int64_t head = (int64_t)(s.q0 + (r >> g2)) * a.Hq + kvh * G + (r & (G - 1));
-    // the first partial lies with the row, the others with their CTAs
-    const int64_t later = (int64_t)a.num_tokens * a.Hq + (int64_t)pr.x * kTreeRows + (r - g * kTreeRows);
-    const int parts = pr.y - pr.x + 1;
-    float M = kNoMax, L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < parts; p0 += kAhead) {
-      float4 v[kAhead];
-      float2 ml[kAhead];
+  Joined sum[kInFlight];
+  for (int p0 = part; p0 < parts; p0 += kSplit * kAhead) {
+    float4 v[kInFlight][kAhead];
+    float2 ml[kInFlight][kAhead];
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) {
+      const int r = min(row0 + k * kAtOnce, rows - 1);
+      // the first partial lies with the row, the others with their CTAs
+      const int64_t head = (int64_t)(q0 + (r >> g2)) * a.Hq + kvh * G + (r & (G - 1));
+      const int64_t later = (int64_t)a.num_tokens * a.Hq + (int64_t)of.x * kTreeRows + (r - g * kTreeRows);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int p = min(p0 + i, parts - 1);
-        const int64_t at = p == 0 ? head : later + (int64_t)p * kTreeRows;
-        ml[i] = a.ws_ml[at];
-        if (p0 + i >= parts) ml[i].y = 0.f;
-        v[i] = reinterpret_cast<const float4*>(a.ws_o + at * D)[lane];
-      }
-      float top = M;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);
-      const float r0 = softmax_exp2((M - top) * qmul);
-      M = top;
-      L *= r0;
-      O.x *= r0, O.y *= r0, O.z *= r0, O.w *= r0;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (ml[i].y == 0.f) continue;   // no key of that part, or not a part
-        const float w = softmax_exp2((ml[i].x - M) * qmul);
-        L = fmaf(w, ml[i].y, L);
-        O.x = fmaf(w, v[i].x, O.x), O.y = fmaf(w, v[i].y, O.y);
-        O.z = fmaf(w, v[i].z, O.z), O.w = fmaf(w, v[i].w, O.w);
+        const int p = p0 + i * kSplit;
+        ml[k][i] = make_float2(kNoMax, 0.f);
+        v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p < parts) {
+          const int64_t row = p == 0 ? head : later + (int64_t)p * kTreeRows;
+          ml[k][i] = a.ws_ml[row];
+          v[k][i] = reinterpret_cast<const float4*>(a.ws_o + row * D)[lane];
+        }
       }
     }
-    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-    reinterpret_cast<uint2*>(out + head * D)[lane] =
-        make_uint2(Mma<T>::pack(O.x * inv, O.y * inv), Mma<T>::pack(O.z * inv, O.w * inv));
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) {
+      float top = sum[k].m;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (ml[k][i].y != 0.f) top = fmaxf(top, ml[k][i].x);
+      sum[k].raise(top, qmul);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (ml[k][i].y != 0.f) sum[k].add(ml[k][i], v[k][i], qmul);   // else no key of that part, or none
+    }
+  }
+  if constexpr (kSplit > 1) {
+    parts_of[threadIdx.x] = sum[0];
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int i = 1; i < kSplit; ++i) {
+      const Joined x = parts_of[threadIdx.x + i * kLanes];
+      if (x.l == 0.f) continue;
+      sum[0].raise(fmaxf(sum[0].m, x.m), qmul);
+      sum[0].add(make_float2(x.m, x.l), x.o, qmul);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kInFlight; ++k) {
+    const int r = row0 + k * kAtOnce;
+    if (r >= rows) continue;
+    const float l = sum[k].l, inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const int64_t head = (int64_t)(q0 + (r >> g2)) * a.Hq + kvh * G + (r & (G - 1));
+    const float4 o = sum[k].o;
+    reinterpret_cast<uint2*>(static_cast<T*>(a.out) + head * D)[lane] =
+        make_uint2(Mma<T>::pack(o.x * inv, o.y * inv), Mma<T>::pack(o.z * inv, o.w * inv));
   }
 }
 
@@ -967,11 +1010,13 @@ cudaError_t launch_t(const TreeArgs& a, cudaStream_t stream) {
   e = launch_pdl(kern, dim3(grid), dim3(kThreads), C::kSmem, stream, tq, tk, tv, a);
   if (e != cudaSuccess) return e;
   if (grid == 1) return cudaSuccess;
-  // the pairs' rows in up to kMergeSlices parts: as many CTAs as the device holds at once
+  // With fewer pairs than CTAs each pair has several partials; with more, two or so.
   const int rows = std::min(a.max_query_len * (int)G, kTreeRows);
-  const int slice = std::max(kMergeThreads / (D / 4), (rows + kMergeSlices - 1) / kMergeSlices);
-  return launch_pdl(tree_merge_kernel<T, D>, dim3((rows + slice - 1) / slice, grid - 1),
-                    dim3(kMergeThreads), 0, stream, a, slice);
+  auto slices = [&](int each) { return dim3((rows + each - 1) / each, grid - 1); };
+  if ((int64_t)a.B * a.Hkv * groups_of(a.max_query_len, (int)G) < grid)
+    return launch_pdl(tree_merge_kernel<T, D, 256 / D>, slices(kMergeRows<D, 256 / D>),
+                      dim3(kMergeThreads), 0, stream, a);
+  return launch_pdl(tree_merge_kernel<T, D, 1>, slices(kMergeRows<D, 1>), dim3(kMergeThreads), 0, stream, a);
 }
 
 }  // namespace
