@@ -49,13 +49,13 @@
 // the largest.
 //
 // Measured (event times of whole calls): 64 contexts of 128 .. 8192 tokens x 16 nodes,
-// 16 q / 8 kv heads x 128, fp16: 95 us = 5.5 TB/s, 82 % of the measured copy rate; a
-// batch-256 mix x 1 .. 32 nodes, 32 / 8 x 64, bf16: 193 us, 80 %; 4 short contexts 12.1
+// 16 q / 8 kv heads x 128, fp16: 94 us = 5.6 TB/s, 83 % of the measured copy rate; a
+// batch-256 mix x 1 .. 32 nodes, 32 / 8 x 64, bf16: 192 us, 80 %; 4 short contexts 11.6
 // us.  In long contexts a chunk takes the time of its bytes: 1.51 us for 64 KB (d = 128,
 // up to 128 rows), 0.75 us for 32 KB (d = 64, up to 64 rows; 0.80 with 128): 6.5 TB/s over
 // all SMs.  With 256 rows at d = 64 it takes 1.38 us, the softmax's latency on two warps
-// a scheduler: 32 contexts x 64 nodes 58 us.  A call begins and ends in 8 us (launch,
-// lengths, table, first data, the join's launch); an item of its own costs 1.4 us (one
+// a scheduler: 32 contexts x 64 nodes 56 us.  A call begins and ends in 8 us (launch,
+// lengths, table, first data, the join's launch), 11 where pairs are split; an item of its own costs 1.4 us (one
 // tile's) to 2 or 3.  On the way there (64 contexts / the mix / 4 short ones / 32 x 64): the
 // first right version 101 / 230 / 18.6 / 64 us; block ids a chunk ahead and not four 101
 // / 215 / 12.9 / 59; items of up to 4 chunks on both tiles, too, - / 229 / 12.3 / 60.
