@@ -170,9 +170,11 @@ __device__ __forceinline__ uint4 load_chunk(const T* row, int e, int vocab) {
   return c.all;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Stores into the same place of another CTA's shared memory.
 __device__ __forceinline__ void store_peer(float2* p, int rank, float2 v) {
@@ -210,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
     }
     return;
   }
+  cluster_arrive();   // this CTA has begun: its shared memory may be written to
   const T* target = static_cast<const T*>(a.target) + (int64_t)q0 * a.target_stride;
   const T* drafts = a.draft ? static_cast<const T*>(a.draft) + (int64_t)q0 * a.draft_stride : nullptr;
   const int V = a.vocab;
@@ -239,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
     draft[i] = q;
   }
   if (tid == 0) path[0] = 0;
+  cluster_wait();   // and so have the others
   __syncthreads();
   if (!drafts) {
     // a sibling before it has the same token: nothing is left for it
@@ -299,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
     const int parity = round++ & 1;
     // every warp's sum to every CTA of the cluster
     if (lane < ranks) store_peer(&sums_of[parity][rank * kWarps + warp], lane, make_float2(sum.hi, sum.lo));
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();
     if (warp == 0) {
       Sum2 all;
       for (int k = lane; k < ranks * kWarps; k += 32) {
