@@ -45,6 +45,10 @@ struct TreeArgs {
   uint32_t* err;
   float qscale;    // scale * log2(e)
   int B, Hq, Hkv, D, NB, MBS, num_tokens, max_query_len, dtype, num_sms;
+  // set by launch_tree_attention: whether pairs are split over CTAs; up to how many chunks
+  // one tile takes an item alone
+  bool split;
+  int one_tile;
 };
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t stream);
 // Query rows of a group: what one CTA holds at a time.

@@ -19,7 +19,7 @@
 // memory.  With more than 128 rows each tile has its own rows and sees every chunk;
 // with up to 128 both tiles have the same rows and take every other chunk, so that
 // one tile's softmax runs beside the other's products, and their sums meet at the end
-// through shared memory, or, up to kWhole chunks, one tile takes the item and the other
+// through shared memory, or, up to kOneTile chunks, one tile takes the item and the other
 // the next one.  S, softmax and P V go by halves of 64 keys; P of a half lies over its S
 // as 16-bit pairs.  16 warps in fixed roles:
 //   warps 0-3, 4-7  softmax of tile 0, 1: thread r owns TMEM lane r
@@ -50,15 +50,16 @@
 //
 // Measured (event times of whole calls): 64 contexts of 128 .. 8192 tokens x 16 nodes,
 // 16 q / 8 kv heads x 128, fp16: 94 us = 5.6 TB/s, 83 % of the measured copy rate; a
-// batch-256 mix x 1 .. 32 nodes, 32 / 8 x 64, bf16: 192 us, 80 %; 4 short contexts 11.6
+// batch-256 mix x 1 .. 32 nodes, 32 / 8 x 64, bf16: 192 us, 80 %; 4 short contexts 11.1
 // us.  In long contexts a chunk takes the time of its bytes: 1.51 us for 64 KB (d = 128,
 // up to 128 rows), 0.75 us for 32 KB (d = 64, up to 64 rows; 0.80 with 128): 6.5 TB/s over
 // all SMs.  With 256 rows at d = 64 it takes 1.38 us, the softmax's latency on two warps
-// a scheduler: 32 contexts x 64 nodes 56 us.  A call begins and ends in 8 us (launch,
-// lengths, table, first data, the join's launch), 11 where pairs are split; an item of its own costs 1.4 us (one
-// tile's) to 2 or 3.  On the way there (64 contexts / the mix / 4 short ones / 32 x 64): the
-// first right version 101 / 230 / 18.6 / 64 us; block ids a chunk ahead and not four 101
-// / 215 / 12.9 / 59; items of up to 4 chunks on both tiles, too, - / 229 / 12.3 / 60.
+// a scheduler: 32 contexts x 64 nodes 56 us.  A call begins and ends in 6.7 us (launch,
+// lengths, table, first data), 7.5 with the join's launch, 11 where pairs are split; an
+// item of its own costs 1.4 us (one tile's) to 2 or 3.  On the way there (64 contexts /
+// the mix / 4 short ones / 32 x 64): the first right version 101 / 230 / 18.6 / 64 us; block
+// ids a chunk ahead and not four 101 / 215 / 12.9 / 59; items of up to 4 chunks on both
+// tiles, too, - / 229 / 12.3 / 60.
 // Measured and left out: stages of 64 keys, twice as many (135 / 316 / 13.2 / 63); up to
 // 64 rows in the upper lanes for tile 1, so that the two tiles' softmax warps are on
 // different quarters of the SM (94 / 224 / 12.5 / 60); Q in both places for that (96 / 221).
@@ -106,10 +107,18 @@ constexpr float kFar = 8388608.f;
 constexpr int kItems = 4;               // items found ahead
 constexpr int kRoles = 15;              // warps that an item is told
 constexpr int kMaskWords = kTreeNodes / 32, kMaskStride = kMaskWords + 1;
-// Items of up to so many chunks (and 128 rows) go to one tile, the next one to the other.
-// With 1, 2, 4, 6, 12: a batch-256 mix 210, 200, 193, 194, 194 us, 152 x 1024 tokens (32
-// q, 8 kv heads x 64, 16 nodes) 73.7, 73.6, 73.9, 73.6, 78.7.
-constexpr int kWhole = 4;
+// Items of up to so many chunks (and 128 rows) go to one tile, the next one to the other,
+// where a CTA has several (a.one_tile is 1 otherwise).  With 1, 2, 4, 6, 12: a batch-256
+// mix 210, 200, 193, 194, 194 us, 152 x 1024 tokens (32 q, 8 kv heads x 64, 16 nodes) 73.7,
+// 73.6, 73.9, 73.6, 78.7; 4 short contexts, an item a CTA, 11.7, 12.1, 12.2, 12.1, 12.1.
+constexpr int kOneTile = 4;
+// Where no context can have more than kWholePairs chunks, and whole pairs leave a CTA no
+// more than kWholeIdle2 / 2 of their time unused on average, pairs are not split, and no
+// second kernel joins them.  Whole and split: 4 contexts of 300 tokens x 16 nodes (16 q, 8
+// kv heads x 128) 9.5, 11.7 us; 16 of 1000 15.6, 22.0; 64 of 1000 (32 q, 8 kv heads x 64) 36.8,
+// 40.5; but 24 of 1000 (192 pairs, a second round for 40 of them) 28.1, 25.9, 1 of 1000 13.8,
+// 10.8, and 40 of 2000 72.8, 63.6.
+constexpr int kWholePairs = 8, kWholeIdle2 = 11;
 constexpr int kGoneRing = 8;            // more than the chunks between a copy and its softmax
 
 template <int D>
@@ -168,19 +177,20 @@ struct Item {
   int c1, q0, n, ctx;
   int place;   // where the sums go: 0 out, 1 the rows' own partials, 2 the CTA's
   int tree;    // which of the trees' masks it needs, counted up; -1: holds no key of a tree
+  int one_tile;
   __device__ __forceinline__ int rows(int g2) const { return min(kTreeRows, (n << g2) - g * kTreeRows); }
   __device__ __forceinline__ int chunks() const { return c1 - c0; }
   // both tiles have rows of their own
   __device__ __forceinline__ bool apart(int g2) const { return rows(g2) > kRows; }
   // both tiles have the same rows, and every other chunk each
-  __device__ __forceinline__ bool shared(int g2) const { return !apart(g2) && chunks() > kWhole; }
+  __device__ __forceinline__ bool shared(int g2) const { return !apart(g2) && chunks() > one_tile; }
   // the place of tile t's Q: items of one tile's rows take the two places in turn
   __device__ __forceinline__ int place_of(int g2, uint32_t m, int t) const {
     return apart(g2) ? t : (int)(m & 1);
   }
   // whether tile t takes the lc-th chunk of the CTA's m-th item
   __device__ __forceinline__ bool takes(int g2, uint32_t m, int lc, int t) const {
-    return apart(g2) || (((int)m + (chunks() > kWhole ? lc : 0)) & 1) == t;
+    return apart(g2) || (((int)m + (chunks() > one_tile ? lc : 0)) & 1) == t;
   }
 };
 
@@ -271,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int4 x = items[slot][0], y = items[slot][1];
     to.place = items[slot][2].x;
     to.tree = items[slot][2].y;
+    to.one_tile = a.one_tile;
     __syncwarp();
     if (lane == 0) mbar_arrive(&item_free[slot]);
     to.b = x.x, to.kvh = x.y, to.g = x.z, to.c0 = x.w;
@@ -594,9 +605,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 14) {
       // ================================================================ items
       // where the CTA's run lies on the line
+      const Seq first = seq_of(a, lane);   // most batches need no more loads
+      auto seqs = [&](int b0) { return b0 == 0 ? first : seq_of(a, b0 + lane); };
       int64_t total = 0;
       for (int b0 = 0; b0 < a.B; b0 += 32)
-        total += __reduce_add_sync(0xffffffffu, (unsigned)units_of(a, seq_of(a, b0 + lane), G));
+        total += __reduce_add_sync(0xffffffffu, (unsigned)units_of(a, seqs(b0), G));
       const int per = (int)((total + gridDim.x - 1) / gridDim.x);
       const int u0 = (int)min(total, (int64_t)blockIdx.x * per), u1 = (int)min(total, (int64_t)u0 + per);
       uint32_t m = 0;
@@ -627,7 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       it = Item{};
       int u = 0;   // units before sequence b0 + ..
       for (int b0 = 0; ok && b0 < a.B && u < u1; b0 += 32) {
-        const int mine = units_of(a, seq_of(a, b0 + lane), G);
+        const Seq here = seqs(b0);
+        const int mine = units_of(a, here, G);
         int sum = mine;   // inclusive prefix
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -640,18 +654,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           in &= in - 1;
           const int start = u + __shfl_sync(0xffffffffu, sum - mine, k);
           it.b = b0 + k;
-          const Seq s = seq_of(a, it.b);
-          it.q0 = s.q0, it.n = s.n, it.ctx = s.ctx;
-          const int chunks = chunks_of(s.ctx), groups = groups_of(s.n, G), each = chunks + kTreePairCost;
+          it.q0 = __shfl_sync(0xffffffffu, here.q0, k);
+          it.n = __shfl_sync(0xffffffffu, here.n, k);
+          it.ctx = __shfl_sync(0xffffffffu, here.ctx, k);
+          const int chunks = chunks_of(it.ctx), groups = groups_of(it.n, G), each = chunks + kTreePairCost;
           for (int p = max(0, u0 - start) / each; ok && p < a.Hkv * groups; ++p) {
             const int at = start + p * each + kTreePairCost;   // the pair's first chunk on the line
             if (at - kTreePairCost >= u1) break;
             it.kvh = p / groups;
             it.g = p - it.kvh * groups;
-            it.c0 = max(0, u0 - at);
-            it.c1 = min(chunks, u1 - at);
+            int t_first = at / per, t_last = (at + chunks - 1) / per;
+            if (a.split) {
+              it.c0 = max(0, u0 - at);
+              it.c1 = min(chunks, u1 - at);
+            } else {   // all of it, where it begins
+              it.c0 = 0;
+              it.c1 = at - kTreePairCost >= u0 ? chunks : 0;
+              t_first = t_last = blockIdx.x;
+            }
             if (it.c1 <= it.c0) continue;
-            const int t_first = at / per, t_last = (at + chunks - 1) / per;
             it.place = t_first == t_last ? 0 : (int)blockIdx.x == t_first ? 1 : 2;
             tell(it, t_first, it.place == 2 ? t_last : -1);
             const bool tree = it.c1 * kKeys > it.ctx - it.n, fresh = tree && it.b != masked_b;
@@ -981,7 +1002,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
 }
 
 template <typename T, int D>
-cudaError_t launch_t(const TreeArgs& a, cudaStream_t stream) {
+cudaError_t launch_t(TreeArgs a, cudaStream_t stream) {
   using C = Cfg<D>;
   auto kern = tree_attention_kernel<T, D>;
   static std::atomic<bool> configured[64];
@@ -1005,15 +1026,19 @@ cudaError_t launch_t(const TreeArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if ((e = make_pool_map(&tk, a.k_cache, a.dtype, a.NB, a.Hkv, a.D)) != cudaSuccess) return e;
   if ((e = make_pool_map(&tv, a.v_cache, a.dtype, a.NB, a.Hkv, a.D)) != cudaSuccess) return e;
-  const int64_t most = (int64_t)a.B * a.Hkv * groups_of(a.max_query_len, (int)G) * ((a.MBS * kBlockSize + kKeys - 1) / kKeys + kTreePairCost);
-  const int grid = (int)std::min<int64_t>(std::min(a.num_sms, kTreeMaxCtas), most);
+  const int64_t pairs = (int64_t)a.B * a.Hkv * groups_of(a.max_query_len, (int)G);
+  const int chunks = (a.MBS * kBlockSize + kKeys - 1) / kKeys;   // of the longest context there can be
+  const int grid = (int)std::min<int64_t>(std::min(a.num_sms, kTreeMaxCtas), pairs * (chunks + kTreePairCost));
+  const int64_t spare = (pairs + grid - 1) / grid * grid - pairs;   // places that whole pairs leave empty
+  a.split = grid > 1 && (chunks > kWholePairs || 2 * chunks * spare > kWholeIdle2 * grid);
+  a.one_tile = pairs > grid ? kOneTile : 1;
   e = launch_pdl(kern, dim3(grid), dim3(kThreads), C::kSmem, stream, tq, tk, tv, a);
   if (e != cudaSuccess) return e;
-  if (grid == 1) return cudaSuccess;
+  if (!a.split) return cudaSuccess;
   // With fewer pairs than CTAs each pair has several partials; with more, two or so.
   const int rows = std::min(a.max_query_len * (int)G, kTreeRows);
   auto slices = [&](int each) { return dim3((rows + each - 1) / each, grid - 1); };
-  if ((int64_t)a.B * a.Hkv * groups_of(a.max_query_len, (int)G) < grid)
+  if (pairs < grid)
     return launch_pdl(tree_merge_kernel<T, D, 256 / D>, slices(kMergeRows<D, 256 / D>),
                       dim3(kMergeThreads), 0, stream, a);
   return launch_pdl(tree_merge_kernel<T, D, 1>, slices(kMergeRows<D, 1>), dim3(kMergeThreads), 0, stream, a);

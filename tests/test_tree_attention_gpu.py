@@ -139,6 +139,19 @@ def test_one_long_context_over_every_sm(dtype):
     c.ok()
 
 
+@pytest.mark.parametrize("seqs", [1, 3, 8, 19, 24, 40])
+@pytest.mark.parametrize("d,ctx,n", [(128, 60, 9), (128, 400, 20), (64, 900, 33), (128, 1020, 4), (64, 1300, 70)])
+def test_pairs_whole_and_split(seqs, d, ctx, n):
+    """Fewer and more pairs than CTAs, contexts of 1 to 11 chunks: whole pairs, pairs over two
+    CTAs, pairs over several, one and two rounds."""
+    rng = np.random.default_rng(seqs)
+    c = Case([(int(rng.integers(0, ctx + 1)), int(rng.integers(1, n + 1))) for _ in range(seqs - 1)] +
+             [(ctx, n)], 16, 8, d, W.DTYPE_F16)
+    c.run()
+    c.check()
+    c.ok()
+
+
 def test_many_short_sequences_and_empty_ones():
     rng = np.random.default_rng(3)
     seqs = [(int(rng.integers(0, 90)), int(rng.integers(0, 20))) for _ in range(400)]
