@@ -516,14 +516,20 @@ template <typename T, bool kVec, int kThreads>
 cudaError_t launch_t(const VerifyArgs& a, cudaStream_t stream) {
   constexpr int kWarps = kThreads / 32;
   auto kern = verify_tree_kernel<T, kVec, kThreads>;
-  // as many CTAs a sequence as the device holds at once, but none with less than a
-  // tile or two a warp
+  // CTAs a sequence: as many as are all on the device at once (a little less than its
+  // places, as a cluster's lie close together), or, where that is one or two, in two turns;
+  // none with less than a tile a warp, and so many at least that the tokens' bits fit
+  // shared memory.  One turn and two, 128256 chosen and 50000 drawn tokens: 80 sequences
+  // 16.3, 14.7 and 18.2, 18.7 us; 128: 21.1, 20.0 and 21.6, 23.0; 160: 28.4, 25.2 and 28.5,
+  // 28.1; 200: 48.7, 37.8 and 34.0, 29.3; 256: 54.2, 41.6 and 42.9, 39.1.
   constexpr int kTile = 512 / (int)sizeof(T);
-  int ranks = 1;
-  while (ranks < kVerifyCluster &&
-         (a.vocab > ranks * kVerifyRun ||   // the tokens' bits fit shared memory
-          (a.B * ranks * kThreads < kVerifyResident * a.num_sms && a.vocab > 2 * ranks * kWarps * kTile)))
-    ranks *= 2;
+  const int places = kVerifyResident / kThreads * a.num_sms * 97 / 100;
+  const int least = (a.vocab + kVerifyRun - 1) / kVerifyRun;
+  int ranks = places / a.B;
+  if (ranks < 3) ranks = 2 * places / a.B;
+  ranks = std::min(std::max(ranks, 1), kVerifyCluster);
+  while (ranks > 1 && a.vocab <= ranks * kWarps * kTile) --ranks;
+  ranks = std::max(ranks, least);
   const int run = kWarps * (((a.vocab + ranks * kWarps - 1) / (ranks * kWarps) + kTile - 1) / kTile * kTile);
   const size_t smem = a.draft ? 0 : (size_t)(run + 31) / 32 * 4;
   cudaLaunchConfig_t cfg = {};
@@ -549,9 +555,9 @@ cudaError_t launch_rows(const VerifyArgs& a, cudaStream_t stream) {
                    (!a.draft || ((reinterpret_cast<uintptr_t>(a.draft) & 15u) == 0 &&
                                  a.draft_stride % N == 0));
   // Larger CTAs while all of a full cluster's are on the device at once, else smaller
-  // ones, of which they are (64 x 1 node over 128256 tokens: 16.5, 12.6 us; 32 x 1..48
-  // chosen nodes over 99991: 11.7, 13.6; 64 x 16 drawn nodes over 128256: 52 to 61, 54 to 65).
-  if (a.B * kVerifyCluster * 512 <= kVerifyResident * a.num_sms)
+  // ones, of which they are (64 x 1 node over 128256 tokens: 16.5, 12.6 us; 38: 14.3, 12.5;
+  // 32 x 1..48 chosen nodes over 99991: 11.7, 13.6).
+  if ((int64_t)a.B * kVerifyCluster * 512 * 9 <= (int64_t)kVerifyResident * a.num_sms * 8)
     return vec ? launch_t<T, true, 512>(a, stream) : launch_t<T, false, 512>(a, stream);
   return vec ? launch_t<T, true, 256>(a, stream) : launch_t<T, false, 256>(a, stream);
 }

@@ -258,6 +258,10 @@ def test_large_vocabularies_and_batches():
     c.go()
     c = Case([2, 3], 300007, drafted=False, spread=1.0)
     c.go()
+    for B in (9, 34, 40, 90, 160, 210, 300):     # one to eight CTAs a sequence, in one turn or two
+        for drafted in (True, False):
+            c = Case([3] * B, 9001, drafted=drafted, seed=B)
+            c.go()
     c = Case([2] * 700, 1500, drafted=True)
     c.go()
     c = Case([3] * 700, 3000, drafted=False)
