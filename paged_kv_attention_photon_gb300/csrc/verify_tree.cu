@@ -24,13 +24,14 @@
 // warp in whose run the sampled sum is passed goes through it once more (L2).  So
 // a step is one launch, and even one sequence has several SMs to read with.
 //
-// Measured: 4 chains of 5 over 32000 tokens 7.0 us (5.1 for one node and 1000 tokens: the
+// Measured: 4 chains of 5 over 32000 tokens 7.4 us (5.1 for one node and 1000 tokens: the
 // launch, three dependent loads, the sums' way over the cluster and the search); 64 x 1
-// node over 128256 tokens 12.6 us; 32 x 1 .. 48 chosen nodes over 99991 11.7 us; 64 x 16
-// drawn nodes over 128256 54 to 65 us, which is up to seven passes one after another in the
-// slowest sequence, 5 to 7 us each: all sequences' first ones share the memory, the last
-// one's are its cluster's latency.  First version 12.8 / - / 18.9 / 111 us: A and B in
-// doubles for every thread, sums of single elements.  Measured and left out: clusters of
+// node over 128256 tokens 13.1 us, 64 chains of 16 24; 32 x 1 .. 48 chosen nodes over 99991
+// 11.8 us; 64 x 16 drawn nodes over 128256 55 to 65 us, which is up to seven passes one
+// after another in the slowest sequence, 5 to 7 us each: all sequences' first ones share
+// the memory, the last one's are its cluster's latency.  The first version, A and B in
+// doubles for every thread and sums of single elements, took 12.8 us for the 4 chains,
+// 18.9 for the chosen nodes and 111 for the drawn ones.  Measured and left out: clusters of
 // 16 (19.1 us for 64 x 1 node, 53 to 62), loads of four chunks ahead of their sums (12.8, 55
 // to 66), a pass's next loads before its sums (17.9, 67).
 #include <math.h>
