@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init_fence();
   }
   if (warp == 0) {
+    __syncwarp();   // with thread 0, which set the barriers up
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&tmem_slot)),
                  "r"(512)
@@ -397,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 qm = fabsf(qmul * mx) < kFar ? qmul : __uint_as_float(__float_as_uint(qmul) & 0x7f800000u);
                 base = __fmaf_rd(-qm, mx, kLift<T>);   // lifted no further, however large
               }
+              __syncwarp();
               if (begun) {
                 // the product of the half before still adds to O
                 ok = cta_wait(&o_done[t][1 - half], (half ? done : done - 1) & 1, gave_up);
@@ -471,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                ? (int64_t)a.num_tokens * a.Hq + (int64_t)blockIdx.x * kTreeRows + group_row
                                : head;
       for (int col = 0; ok && col < D; col += 32) {
+        __syncwarp();   // lanes without a row skip the stores below
         float o[32];
         tmem_ld32(t_o + col, o);
         if (both) {
@@ -770,6 +773,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int n_chunks = it.chunks(), place = it.place_of(g2, m, t);
           const uint64_t q_desc = q_desc0 + (uint64_t)((place * C::kQBytes) >> 4);
           ok = cta_wait(&q_full[place], (place ? q_uses1 : q_uses0) & 1, gave_up);
+          // An item with rows of both tiles hands both places back.  Without this wait a
+          // warp that had nothing to do in the item before could hand the other place back
+          // twice in one phase, while the other tile's products still read it.
+          if (ok && it.apart(g2)) ok = cta_wait(&q_full[1 - place], (place ? q_uses0 : q_uses1) & 1, gave_up);
           if (!ok) break;
           for (int lc = 0; lc < n_chunks; ++lc) {
             const uint32_t kc = chunk0 + lc;

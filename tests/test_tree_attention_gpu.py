@@ -176,6 +176,34 @@ def test_mixed_lengths_share_runs():
         assert np.array_equal(c.raw(), first)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ctx,lo,hi", [(60, 28, 40), (900, 28, 127)])
+def test_items_of_one_tile_and_of_two_in_turn(d, ctx, lo, hi):
+    """Each CTA has several items of few chunks: those of one tile's rows, which the other tile
+    passes over, before and after those of both tiles' rows.  Calls in a row, on either of two
+    batches."""
+    rng = np.random.default_rng(ctx + d)
+    both = []
+    for _ in range(2):
+        seqs = [(int(np.exp(rng.uniform(2, np.log(ctx)))), int(rng.integers(lo, hi + 1)))
+                for _ in range(48)]
+        both.append(Case(seqs, 24, 3, d, W.DTYPE_F16))
+    firsts = []
+    for c in both:
+        c.run()
+        c.ok()
+        c.check()
+        firsts.append(c.raw())
+    for _ in range(8):
+        for c in both:
+            c.out.fill_(-1)
+        for i in range(100):
+            both[i % 2].run()
+        for c, first in zip(both, firsts):
+            c.ok()
+            assert np.array_equal(c.raw(), first)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0, 1e-30])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_scales(scale, dtype):
