@@ -172,9 +172,11 @@ __device__ __forceinline__ uint4 load_chunk(const T* row, int e, int vocab) {
 }
 
 __device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();   // the aligned form is for warps whose lanes have met
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+  __syncwarp();   // the aligned form is for warps whose lanes have met
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Stores into the same place of another CTA's shared memory.
