@@ -403,13 +403,7 @@ __global__ void __launch_bounds__(TcCfg<T, D>::kThreads)
     }
     mbar_init_fence();
   }
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&tmem_slot)),
-                 "r"(NT * kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 0) tmem_alloc(&tmem_slot, NT * kTmemCols);
   for (int p = tid; p < kSuper * (D / 8); p += C::kThreads) {
     const int r = p / (D / 8), ch = p % (D / 8);
     const bool valid = r < rows_here;
@@ -718,10 +712,7 @@ __global__ void __launch_bounds__(TcCfg<T, D>::kThreads)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(NT * kTmemCols)
-                 : "memory");
+  if (warp == 0) tmem_dealloc(tmem, NT * kTmemCols);
 #ifdef PHOTON_PROBE
   if (tid == 0 && cta_lin < 4096) g_tc_cta[cta_lin][1] = global_timer_ns();
 #endif

@@ -307,13 +307,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     mbar_init_fence();
   }
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&tmem_slot)),
-                 "r"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 0) tmem_alloc(&tmem_slot, 512);
   if (tid == 32 * 8) {
     prefetch_tensor_map(&tm_q);
     prefetch_tensor_map(&tm_k);
@@ -351,7 +345,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     return to.n > 0;
   };
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPaSoftmaxRegs));
+    more_registers<kPaSoftmaxRegs>();
     // ================================================================ softmax rows
     const int t = warp >> 2;
     const int trow = (warp & 3) * 32 + lane;   // row inside the tile = TMEM lane
@@ -521,7 +515,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     if (lane == 0) bulk_store_wait_read<0>();   // before the CTA's shared memory goes
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaOtherRegs));
+    fewer_registers<kPaOtherRegs>();
     if (warp == 8) {
       // ================================================================ Q and K copies
       uint32_t kc = 0;                      // chunks so far
@@ -755,9 +749,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   if (!ok && lane == 0) raise_error(a.err, kErrTimeout);
   tc_fence_before();
   __syncthreads();
-  if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
-                 : "memory");
+  if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 template <typename T, int D>

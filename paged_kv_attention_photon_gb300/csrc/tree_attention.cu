@@ -252,14 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2 * kTiles; ++i) mbar_init(&drained[i], 1);
     mbar_init_fence();
   }
-  if (warp == 0) {
-    __syncwarp();   // with thread 0, which set the barriers up
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&tmem_slot)),
-                 "r"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 0) tmem_alloc(&tmem_slot, 512);
   if (tid == 32 * 8) {
     prefetch_tensor_map(&tm_q);
     prefetch_tensor_map(&tm_k);
@@ -291,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    more_registers<kSoftmaxRegs>();
     // ================================================================ softmax rows
     const int t = warp >> 2, w4 = warp & 3;
     const int trow = w4 * 32 + lane;           // row inside the tile = TMEM lane
@@ -521,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();   // O is read before the next item's products (p_full orders them)
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    fewer_registers<kOtherRegs>();
     if (warp == 8 || warp == 9) {
       // ================================================================ copies
       // warp 8: Q and K, warp 9: V.  Lane i < 8 copies block i of a chunk.
@@ -901,9 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!ok && lane == 0) raise_error(a.err, kErrTimeout);
   tc_fence_before();
   __syncthreads();
-  if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
-                 : "memory");
+  if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 // The weighted sums of some partials of a row: l, and four elements of o, against the
