@@ -119,7 +119,12 @@ constexpr int kOneTile = 4;
 // 40.5; but 24 of 1000 (192 pairs, a second round for 40 of them) 28.1, 25.9, 1 of 1000 13.8,
 // 10.8, and 40 of 2000 72.8, 63.6.
 constexpr int kWholePairs = 8, kWholeIdle2 = 11;
-constexpr int kGoneRing = 8;            // more than the chunks between a copy and its softmax
+// Chunks whose missing blocks are remembered.  Softmax reads a chunk's entry when its S
+// is done, which is not when its stage is handed back: until the softmax has gone on, its
+// tile's issuer still passes over what the other tile takes, kOneTile + 1 chunks at most
+// (the last one of an item on both tiles, and an item on one), and hands back those
+// stages too.  So copies run ahead of the softmax by up to that and the stages.
+constexpr int kGoneRing = 16;
 
 template <int D>
 struct Cfg {
@@ -132,7 +137,8 @@ struct Cfg {
   static constexpr int kOffMeet = kOffV + kVStages * kKvBytes;   // 4 warps x 32 columns x 32 rows
   static constexpr int kOffMask = kOffMeet + 4 * 4096;
   static constexpr int kSmem = kOffMask + kTreeNodes * kMaskStride * 4 + 1024;   // + alignment to a swizzle atom
-  static_assert(kGoneRing >= kKStages + 2 && kGoneRing >= kVStages + 2, "the ring of missing blocks");
+  static_assert(kGoneRing > kKStages + kOneTile + 1, "the ring of K's missing blocks");
+  static_assert(kGoneRing > kVStages, "V's are read before the stage is handed back");
 };
 
 // MN-major V operand (sw128_desc walked along N): 64-element blocks of N are kKeys

@@ -290,6 +290,40 @@ def test_blocks_outside_the_pool_are_left_out():
     assert not got[c.starts[2]:c.starts[3]].any()   # no key is left
 
 
+def test_blocks_outside_the_pool_among_items_of_one_and_four_chunks():
+    """Every CTA has several items, one tile's each: the other tile passes over them, and copies
+    run as far ahead as they can.  Ids outside the pool in a third of the sequences."""
+    rng = np.random.default_rng(11)
+    for chunks in ((1, 4), (4, 4)):
+        c = Case([(128 * chunks[i % 2] - int(rng.integers(4, 60)), int(rng.integers(1, 4)))
+                  for i in range(900)], 2, 1, 64, W.DTYPE_F16)
+        held = c.tables.copy()
+        there = []
+        for b in range(900):
+            mask = np.ones(c.ctx[b], dtype=bool)
+            if b % 3 == 0:
+                used = -(-int(c.ctx[b]) // 16)
+                lost = rng.choice(used, int(rng.integers(1, used)), replace=False)
+                c.tables[b, lost] = rng.choice([c.nb, -1, 1 << 30], len(lost))
+                held[b, lost] = 0
+                mask = ~np.isin(np.arange(c.ctx[b]) // 16, lost)
+            there.append(mask)
+        c.up()
+        c.run()
+        assert P.photon_get_last_device_error() == (6, 1)
+        first = c.raw()
+        got = c.values()
+        c.tables = held
+        for b in range(900):
+            s, n = c.starts[b], c.n[b]
+            want, bound = c.want(b, there=there[b])
+            assert (np.abs(got[s:s + n] - want) <= bound).all(), b
+        for _ in range(40):
+            c.run()
+        assert np.array_equal(c.raw(), first)
+        assert P.photon_get_last_device_error() == (6, 1)
+
+
 def test_parents_outside_their_tree_count_as_roots():
     c = Case([(60, 10), (20, 5)], 4, 2, 64, W.DTYPE_F16)
     c.ok()
