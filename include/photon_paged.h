@@ -494,7 +494,8 @@ size_t photon_paged_tree_attention_workspace_size(const photon_paged_shape_t* sh
  * (parents[i] = i - 1) is photon_paged_multi_query.
  *   q, out        [num_tokens][num_q_heads][head_dim]
  *   context_lens  count the tree's nodes, whose K and V rows are in the cache
- * Any NaN in a sequence's own V may reach any of its rows.  Rows of out that belong
+ * What is not finite in K and V of a key reaches the rows of nodes that see the key
+ * and no others.  Rows of out that belong
  * to no sequence are left as they were.  dtype must be PHOTON_F16 or PHOTON_BF16.
  * A sequence with more nodes than max_query_len sets bit 32 and gets max_query_len
  * zero rows (none if its rows lie outside [0, num_tokens)); n > ctx or a context

@@ -46,7 +46,8 @@
 // photon_paged_multi_query and photon_prompt_attention: a product with their
 // rounding errors besides would be half again as many.  fp16 weights are lifted to
 // the upper end of fp16's range (kLift), so that what they lose lies below 2^-32 of
-// the largest.
+// the largest.  A zero weight times an infinity would not vanish: what is not finite in
+// V of a tree's nodes is kept out of the product and reaches the rows that see it apart.
 //
 // Measured (event times of whole calls): 64 contexts of 128 .. 8192 tokens x 16 nodes,
 // 16 q / 8 kv heads x 128, fp16: 94 us = 5.6 TB/s, 83 % of the measured copy rate; a
@@ -153,6 +154,20 @@ __device__ __forceinline__ uint64_t v_operand(uint32_t saddr) {
   return d;
 }
 
+// Which of two elements are infinities or NaN (bits 15 and 31); 8 elements without them.
+constexpr uint32_t kMagnitudes = 0x7fff7fffu;
+template <typename T>
+__device__ __forceinline__ uint32_t odd_pair(uint32_t x) {
+  constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+  constexpr uint32_t kOne = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+  return ((x & kExp) + kOne) & 0x80008000u;
+}
+template <typename T>
+__device__ __forceinline__ uint4 even8(uint4 x) {
+  auto one = [](uint32_t v) -> uint32_t { return v & ~((odd_pair<T>(v) >> 15) * 0xffffu); };
+  return make_uint4(one(x.x), one(x.y), one(x.z), one(x.w));
+}
+
 // A sequence's tree and context; n == 0: empty or rejected.
 struct Seq {
   int q0, n, ctx;
@@ -216,8 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint8_t k_gone[kGoneRing], v_gone[kGoneRing];   // blocks of a chunk that are not there
   __shared__ int up[kTreeNodes];
   __shared__ uint32_t tmem_slot;
-  __shared__ int gave_up_word;
+  __shared__ int gave_up_word, odd_word;
   volatile int* gave_up = &gave_up_word;
+  volatile int* odd = &odd_word;   // a node's V was not finite, in some item so far
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(tree_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sQ = smem_addr(smem), sK = sQ + C::kOffK, sV = sQ + C::kOffV;
@@ -227,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = a.Hq / a.Hkv, g2 = __ffs(G) - 1;   // a power of two
 
   if (tid == 0) {
-    gave_up_word = 0;
+    gave_up_word = odd_word = 0;
     for (int i = 0; i < SK; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_free[i], kTiles);
@@ -517,6 +533,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      if (it.tree >= 0 && *odd) {
+        // what of the item's V is not finite, to the rows that see it, whatever its weight
+        if (!mask_there) {
+          ok = cta_wait(&mask_full, it.tree & 1, gave_up);
+          if (!ok) break;
+          mask_there = true;
+        }
+        const int j0 = max(0, it.c0 * kKeys - tree0), j1 = min(it.n, it.c1 * kKeys - tree0);
+#pragma unroll 1
+        for (int j = store ? j0 : j1; j < j1; ++j) {
+          if (!((mask[j >> 5] >> (j & 31)) & 1u)) continue;
+          const int key = tree0 + j;
+          const int id = __ldg(a.block_tables + (int64_t)it.b * a.MBS + key / kBlockSize);
+          if (id < 0 || id >= a.NB) continue;
+          const T* v = static_cast<const T*>(a.v_cache) +
+                       (((int64_t)id * a.Hkv + it.kvh) * kBlockSize + key % kBlockSize) * D;
+#pragma unroll 1
+          for (int e = 0; e < D; ++e) {
+            const float x = Elem<T>::to_f32(v[e]);
+            if (fabsf(x) < INFINITY) continue;
+            if (it.place == 0) {
+              T* dst = static_cast<T*>(a.out) + head * D + e;
+              *dst = Elem<T>::narrow(Elem<T>::to_f32(*dst) + x);
+            } else {
+              a.ws_o[part * D + e] += x;
+            }
+          }
+        }
+      }
       tc_fence_before();   // O is read before the next item's products (p_full orders them)
     }
   } else {
@@ -854,6 +899,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (r >= valid || (gone >> (r >> 4)) & 1u)
                   *reinterpret_cast<uint4*>(rows + (ch >> 3) * (kKeys * 128) + r * 128 + ((ch & 7) << 4)) =
                       make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_async_smem();
+              __syncwarp();
+            }
+            // A node's V meets zero weights, too, of the rows that do not see it: what of it
+            // is not finite is taken out, and added at the item's end to the rows that do.
+            // (Where both tiles do it: told first, so that who finds it gone is told.)  The
+            // look at it runs beside the softmax; with four rows a turn its code drives the
+            // softmax's out of the instruction cache (a batch-256 mix 193 -> 222 us).
+            const int tree_row = max(0, it.ctx - it.n - (it.c0 + lc) * kKeys);   // the chunk's first
+            if (tree_row < valid) {
+              unsigned char* rows = smem + C::kOffV + (vc % SV) * C::kKvBytes;
+              // a lane's eighth of the row, then the same of every kRowsApart-th row
+              constexpr int kRowsApart = 32 / (D / 8);
+              const int r0 = tree_row + lane / (D / 8), ch = lane % (D / 8);
+              unsigned char* mine = rows + (ch >> 3) * (kKeys * 128) + ((ch & 7) << 4);
+              __syncwarp();   // filled up above
+              uint32_t largest = 0;   // of the magnitudes, as integers
+#pragma unroll 1
+              for (int r = r0; r < valid; r += kRowsApart) {
+                const uint4 x = *reinterpret_cast<const uint4*>(mine + r * 128);
+                largest = __vmaxu2(largest, __vmaxu2(__vmaxu2(x.x & kMagnitudes, x.y & kMagnitudes),
+                                                     __vmaxu2(x.z & kMagnitudes, x.w & kMagnitudes)));
+              }
+              const bool found = odd_pair<T>(largest) != 0;
+              if (__any_sync(0xffffffffu, found)) {
+                if (found) *odd = 1;
+                __threadfence_block();
+#pragma unroll 1
+                for (int r = r0; found && r < valid; r += kRowsApart) {
+                  uint4* at = reinterpret_cast<uint4*>(mine + r * 128);
+                  *at = even8<T>(*at);
+                }
               }
               fence_async_smem();
               __syncwarp();

@@ -269,6 +269,58 @@ def test_nan_in_a_row_and_infinities_elsewhere():
         assert (np.abs(got[i] - want[i]) <= bound[i]).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv,seqs", [
+    (4, 2, [(30, 9), (7, 3), (200, 40)]),                       # an item each
+    (8, 1, [(3, 16), (60, 2), (100, 33), (250, 64)]),           # rows of both tiles among others
+    (4, 2, [(9000, 20)]),                                       # one context over every SM
+    (2, 1, [(90 + i % 50, 1 + i % 13) for i in range(700)]),    # several items a CTA
+    (4, 2, [(760, 30)] * 3 + [(120, 200)]),                     # both tiles' chunks in turn
+])
+def test_v_that_is_not_finite_reaches_the_rows_that_see_it(hq, hkv, seqs, d, dtype):
+    """Infinities and NaN in V of some nodes: the rows that see one have it, the others none."""
+    rng = np.random.default_rng(d + len(seqs))
+    c = Case(seqs, hq, hkv, d, dtype, kind="forest", seed=3)
+    odd = {}
+    for b, n in enumerate(c.n):
+        marks = odd[b] = np.zeros((n, hkv, d))
+        for i in rng.choice(n, min(n, 1 + n // 6), replace=False):
+            for h in range(hkv):
+                marks[i, h, rng.choice(d, 3, replace=False)] = rng.choice([np.inf, -np.inf, np.nan], 3)
+        if b % 3 == 1:
+            marks[:] = 0                                        # a sequence without
+    finite = c.pools[1].copy()
+    wide = I.to_f64(c.pools[1], dtype)
+    for b, n in enumerate(c.n):
+        j = c.ctx[b] - n + np.arange(n)
+        at = (c.tables[b, j // 16], slice(None), j % 16)
+        hit = odd[b] != 0
+        held = wide[at]
+        wide[at] = np.where(hit, odd[b], held)
+        even = finite[at]
+        even[hit] = 0
+        finite[at] = even
+    c.pools[1] = I.narrow(wide, dtype)
+    c.up()
+    c.run()
+    got = c.values()
+    c.pools[1] = finite
+    for b, n in enumerate(c.n):
+        s = c.starts[b]
+        want, bound = c.want(b)
+        see = T.sees(c.parents[s:s + n])
+        extra = np.zeros((n, hkv, d))
+        for i in range(n):
+            with np.errstate(invalid="ignore"):
+                extra[i] = odd[b][see[i]].sum(0)                # inf - inf: NaN
+        want = want + np.repeat(extra, hq // hkv, axis=1)
+        rows, plain = got[s:s + n], np.isfinite(want)
+        assert (np.abs(rows[plain] - want[plain]) <= bound[plain]).all(), b
+        assert np.array_equal(rows[~plain], want[~plain], equal_nan=True), b
+    c.ok()
+
+
 def test_blocks_outside_the_pool_are_left_out():
     c = Case([(400, 20), (70, 3), (0, 2)], 4, 2, 128, W.DTYPE_F16)
     lost = {0: [0, 7, 11], 1: [2], 2: [0]}
