@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
   for (int i = tid; i < n; i += kThreads) {
     int up = __ldg(a.parents + q0 + i);
     int x = __ldg(a.tokens + q0 + i);
-    if (up < -1 || up >= i || x >= V) {
+    if (up < -1 || up >= i || (x >= V && i > 0)) {   // (node 0's token is not used)
       if (rank == 0) raise_error(a.err, kErrTree);
       if (up < -1 || up >= i) up = -1;
     }

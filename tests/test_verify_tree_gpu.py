@@ -179,6 +179,15 @@ def test_the_same_token_twice_and_padding():
     assert P.photon_get_last_device_error() == (6, 64)
 
 
+@pytest.mark.parametrize("drafted", [True, False])
+def test_the_first_nodes_token_is_not_used(drafted):
+    c = Case([4, 1, 7], 90, drafted=drafted)
+    for first in (90, 1 << 30, -2, 0):
+        c.tokens[c.starts[:-1]] = first
+        c.go()
+        assert P.photon_get_last_device_error() == (0, 0)
+
+
 def test_sampling_numbers_at_the_borders():
     """0 and the largest float below 1; rows whose first or last entries are 0."""
     low, high = 0.0, float(np.nextafter(np.float32(1), np.float32(0)))
