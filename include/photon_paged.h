@@ -562,8 +562,8 @@ photon_status_t photon_verify_tree(const void* target_probs, int64_t target_stri
  *                 number of layers, no pool twice.  Read during the call
  *   context_lens  as for the attention, with the tree's nodes
  * A path that does not rise within [0, n), or a path_len outside [0, n], sets bit 64,
- * a block id outside the pool bit 1, a bad context bit 4: that sequence is left as it
- * was.  num_pools == 0, num_seqs == 0, num_tokens == 0 or max_query_len == 0 is a
+ * a block id outside the pool that a row moves from or to bit 1, a bad context (of a
+ * sequence with nodes) bit 4: that sequence is left as it was.  num_pools == 0, num_seqs == 0, num_tokens == 0 or max_query_len == 0 is a
  * no-op.  Uses shape: num_seqs, num_kv_heads, head_dim, num_blocks,
  * max_blocks_per_seq, dtype (16-bit or 32-bit rows). */
 photon_status_t photon_cache_compact(void* const* pools, int32_t num_pools,

@@ -38,12 +38,13 @@ __global__ void __launch_bounds__(kCompactThreads)
     return;
   }
   const int n = q1 - q0;
-  if (m == 0 || n == 0) return;
-  if (ctx < n || ctx > a.MBS * kBlockSize || m < 0 || m > n) {
-    if (first_group && tid == 0)
-      raise_error(a.err, m < 0 || m > n ? kErrTree : kErrContext);
+  const bool bad_path = m < 0 || m > n;
+  // (a sequence without nodes has no use for its context)
+  if (bad_path || (n > 0 && (ctx < n || ctx > a.MBS * kBlockSize))) {
+    if (first_group && tid == 0) raise_error(a.err, bad_path ? kErrTree : kErrContext);
     return;
   }
+  if (m == 0) return;
   if (tid == 0) bad = 0;
   __syncthreads();
   const int first = ctx - n;

@@ -99,6 +99,27 @@ def test_what_is_refused_is_left_as_it_was():
     c.check(skip=(0, 1, 2))
 
 
+def test_what_is_wrong_shows_where_nothing_moves():
+    """A sequence without nodes, and one of which nothing was accepted."""
+    def one(bits, **change):
+        c = Moves([(20, 6, 4), (31, 0, 0), (9, 5, 0)], 2, 64, W.DTYPE_F16, 2)
+        for name, (b, value) in change.items():
+            getattr(c, name)[b] = value
+        c.run()
+        assert P.photon_get_last_device_error() == ((6, bits) if bits else (0, 0)), change
+        c.count[1:] = 0
+        c.check()
+
+    one(0)
+    one(64, count=(1, 2))
+    one(64, count=(1, -1))
+    one(64, count=(2, -1))
+    one(4, ctx=(2, 4))
+    one(4, ctx=(2, -1))
+    one(4, ctx=(2, 1 << 20))
+    one(0, ctx=(1, -1))          # no nodes: its context is not looked at
+
+
 def test_pool_past_32_bits():
     c = Moves([(40, 20, 6), (7, 9, 4)], 4, 128, W.DTYPE_F16, 1, seed=3)
     NB = 300000                        # 16 KB a block: 4.9 GB
