@@ -78,12 +78,14 @@ __device__ __forceinline__ Pair sub2(Pair a, Pair b) {   // a - b, rounded once
   return fma2(b, pair(-1.f, -1.f), a);
 }
 
-// A sum held in two floats.
+// A sum held in two floats.  a + b and b + a are the same bits (what hi rounds off is
+// exact in either order, and is added to lo + rest), so that lanes which exchange their
+// sums hold the same one: all of a warp walks the tree, and has to go one way.
 struct Sum2 {
   float hi = 0.f, lo = 0.f;
   __device__ __forceinline__ void add(float x, float rest) {
     const float s = hi + x, b = s - hi;
-    lo += ((hi - (s - b)) + (x - b)) + rest;
+    lo = (lo + rest) + ((hi - (s - b)) + (x - b));
     hi = s;
   }
   __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
