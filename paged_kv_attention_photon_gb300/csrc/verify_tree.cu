@@ -88,6 +88,12 @@ struct Sum2 {
     lo = (lo + rest) + ((hi - (s - b)) + (x - b));
     hi = s;
   }
+  // lo no more than half a step of hi
+  __device__ __forceinline__ void settle() {
+    const float s = hi + lo, b = s - hi;
+    lo = (hi - (s - b)) + (lo - b);
+    hi = s;
+  }
   __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
   __device__ __forceinline__ bool positive() const { return hi + lo > 0.f; }
   __device__ __forceinline__ bool above(const Sum2& t) const { return (hi - t.hi) + (lo - t.lo) > 0.f; }
@@ -144,17 +150,22 @@ __device__ __forceinline__ bool passes(float p, float q, const Sum2& L, float u,
 // An entry as a probability: NaN and negative ones are 0, ones above 1 are 1.
 __device__ __forceinline__ float as_prob(float x) { return __saturatef(x); }
 
-// r = (p - L q)+ of two elements as r + rest, L = hi + lo.
+// r = (p - L q)+ of two elements as r + rest, L = hi + lo.  What is left may be a small
+// part of p, next to L q: whether anything is hangs on all of L q, and r takes what rest
+// has of it, so that sums are as exact as what they add up.
 __device__ __forceinline__ void left_of(float2 p, float2 q, float hi, float lo, Pair& r, Pair& rest) {
-  const Pair h = pair(hi, hi), qq = pair(q.x, q.y);
+  const Pair h = pair(hi, hi), qq = pair(q.x, q.y), pp = pair(p.x, p.y);
   const Pair y = mul2(h, qq);
-  const float2 yf = parts(y);
   // what rounding y has cost, and L's second part
   const Pair yl = fma2(pair(lo, lo), qq, fma2(h, qq, sub2(0, y)));
-  const Pair m = pair(fmaxf(p.x, yf.x), fmaxf(p.y, yf.y));
-  r = sub2(m, y);   // 0 where p <= y; (m - r) - y is exact, as m >= y >= 0
-  const float2 e = parts(sub2(sub2(sub2(m, r), y), yl));
-  rest = pair(p.x > yf.x ? e.x : 0.f, p.y > yf.y ? e.y : 0.f);
+  const Pair d = sub2(pp, y);
+  // (p - d) - y is exact: p > y or so near to it that d is
+  const Pair e = sub2(sub2(sub2(pp, d), y), yl);
+  const Pair s = add2(d, e);
+  const float2 df = parts(d), ylf = parts(yl), sf = parts(s), ef = parts(sub2(e, sub2(s, d)));
+  const bool x = df.x > ylf.x, z = df.y > ylf.y;
+  r = pair(x ? sf.x : 0.f, z ? sf.y : 0.f);
+  rest = pair(x ? ef.x : 0.f, z ? ef.y : 0.f);
 }
 
 // 16 bytes of a row from element e on; what lies behind its end is 0.
@@ -354,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
               L.add(F.hi, F.lo);
             else
               L.add(1.f, 0.f);
+            L.settle();
             F.hi = -1.f;
             F.lo = 0.f;
             continue;

@@ -164,6 +164,29 @@ def test_many_siblings():
         c.go()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kinds,rejected", [([2, 1, 1, 0], n) for n in (1, 2, 20, 60, 80)] +
+                         [([1.25, 1.25, 1.25, 0.25], n) for n in (1, 2, 9, 12, 13, 14, 18)])
+def test_what_is_left_after_many_rejections(kinds, rejected, dtype):
+    """Children that the target does not take: what is left comes ever closer to nothing in
+    (p - L q)+, but stays where p / q is largest.  Every fourth entry is of one of four kinds of
+    p / q, with q alike.  After the second rejection only the first kind is left, and each takes
+    the same share from what L lacks to its p / q: 0.75 of it stays in the first case (2^-33 after
+    80), 0.25 in the second (2^-36 after 18)."""
+    vocab, n = 4096, rejected + 1
+    c = Case([n] * 6, vocab, dtype)
+    q = np.full(vocab, 2.0 ** -12)
+    c.p[:], c.q[:] = I.narrow(np.tile(kinds, vocab // 4) * q, dtype), I.narrow(q, dtype)
+    for s in c.starts[:-1]:
+        c.parents[s + 1:s + n] = 0
+        c.tokens[s + 1:s + n] = 4 * np.arange(rejected) + 3
+    c.accept[:] = 0.9
+    c.sample[:] = [0.0, 0.2502, 0.5003, 0.7204, 0.9305, 0.9994]
+    # the last child of one sequence is of the first kind: accepted where it stands last
+    c.tokens[c.starts[2] + n - 1] = 400
+    assert c.go() == 1
+
+
 def test_the_same_token_twice_and_padding():
     c = Case([8, 8], 60, drafted=False)
     c.parents[:] = np.tile([-1, 0, 0, 0, 0, 0, 0, 0], 2)
