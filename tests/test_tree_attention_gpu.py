@@ -230,6 +230,47 @@ def test_scores_of_any_size(dtype, scale, size):
         assert (np.abs(got[s:s + n]) <= np.abs(v).max() * (1 + 1.25 * I.EPS[dtype])).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", [0.125, 40.0, -40.0, 3e4, -1e20, 1e30])
+def test_the_largest_scores_share_a_row(scale, dtype, d):
+    """Scores are exact (small integers in one element), and those below the largest lie 1200 |scale|
+    and more below it: a row is the mean of the V of the keys that it sees with the largest one.
+    Each such key's weight is rounded once, the exponentials and sums are off by 2^-18, and the
+    output is rounded."""
+    rng = np.random.default_rng(7)
+    c = Case([(0, 1), (300, 9), (30, 2), (2000, 3), (9000, 20), (130, 90)], 4, 2, d, dtype, scale=scale)
+    c.q[:] = I.narrow(np.zeros(1), dtype)[0]
+    c.q[:, :, 5] = I.narrow(np.array([60.0]), dtype)[0]
+    tops = []
+    for b in range(len(c.n)):
+        ctx, n = int(c.ctx[b]), int(c.n[b])
+        first = rng.integers(-60, 41, ctx).astype(float)
+        top = rng.random(ctx) < 3.0 / ctx                       # a few anywhere, some nodes, the root
+        top[ctx - n:] |= rng.random(n) < 0.3
+        top[ctx - n] = True
+        first[top] = 60.0
+        j = np.arange(ctx)
+        k = I.narrow(np.sign(scale) * first, dtype)
+        rows = c.pools[0][c.tables[b, j // 16], :, j % 16]
+        rows[:, :, 5] = k[:, None]
+        c.pools[0][c.tables[b, j // 16], :, j % 16] = rows
+        tops.append(top)
+    c.up()
+    c.run()
+    got = c.values()
+    for b, top in enumerate(tops):
+        s, n, ctx = c.starts[b], int(c.n[b]), int(c.ctx[b])
+        v = T.cached_rows(c.pools[1], c.tables[b], c.ctx[b], dtype)
+        see = np.ones((n, ctx), dtype=bool)
+        see[:, ctx - n:] = T.sees(c.parents[s:s + n])
+        w = (see & top).astype(float)
+        want = np.repeat(np.einsum("nj,jhd->nhd", w / w.sum(-1, keepdims=True), v), 2, axis=1)
+        off = (I.EPS[dtype] / 2 + 2.0 ** -18) * np.abs(v).max()
+        assert (np.abs(got[s:s + n] - want) <= off + I.EPS[dtype] / 2 * (np.abs(want) + off) + 2.0 ** -25).all(), b
+    c.ok()
+
+
 def test_many_keys_of_little_weight():
     """What lies 2^-24 below the first key adds up (fp16 weights are lifted)."""
     c = Case([(9000, 1)], 1, 1, 64, W.DTYPE_F16, scale=1.0)
