@@ -45,6 +45,8 @@ namespace {
 
 constexpr int kVerifyResident = 1024;   // threads per SM: 64 registers each
 constexpr int kVerifyCluster = 8;   // most CTAs of a cluster
+// What is left of 1 so far below it that 48 bits of that are few of its own.
+constexpr float kLittle = 1.f / (1 << 20);
 constexpr int kVerifyRun = kVerifyVocab / kVerifyCluster;   // most tokens of a CTA's run
 
 // Two floats in one register pair, and the paired instructions.
@@ -139,10 +141,10 @@ __device__ __forceinline__ Sum2 of_lane(const Sum2& x, int lane) {
   s.lo = __shfl_sync(0xffffffffu, x.lo, lane);
   return s;
 }
-// x > y for x = max(0, p - L q), y = u F q: in single precision where that is clear
-// (each side is off by a few 2^-24 of what goes into it), else in double.
+// x > y for x = max(0, p - L q), y = u F q, L settled: in single precision where that is
+// clear (each side is off by a few 2^-24 of what goes into it), else in double.
 __device__ __forceinline__ bool passes(float p, float q, const Sum2& L, float u, const Sum2& F) {
-  const float lq = L.hi * q, x = fmaxf(p - lq, 0.f), y = u * F.hi * q;
+  const float lq = L.hi * q, x = fmaxf(p - lq, 0.f), y = u * (F.hi + F.lo) * q;
   if (fabsf(x - y) > 1e-5f * (p + lq + y)) return x > y;
   return fmax((double)p - L.value() * (double)q, 0.0) > (double)u * F.value() * (double)q;
 }
@@ -385,8 +387,16 @@ __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
             z.add(-up_to.hi, -up_to.lo);
             z.add(mine.hi, 0.f);
             if (!z.positive()) z = Sum2{};
-            const unsigned yes =
-                __ballot_sync(0xffffffffu, child && passes(mine.hi, 1.f, Sum2{}, number[i], z));
+            bool pass = child && passes(mine.hi, 1.f, Sum2{}, number[i], z);
+            if (child && z.hi + z.lo < kLittle) {
+              // of 48 bits few are left: in double, one after another
+              double Z = 1.0;
+              for (int j = node + 1; j < i; ++j)
+                if (parent[j] == node && token[j] >= 0) Z = fmax(0.0, Z - (double)prob[j]);
+              pass = (double)mine.hi > (double)number[i] * Z;
+            }
+            __syncwarp();
+            const unsigned yes = __ballot_sync(0xffffffffu, pass);
             if (yes) taken = i0 + __ffs(yes) - 1;
             some = true;
             lost = of_lane(up_to, 31);

@@ -164,6 +164,30 @@ def test_many_siblings():
         c.go()
 
 
+@pytest.mark.parametrize("shrink", [0.25, 2.0 ** -6, 2.0 ** -12])
+@pytest.mark.parametrize("before", [1, 2, 3, 5])
+def test_chosen_children_that_leave_little(before, shrink):
+    """Each child before the last takes all but a random share below `shrink` of what is left, and is
+    rejected; the last one's probability is 0.2 % above or below what it is accepted from."""
+    rng = np.random.default_rng(before)
+    n = before + 2
+    c = Case([n] * 200, 60, W.DTYPE_F32, drafted=False)
+    c.p[:] = 0
+    high = np.nextafter(np.float32(1), np.float32(0))
+    for b, s in enumerate(c.starts[:-1]):
+        c.parents[s + 1:s + n] = 0
+        c.tokens[s + 1:s + n] = rng.permutation(60)[:n - 1]
+        left = 1.0                                             # exact in 64 bits
+        for i in range(before):
+            x = np.float32(left * (1 - shrink * rng.uniform(0.1, 1)))
+            c.p[s, c.tokens[s + 1 + i]] = x
+            left -= float(x)
+        c.accept[s + 1:s + n] = high
+        c.accept[s + n - 1] = u = np.float32(rng.uniform(0.2, 0.9))
+        c.p[s, c.tokens[s + n - 1]] = np.float32(float(u) * left * (1.002 if b % 2 else 0.998))
+    assert c.go() == 100
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("kinds,rejected", [([2, 1, 1, 0], n) for n in (1, 2, 20, 60, 80)] +
                          [([1.25, 1.25, 1.25, 0.25], n) for n in (1, 2, 9, 12, 13, 14, 18)])
