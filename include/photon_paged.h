@@ -542,7 +542,10 @@ photon_status_t photon_paged_tree_attention(const void* q, const void* k_cache,
  *   path_len      int32 [num_seqs]: how many (0 for a sequence without nodes or
  *                 rejected with bit 32)
  *   next_token    int32 [num_seqs]; -1 where path_len is 0
- * Acceptances are decided in 64 bits, and sums of r held to 48 bits.  vocab <= 2^20,
+ * Sums of r are held to about 48 bits, acceptances decided in single precision where that
+ * is clear and else in double on those sums; where rejections have left less than a
+ * millionth (drawn children get there once in a million times), all is done in double, a
+ * pass over the rows for each further rejection.  vocab <= 2^20,
  * num_seqs <= 65535 (PHOTON_ERR_UNSUPPORTED).  num_seqs == 0 is a no-op. */
 photon_status_t photon_verify_tree(const void* target_probs, int64_t target_stride,
                                    const void* draft_probs, int64_t draft_stride, int32_t vocab,

@@ -12,6 +12,11 @@
 // rows for F, none if no sibling follows (the sampling pass finds the sum itself).
 // Without q a child is a point mass: Z loses r(x), and the row needs no pass at all.
 //
+// (p - L q)+ loses what p and L q have in common: where F is a millionth of L, the rest of
+// the tree is verified as the definition says it, in double: each element's r from p and
+// the row sums so far, a pass over the rows for each of them.  Children that the draft
+// drew get there once in a million times.
+//
 // What it answers are whole numbers, so what they hang on is held to about 48 bits:
 // L, F and the row sums are pairs of floats whose rounding errors are carried along
 // (two-sum), two elements an instruction; a test is made in single precision, and
@@ -45,7 +50,7 @@ namespace {
 
 constexpr int kVerifyResident = 1024;   // threads per SM: 64 registers each
 constexpr int kVerifyCluster = 8;   // most CTAs of a cluster
-// What is left of 1 so far below it that 48 bits of that are few of its own.
+// What is left of 1 (of L) so far below it that 48 bits of that are few of its own.
 constexpr float kLittle = 1.f / (1 << 20);
 constexpr int kVerifyRun = kVerifyVocab / kVerifyCluster;   // most tokens of a CTA's run
 
@@ -203,17 +208,130 @@ __device__ __forceinline__ void store_peer(float2* p, int rank, float2 v) {
       : "memory");
 }
 
+// What of a sequence's verification is in shared memory.
+template <int kWarps>
+struct VerifyTree {
+  int parent[kTreeNodes], token[kTreeNodes], path[kTreeNodes];
+  float prob[kTreeNodes], draft[kTreeNodes], number[kTreeNodes];
+  double inverse[kTreeNodes];   // 1 / Z of each rejection
+  float2 sums_of[2][kVerifyCluster * kWarps];
+};
+
+// The rest of a walk from `node`, the len-th of the path, by its definition and in double:
+// r after some rejections is p through r <- max(0, r / Z - q) for each of them.  Slow, for
+// where little is left; every thread of the cluster goes the same way, by itself.
+template <typename T, int kWarps>
+__device__ __noinline__ void finish_in_double(const VerifyArgs& a, VerifyTree<kWarps>& s, int b, int ranks,
+                                              int node, int len, int round) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x % ranks;
+  const int q0 = __ldg(a.query_start + b), n = __ldg(a.query_start + b + 1) - q0, V = a.vocab;
+  const int each = (V + ranks * kWarps - 1) / (ranks * kWarps);
+  const int run0 = min(V, (rank * kWarps + warp) * each), run1 = min(V, run0 + each);
+  int times = 0;
+  auto left = [&](float p, float q) -> double {
+    double r = p;
+    for (int j = 0; j < times && r > 0.0; ++j) r = fma(r, s.inverse[j], -(double)q);
+    return fmax(r, 0.0);
+  };
+  auto of_row = [&](int e) -> double {
+    const int64_t row = q0 + node;
+    return left(as_prob(Elem<T>::to_f32(static_cast<const T*>(a.target)[row * a.target_stride + e])),
+                as_prob(Elem<T>::to_f32(static_cast<const T*>(a.draft)[row * a.draft_stride + e])));
+  };
+  auto share = [&](int k) -> double {   // of the last sum, warp k's of the cluster
+    const float2 x = s.sums_of[(round - 1) & 1][k];
+    return __hiloint2double(__float_as_int(x.y), __float_as_int(x.x));
+  };
+  auto sum = [&]() -> double {
+    double mine = 0.0;
+    for (int e = run0 + lane; e < run1; e += 32) mine += of_row(e);
+    __syncwarp();
+    for (int o = 1; o < 32; o <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    const int parity = round++ & 1;
+    if (lane < ranks)
+      store_peer(&s.sums_of[parity][rank * kWarps + warp], lane,
+                 make_float2(__int_as_float(__double2loint(mine)), __int_as_float(__double2hiint(mine))));
+    cluster_arrive();
+    cluster_wait();
+    double all = 0.0;
+    for (int k = 0; k < ranks * kWarps; ++k) all += share(k);
+    return all;
+  };
+  double Z = 1.0;
+  for (int j = node + 1; j < n; ++j) {
+    if (s.parent[j] != node || s.token[j] < 0) continue;
+    if (left(s.prob[j], s.draft[j]) > (double)s.number[j] * Z * (double)s.draft[j]) {
+      if (tid == 0) s.path[len] = j;
+      ++len;
+      node = j;
+      times = 0;
+      Z = 1.0;
+      continue;   // its children come after it
+    }
+    __syncthreads();   // nobody reads the list
+    if (tid == 0) s.inverse[times] = Z > 0.0 ? 1.0 / Z : 1.0;
+    __syncthreads();
+    ++times;
+    if (Z > 0.0) Z = sum();   // else nothing will be left again
+  }
+  double all = sum();
+  if (!(all > 0.0) && times > 0) {   // the target's own row
+    times = 0;
+    all = sum();
+  }
+  __syncthreads();   // the path is written
+  if (rank == 0) {
+    for (int i = tid; i < n; i += 32 * kWarps) a.path[q0 + i] = i < len ? s.path[i] : -1;
+    if (tid == 0) a.path_len[b] = len;
+    if (tid == 0 && !(all > 0.0)) a.next[b] = -1;
+  }
+  if (!(all > 0.0)) return;
+  const double t = (double)__ldg(a.sample + b) * all;
+  // the warp in whose run t is passed, or the last that holds anything
+  double before = 0.0, up_to = 0.0;
+  int owner = 0;
+  for (int k = 0; k < ranks * kWarps; ++k) {
+    const double x = share(k);
+    if (x > 0.0) {
+      owner = k;
+      before = up_to;
+    }
+    up_to += x;
+    if (x > 0.0 && up_to > t) break;
+  }
+  if (owner != rank * kWarps + warp) return;
+  int answer = -1;
+  for (int e0 = run0; e0 < run1; e0 += 32) {
+    const double x = e0 + lane < run1 ? of_row(e0 + lane) : 0.0;
+    __syncwarp();
+    double y = x;
+    for (int o = 1; o < 32; o <<= 1) {
+      const double z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    y += before;
+    const unsigned held = __ballot_sync(0xffffffffu, x > 0.0);
+    const unsigned hit = __ballot_sync(0xffffffffu, x > 0.0 && y > t);
+    if (held) answer = e0 + (hit ? __ffs(hit) - 1 : 31 - __clz(held));
+    if (hit) break;
+    before = __shfl_sync(0xffffffffu, y, 31);
+  }
+  if (lane == 0) a.next[b] = answer;
+}
+
 // kVec: rows begin on 16-byte boundaries.
 template <typename T, bool kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
-    verify_tree_kernel(const VerifyArgs a, int ranks) {
+    verify_tree_kernel(const __grid_constant__ VerifyArgs a, int ranks) {
   constexpr int kWarps = kThreads / 32, N = 16 / sizeof(T), kTile = 32 * N, kDepth = 8 / N;   // elements of a lane, of a warp; loads ahead
-  __shared__ int parent[kTreeNodes], token[kTreeNodes], path[kTreeNodes];
-  __shared__ float prob[kTreeNodes], draft[kTreeNodes], number[kTreeNodes];
-  __shared__ float2 sums_of[2][kVerifyCluster * kWarps];
+  __shared__ VerifyTree<kWarps> tree;
+  auto &parent = tree.parent, &token = tree.token, &path = tree.path;
+  auto &prob = tree.prob, &draft = tree.draft, &number = tree.number;
+  auto& sums_of = tree.sums_of;
   __shared__ float2 threshold, owner_before;
   __shared__ float2 state_less;   // L
   __shared__ int state_node, state_len, state_sweep, state_out, row_left, owner_warp;
+  enum { kNone, kSome, kLittleLeft };   // of a row; kSome of a walk: a pass is wanted
   extern __shared__ uint32_t out[];   // a bit for each token of the CTA's run
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / ranks, rank = blockIdx.x % ranks;
@@ -331,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
       }
       all.over(32);
       row = all;
-      if (lane == 0) row_left = all.positive();
+      // L q and p have nearly all of their bits in common (never where L is 0)
+      if (lane == 0) row_left = all.hi < kLittle * less.x ? kLittleLeft : all.positive() ? kSome : kNone;
     }
   };
   // ---- the walk: warp 0, up to the next pass that it needs.  Doubles are for one
@@ -341,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
   F.hi = 1.f;   // < 0: not known yet
   while (true) {
     if (warp == 0) {
-      bool want = false, some = false;
+      bool some = false;
+      int want = kNone;
       while (true) {
         int taken = -1;
         some = false;   // a child of the node was rejected
@@ -356,17 +476,18 @@ __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
           }
           if (j == n) break;
           if (F.hi < 0.f) {
-            want = true;
+            want = kSome;
+            break;
+          }
+          if (F.hi < kLittle * L.hi) {
+            want = kLittleLeft;
             break;
           }
           last = j;
           if (passes(prob[j], draft[j], L, number[j], F)) {
             taken = j;
           } else {
-            if (F.positive())
-              L.add(F.hi, F.lo);
-            else
-              L.add(1.f, 0.f);
+            L.add(F.hi, F.lo);
             L.settle();
             F.hi = -1.f;
             F.lo = 0.f;
@@ -421,7 +542,11 @@ __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
     prow = target + (int64_t)state_node * a.target_stride;
     qrow = drafts + (int64_t)state_node * a.draft_stride;
     less = state_less;
-    if (!state_sweep) break;
+    if (state_sweep == kNone) break;
+    if (state_sweep == kLittleLeft) {
+      finish_in_double<T, kWarps>(a, tree, b, ranks, state_node, state_len, round);
+      return;
+    }
     sweep();
     if (warp == 0) F = row;
   }
@@ -443,6 +568,10 @@ __global__ void __launch_bounds__(kThreads, kVerifyResident / kThreads)
   }
   sweep();
   __syncthreads();
+  if (row_left == kLittleLeft) {
+    finish_in_double<T, kWarps>(a, tree, b, ranks, state_node, state_len, round);
+    return;
+  }
   if (!row_left && (marked || less.x != 0.f)) {   // nothing is left: the target's own row
     marked = false;
     less = make_float2(0.f, 0.f);

@@ -211,6 +211,27 @@ def test_what_is_left_after_many_rejections(kinds, rejected, dtype):
     assert c.go() == 1
 
 
+@pytest.mark.parametrize("kinds,rejected", [([2, 1, 1, 0], 150), ([2, 1, 1, 0], 254),
+                                            ([1.25, 1.25, 1.25, 0.25], 40), ([1.25, 1.25, 1.25, 0.25], 254)])
+def test_rejections_that_leave_less_than_48_bits_tell(kinds, rejected):
+    test_what_is_left_after_many_rejections(kinds, rejected, W.DTYPE_F32)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab,spread,apart", [(2, 1.0, 1.0), (3, 4.0, 1.0), (8, 3.0, 3.0), (40, 0.3, 1.0),
+                                               (450, 6.0, 3.0), (5000, 2.0, 0.1)])
+def test_siblings_of_the_same_tokens(vocab, spread, apart, dtype):
+    """Drawn children that come again and again: what is left may be a sliver of p."""
+    rng = np.random.default_rng(vocab)
+    c = Case([60] * 24, vocab, dtype, spread=spread, apart=apart, seed=vocab)
+    for s, n in zip(c.starts, c.n):
+        c.parents[s + 1:s + n] = 0
+        held = c.tokens[s + 1:s + n]
+        c.tokens[s + 1:s + n] = rng.choice(held[:max(1, int(rng.integers(1, 30)))], n - 1)
+        c.accept[s + 1:s + n] = rng.choice([0.5, 0.97, 0.999], n - 1)
+    c.go()
+
+
 def test_the_same_token_twice_and_padding():
     c = Case([8, 8], 60, drafted=False)
     c.parents[:] = np.tile([-1, 0, 0, 0, 0, 0, 0, 0], 2)
