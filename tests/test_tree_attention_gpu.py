@@ -152,6 +152,21 @@ def test_pairs_whole_and_split(seqs, d, ctx, n):
     c.ok()
 
 
+@pytest.mark.parametrize("seqs", [4, 60])
+@pytest.mark.parametrize("wider", [1, 60, 4000])
+def test_tables_wider_than_any_context(seqs, wider):
+    """A table of the longest context that there may be: any numbers behind a context's blocks."""
+    rng = np.random.default_rng(wider)
+    c = Case([(int(rng.integers(0, 300)), int(rng.integers(1, 20))) for _ in range(seqs)], 16, 8, 64,
+             W.DTYPE_F16, seed=seqs)
+    c.tables = np.concatenate([c.tables, rng.integers(-9, 2 ** 30, (seqs, wider), dtype=np.int32)], 1)
+    c.mbs += wider
+    c.up()
+    c.run(longest=min(256, c.longest + wider))
+    c.check()
+    c.ok()
+
+
 def test_many_short_sequences_and_empty_ones():
     rng = np.random.default_rng(3)
     seqs = [(int(rng.integers(0, 90)), int(rng.integers(0, 20))) for _ in range(400)]
