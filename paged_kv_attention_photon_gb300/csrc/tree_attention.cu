@@ -46,8 +46,13 @@
 // photon_paged_multi_query and photon_prompt_attention: a product with their
 // rounding errors besides would be half again as many.  fp16 weights are lifted to
 // the upper end of fp16's range (kLift), so that what they lose lies below 2^-32 of
-// the largest.  A zero weight times an infinity would not vanish: what is not finite in
-// V of a tree's nodes is kept out of the product and reaches the rows that see it apart.
+// the largest.  A zero weight times an infinity would not vanish: a CTA that ends with a row
+// that is not finite goes through its items again, with what of the nodes' V is not finite
+// kept out of the product and added to the rows that see it.  (Taken out always, and in a
+// second pass: 128 contexts of 100 .. 400 tokens x 16 nodes, 16 q / 16 kv heads x 128, 96 and 88
+// us, a batch-256 mix 190 and 187, 4 short contexts 11.5 and 11.6: the look at V lies between its
+// copy and its product, and its code drives the softmax's out of the instruction cache, with
+// four rows a turn in the mix 220.)
 //
 // Measured (event times of whole calls): 64 contexts of 128 .. 8192 tokens x 16 nodes,
 // 16 q / 8 kv heads x 128, fp16: 94 us = 5.6 TB/s, 83 % of the measured copy rate; a
@@ -94,7 +99,7 @@ constexpr int kTiles = 2;
 constexpr int kThreads = 512;           // four warpgroups
 // Registers a thread: 512 x 128 at launch, dealt anew to the softmax warpgroups and
 // the other two (160 + 160 + 96 + 96 = 4 x 128).
-constexpr int kSoftmaxRegs = 160, kOtherRegs = 96;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 160, kOtherRegs = 96;
 constexpr uint32_t kTmemO = 256;        // S of tile t: columns [128 t, 128 t + 128); then the O's
 constexpr float kRescale = 8.f;         // the running maximum moves by 2^8 or not at all
 // Weights are 2^(score - maximum + lift): see the top.
@@ -154,18 +159,26 @@ __device__ __forceinline__ uint64_t v_operand(uint32_t saddr) {
   return d;
 }
 
-// Which of two elements are infinities or NaN (bits 15 and 31); 8 elements without them.
-constexpr uint32_t kMagnitudes = 0x7fff7fffu;
+// 8 elements with 0 in the place of infinities and NaN.
 template <typename T>
-__device__ __forceinline__ uint32_t odd_pair(uint32_t x) {
-  constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
-  constexpr uint32_t kOne = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
-  return ((x & kExp) + kOne) & 0x80008000u;
+__device__ __forceinline__ uint4 finite8(uint4 x) {
+  auto two = [](uint32_t v) -> uint32_t {
+    constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+    constexpr uint32_t kOne = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+    const uint32_t full = ((v & kExp) + kOne) & 0x80008000u;   // bits 15 and 31: all of an exponent is set
+    return v & ~((full >> 15) * 0xffffu);
+  };
+  return make_uint4(two(x.x), two(x.y), two(x.z), two(x.w));
 }
-template <typename T>
-__device__ __forceinline__ uint4 even8(uint4 x) {
-  auto one = [](uint32_t v) -> uint32_t { return v & ~((odd_pair<T>(v) >> 15) * 0xffffu); };
-  return make_uint4(one(x.x), one(x.y), one(x.z), one(x.w));
+__device__ __forceinline__ void mbar_inval(uint64_t* bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// sum += 0 x: NaN from an infinity or NaN on.
+__device__ __forceinline__ void add_zero_times(float2& sum, float x, float y) {
+  asm("{\n.reg .b64 s, v, z;\nmov.b64 s, {%0, %1};\nmov.b64 v, {%2, %3};\nmov.b64 z, {%4, %4};\n"
+      "fma.rn.f32x2 s, v, z, s;\nmov.b64 {%0, %1}, s;\n}"
+      : "+f"(sum.x), "+f"(sum.y)
+      : "f"(x), "f"(y), "f"(0.f));
 }
 
 // A sequence's tree and context; n == 0: empty or rejected.
@@ -215,77 +228,80 @@ struct Item {
   }
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    tree_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
-                          const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
-  using C = Cfg<D>;
-  constexpr int SK = C::kKStages, SV = C::kVStages;
-  extern __shared__ unsigned char tree_smem_raw[];
-  __shared__ __align__(8) uint64_t k_full[SK], k_free[SK], v_full[SV], v_free[SV],
+template <int D>
+struct Shared {
+  uint64_t k_full[Cfg<D>::kKStages], k_free[Cfg<D>::kKStages], v_full[Cfg<D>::kVStages], v_free[Cfg<D>::kVStages],
       q_full[kTiles], q_free[kTiles], s_full[kTiles][2], p_full[kTiles][2], o_done[kTiles][2], item_full[kItems],
       item_free[kItems], mask_full, mask_free, meet_full[4], meet_free[4], drained[2 * kTiles];
-  __shared__ int4 items[kItems][3];
-  __shared__ float2 meet_ml[4][32];
-  __shared__ uint8_t k_gone[kGoneRing], v_gone[kGoneRing];   // blocks of a chunk that are not there
-  __shared__ int up[kTreeNodes];
-  __shared__ uint32_t tmem_slot;
-  __shared__ int gave_up_word, odd_word;
-  volatile int* gave_up = &gave_up_word;
-  volatile int* odd = &odd_word;   // a node's V was not finite, in some item so far
+  int4 items[kItems][3];
+  float2 meet_ml[4][32];
+  uint8_t k_gone[kGoneRing], v_gone[kGoneRing];   // blocks of a chunk that are not there
+  int up[kTreeNodes];
+  uint32_t tmem_slot;
+  int gave_up, odd;   // a wait ran out; some row is not finite
+
+  template <typename F>
+  __device__ __forceinline__ void barriers(F one) {   // one(barrier, arrivals)
+      for (int i = 0; i < Cfg<D>::kKStages; ++i) {
+        one(&k_full[i], 1);
+        one(&k_free[i], kTiles);
+      }
+      for (int i = 0; i < Cfg<D>::kVStages; ++i) {
+        one(&v_full[i], 1);
+        one(&v_free[i], kTiles);
+      }
+      for (int t = 0; t < kTiles; ++t) {
+        one(&q_full[t], 1);
+        one(&q_free[t], kTiles);
+        for (int h = 0; h < 2; ++h) {
+          one(&s_full[t][h], 1);
+          one(&p_full[t][h], 4);   // one arrival per softmax warp
+          one(&o_done[t][h], 1);
+        }
+      }
+      for (int i = 0; i < kItems; ++i) {
+        one(&item_full[i], 1);
+        one(&item_free[i], kRoles);
+      }
+      one(&mask_full, 1);
+      one(&mask_free, 8);
+      for (int i = 0; i < 4; ++i) {
+        one(&meet_full[i], 1);
+        one(&meet_free[i], 1);
+      }
+      for (int i = 0; i < 2 * kTiles; ++i) one(&drained[i], 1);
+  }
+};
+
+// All of a CTA's items, by warps in their roles.  kCareful: with an eye to V that is not
+// finite.
+template <typename T, int D, bool kCareful>
+__device__ __forceinline__ void attend_items(Shared<D>& sh, const TreeArgs& a, const CUtensorMap* tm_q,
+                                             const CUtensorMap* tm_k, const CUtensorMap* tm_v) {
+  using C = Cfg<D>;
+  constexpr int SK = C::kKStages, SV = C::kVStages;
+  auto &k_full = sh.k_full, &k_free = sh.k_free;
+  auto &v_full = sh.v_full, &v_free = sh.v_free;
+  auto &q_full = sh.q_full, &q_free = sh.q_free;
+  auto &s_full = sh.s_full, &p_full = sh.p_full, &o_done = sh.o_done;
+  auto &item_full = sh.item_full, &item_free = sh.item_free;
+  auto &mask_full = sh.mask_full, &mask_free = sh.mask_free;
+  auto &meet_full = sh.meet_full, &meet_free = sh.meet_free;
+  auto& drained = sh.drained;
+  auto& items = sh.items;
+  auto& meet_ml = sh.meet_ml;
+  auto &k_gone = sh.k_gone, &v_gone = sh.v_gone;
+  auto& up = sh.up;
+  volatile int* gave_up = &sh.gave_up;
+  extern __shared__ unsigned char tree_smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(tree_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sQ = smem_addr(smem), sK = sQ + C::kOffK, sV = sQ + C::kOffV;
   uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::kOffMask);
   auto uniform = [](uint32_t x) -> uint32_t { return __shfl_sync(0xffffffffu, x, 0); };
+  const uint32_t tmem = uniform(sh.tmem_slot);
   const int tid = threadIdx.x, warp = (int)uniform(tid >> 5), lane = tid & 31;
   const int G = a.Hq / a.Hkv, g2 = __ffs(G) - 1;   // a power of two
-
-  if (tid == 0) {
-    gave_up_word = odd_word = 0;
-    for (int i = 0; i < SK; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_free[i], kTiles);
-    }
-    for (int i = 0; i < SV; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_free[i], kTiles);
-    }
-    for (int t = 0; t < kTiles; ++t) {
-      mbar_init(&q_full[t], 1);
-      mbar_init(&q_free[t], kTiles);
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(&s_full[t][h], 1);
-        mbar_init(&p_full[t][h], 4);   // one arrival per softmax warp
-        mbar_init(&o_done[t][h], 1);
-      }
-    }
-    for (int i = 0; i < kItems; ++i) {
-      mbar_init(&item_full[i], 1);
-      mbar_init(&item_free[i], kRoles);
-    }
-    mbar_init(&mask_full, 1);
-    mbar_init(&mask_free, 8);
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&meet_full[i], 1);
-      mbar_init(&meet_free[i], 1);
-    }
-    for (int i = 0; i < 2 * kTiles; ++i) mbar_init(&drained[i], 1);
-    mbar_init_fence();
-  }
-  if (warp == 0) tmem_alloc(&tmem_slot, 512);
-  if (tid == 32 * 8) {
-    prefetch_tensor_map(&tm_q);
-    prefetch_tensor_map(&tm_k);
-  }
-  if (tid == 32 * 9) prefetch_tensor_map(&tm_v);
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = uniform(tmem_slot);
 
   bool ok = true;
   Item it;
@@ -482,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       float other = 0.f;
+      float2 zero = make_float2(0.f, 0.f);   // NaN if a sum is not finite
       const bool store = group_row < rows;
       const int64_t head = (int64_t)(it.q0 + (row >> g2)) * a.Hq + it.kvh * G + (row & (G - 1));
       const int64_t part = it.place == 2
@@ -513,6 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) o[i] *= factor;
         }
         if (!store) continue;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) add_zero_times(zero, o[i], o[i + 1]);
         if (it.place == 0) {
           const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
           T* dst = static_cast<T*>(a.out) + head * D + col;
@@ -533,7 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if (it.tree >= 0 && *odd) {
+      if (it.tree >= 0 && !(zero.x + zero.y == 0.f)) sh.odd = 1;
+      __syncwarp();
+      if (kCareful && it.tree >= 0) {
         // what of the item's V is not finite, to the rows that see it, whatever its weight
         if (!mask_there) {
           ok = cta_wait(&mask_full, it.tree & 1, gave_up);
@@ -574,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t* full = is_v ? v_full : k_full;
       uint64_t* freed = is_v ? v_free : k_free;
       uint8_t* missing = is_v ? v_gone : k_gone;
-      const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+      const CUtensorMap* map = is_v ? tm_v : tm_k;
       const uint32_t ring = is_v ? sV : sK;
       uint32_t kc = 0, q_uses[kTiles] = {0, 0};   // chunks, Q tiles of each place asked for so far
       // Block ids come for four chunks at a time (a lane each), asked for a group ahead,
@@ -626,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive_expect_tx(&q_full[i], C::kQBytes);
 #pragma unroll
               for (int h = 0; h < D / 64; ++h)
-                tma_load_box3(sQ + i * C::kQBytes + h * (kRows * 128), &tm_q, h * 64, it.kvh * G,
+                tma_load_box3(sQ + i * C::kQBytes + h * (kRows * 128), tm_q, h * 64, it.kvh * G,
                               it.q0 + (first >> g2), &q_full[i]);
             }
             __syncwarp();
@@ -903,35 +924,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               fence_async_smem();
               __syncwarp();
             }
-            // A node's V meets zero weights, too, of the rows that do not see it: what of it
-            // is not finite is taken out, and added at the item's end to the rows that do.
-            // (Where both tiles do it: told first, so that who finds it gone is told.)  The
-            // look at it runs beside the softmax; with four rows a turn its code drives the
-            // softmax's out of the instruction cache (a batch-256 mix 193 -> 222 us).
+            // A node's V meets zero weights, too, of the rows that do not see it: here what
+            // of it is not finite is taken out, and added at the item's end to the rows that
+            // do.  (Where both tiles see the chunk both do it, as above.)
             const int tree_row = max(0, it.ctx - it.n - (it.c0 + lc) * kKeys);   // the chunk's first
-            if (tree_row < valid) {
+            if (kCareful && tree_row < valid) {
               unsigned char* rows = smem + C::kOffV + (vc % SV) * C::kKvBytes;
-              // a lane's eighth of the row, then the same of every kRowsApart-th row
-              constexpr int kRowsApart = 32 / (D / 8);
-              const int r0 = tree_row + lane / (D / 8), ch = lane % (D / 8);
-              unsigned char* mine = rows + (ch >> 3) * (kKeys * 128) + ((ch & 7) << 4);
               __syncwarp();   // filled up above
-              uint32_t largest = 0;   // of the magnitudes, as integers
 #pragma unroll 1
-              for (int r = r0; r < valid; r += kRowsApart) {
-                const uint4 x = *reinterpret_cast<const uint4*>(mine + r * 128);
-                largest = __vmaxu2(largest, __vmaxu2(__vmaxu2(x.x & kMagnitudes, x.y & kMagnitudes),
-                                                     __vmaxu2(x.z & kMagnitudes, x.w & kMagnitudes)));
-              }
-              const bool found = odd_pair<T>(largest) != 0;
-              if (__any_sync(0xffffffffu, found)) {
-                if (found) *odd = 1;
-                __threadfence_block();
-#pragma unroll 1
-                for (int r = r0; found && r < valid; r += kRowsApart) {
-                  uint4* at = reinterpret_cast<uint4*>(mine + r * 128);
-                  *at = even8<T>(*at);
-                }
+              for (int i = lane; i < (valid - tree_row) * (D / 8); i += 32) {
+                const int r = tree_row + i / (D / 8), ch = i % (D / 8);
+                uint4* at = reinterpret_cast<uint4*>(rows + (ch >> 3) * (kKeys * 128) + r * 128 + ((ch & 7) << 4));
+                *at = finite8<T>(*at);
               }
               fence_async_smem();
               __syncwarp();
@@ -975,10 +979,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  if (!ok && lane == 0) raise_error(a.err, kErrTimeout);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
+  __shared__ __align__(16) Shared<D> sh;
+  const int tid = threadIdx.x, warp = (int)__shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (tid == 0) {
+    sh.gave_up = sh.odd = 0;
+    sh.barriers([](uint64_t* bar, int n) { mbar_init(bar, n); });
+    mbar_init_fence();
+  }
+  if (warp == 0) tmem_alloc(&sh.tmem_slot, 512);
+  if (tid == 32 * 8) {
+    prefetch_tensor_map(&tm_q);
+    prefetch_tensor_map(&tm_k);
+  }
+  if (tid == 32 * 9) prefetch_tensor_map(&tm_v);
+  pdl_wait_primary();
+  pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, 512);
+  tc_fence_after();
+
+  attend_items<T, D, false>(sh, a, &tm_q, &tm_k, &tm_v);
+  tc_fence_before();
+  __syncthreads();
+  if (sh.odd && !sh.gave_up) {
+    // Some row is not finite, which may have come from a node that it does not see: all
+    // of the CTA's items once more.  Everything that was in flight is done.
+    if (warp < 8)
+      fewer_registers<kLaunchRegs>();
+    else
+      more_registers<kLaunchRegs>();
+    if (tid == 0) {
+      sh.barriers([](uint64_t* bar, int) { mbar_inval(bar); });
+      sh.barriers([](uint64_t* bar, int n) { mbar_init(bar, n); });
+      mbar_init_fence();
+    }
+    __syncthreads();
+    tc_fence_after();
+    attend_items<T, D, true>(sh, a, &tm_q, &tm_k, &tm_v);
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (tid == 0 && sh.gave_up) raise_error(a.err, kErrTimeout);
+  if (warp == 0) tmem_dealloc(sh.tmem_slot, 512);
 }
 
 // The weighted sums of some partials of a row: l, and four elements of o, against the
