@@ -54,14 +54,14 @@
 // copy and its product, and its code drives the softmax's out of the instruction cache, with
 // four rows a turn in the mix 220.)
 //
-// Measured (event times of whole calls): 64 contexts of 128 .. 8192 tokens x 16 nodes,
-// 16 q / 8 kv heads x 128, fp16: 94 us = 5.6 TB/s, 83 % of the measured copy rate; a
-// batch-256 mix x 1 .. 32 nodes, 32 / 8 x 64, bf16: 192 us, 80 %; 4 short contexts 11.1
+// Measured (event times of calls in a row): 64 contexts of 128 .. 8192 tokens x 16 nodes,
+// 16 q / 8 kv heads x 128, fp16: 96 us = 5.5 TB/s, 81 % of the measured copy rate; a
+// batch-256 mix x 1 .. 32 nodes, 32 / 8 x 64, bf16: 189 us, 82 %; 4 short contexts 12.0
 // us.  In long contexts a chunk takes the time of its bytes: 1.51 us for 64 KB (d = 128,
 // up to 128 rows), 0.75 us for 32 KB (d = 64, up to 64 rows; 0.80 with 128): 6.5 TB/s over
 // all SMs.  With 256 rows at d = 64 it takes 1.38 us, the softmax's latency on two warps
-// a scheduler: 32 contexts x 64 nodes 56 us.  A call begins and ends in 6.7 us (launch,
-// lengths, table, first data), 7.5 with the join's launch, 11 where pairs are split; an
+// a scheduler: 32 contexts x 64 nodes 58 us.  A call begins and ends in 7.1 us (launch,
+// lengths, table, first data), 8.2 with the join's launch, 11 where pairs are split; an
 // item of its own costs 1.4 us (one tile's) to 2 or 3.  On the way there (64 contexts /
 // the mix / 4 short ones / 32 x 64): the first right version 101 / 230 / 18.6 / 64 us; block
 // ids a chunk ahead and not four 101 / 215 / 12.9 / 59; items of up to 4 chunks on both
@@ -120,10 +120,11 @@ constexpr int kMaskWords = kTreeNodes / 32, kMaskStride = kMaskWords + 1;
 constexpr int kOneTile = 4;
 // Where no context can have more than kWholePairs chunks, and whole pairs leave a CTA no
 // more than kWholeIdle2 / 2 of their time unused on average, pairs are not split, and no
-// second kernel joins them.  Whole and split: 4 contexts of 300 tokens x 16 nodes (16 q, 8
-// kv heads x 128) 9.5, 11.7 us; 16 of 1000 15.6, 22.0; 64 of 1000 (32 q, 8 kv heads x 64) 36.8,
-// 40.5; but 24 of 1000 (192 pairs, a second round for 40 of them) 28.1, 25.9, 1 of 1000 13.8,
-// 10.8, and 40 of 2000 72.8, 63.6.
+// second kernel joins them.  What contexts can have is the table's width, all that the host
+// knows: with a table of more than 64 blocks pairs are split, however short the contexts are.
+// Whole and split: 4 contexts of 300 tokens x 16 nodes (16 q, 8 kv heads x 128) 9.9, 11.9 us; 16
+// of 1000 15.8, 22.2; 64 of 1000 (32 q, 8 kv heads x 64) 39.0, 40.7; but 24 of 1000 (192 pairs, a
+// second round for 40 of them) 28.1, 25.9, 1 of 1000 13.8, 10.8, and 40 of 2000 72.8, 63.6.
 constexpr int kWholePairs = 8, kWholeIdle2 = 11;
 // Chunks whose missing blocks are remembered.  Softmax reads a chunk's entry when its S
 // is done, which is not when its stage is handed back: until the softmax has gone on, its

@@ -29,10 +29,10 @@
 // warp in whose run the sampled sum is passed goes through it once more (L2).  So
 // a step is one launch, and even one sequence has several SMs to read with.
 //
-// Measured: 4 chains of 5 over 32000 tokens 7.4 us (5.1 for one node and 1000 tokens: the
+// Measured: 4 chains of 5 over 32000 tokens 7.2 us (4.8 for one node and 1000 tokens: the
 // launch, three dependent loads, the sums' way over the cluster and the search); 64 x 1
-// node over 128256 tokens 13.1 us, 64 chains of 16 24; 32 x 1 .. 48 chosen nodes over 99991
-// 11.8 us; 64 x 16 drawn nodes over 128256 55 to 65 us, which is up to seven passes one
+// node over 128256 tokens 12.9 us, 64 chains of 16 24; 32 x 1 .. 48 chosen nodes over 99991
+// 12.3 us; 64 x 16 drawn nodes over 128256 56 to 70 us, as the draws fall, which is up to seven passes one
 // after another in the slowest sequence, 5 to 7 us each: all sequences' first ones share
 // the memory, the last one's are its cluster's latency.  The first version, A and B in
 // doubles for every thread and sums of single elements, took 12.8 us for the 4 chains,
