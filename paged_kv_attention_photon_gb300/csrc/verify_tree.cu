@@ -15,7 +15,8 @@
 // (p - L q)+ loses what p and L q have in common: where F is a millionth of L, the rest of
 // the tree is verified as the definition says it, in double: each element's r from p and
 // the row sums so far, a pass over the rows for each of them.  Children that the draft
-// drew get there once in a million times.
+// drew get there once in a million times.  (Never mind the time: 8 sequences with 255
+// rejections each over 128256 tokens 20 ms, 320 where hardly an element drops out.)
 //
 // What it answers are whole numbers, so what they hang on is held to about 48 bits:
 // L, F and the row sums are pairs of floats whose rounding errors are carried along
