@@ -495,8 +495,9 @@ size_t photon_paged_tree_attention_workspace_size(const photon_paged_shape_t* sh
  *   q, out        [num_tokens][num_q_heads][head_dim]
  *   context_lens  count the tree's nodes, whose K and V rows are in the cache
  * What is not finite in K and V of a key reaches the rows of nodes that see the key
- * and no others.  Rows of out that belong
- * to no sequence are left as they were.  dtype must be PHOTON_F16 or PHOTON_BF16.
+ * and no others; a call whose outputs are not all finite may take up to twice as long.
+ * Rows of out that belong to no sequence are left as they were.  dtype must be
+ * PHOTON_F16 or PHOTON_BF16.
  * A sequence with more nodes than max_query_len sets bit 32 and gets max_query_len
  * zero rows (none if its rows lie outside [0, num_tokens)); n > ctx or a context
  * outside [0, max_blocks_per_seq * block_size] sets bit 4 and gets zero rows; a block
